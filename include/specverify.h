@@ -428,6 +428,133 @@ int spec_tree_attention(const void* q, const void* k_cache,
                         void* stream);
 
 /*
+ * 4-bit KV cache.  A position of one key/value head holds D codes (e2m1, two
+ * per byte, the even head dim in the low half byte) and D / 16 block scales
+ * (e4m3, one per 16 consecutive head dims); the value a code c stands for is
+ *   unit * scale * c,   c in +-{0, 0.5, 1, 1.5, 2, 3, 4, 6},
+ * with k_unit and v_unit powers of two in [2^-64, 2^64] that the caller keeps
+ * with the cache (they place the scales' range, 2^-9 .. 448).  Every value is
+ * exact in bf16.  Arrays (device, row-major, contiguous):
+ *   codes [B, Hkv, S, D / 2] uint8, scales [B, Hkv, S, D / 16] uint8,
+ * one pair for the keys and one for the values: 4.5 bits per element.
+ * spec_kv_commit and spec_kv_evict move them like any other cache plane.
+ * D is 64 or 128 (else SPEC_ERR_UNSUPPORTED).
+ *
+ * spec_kv4_append: round new keys and values k, v [B, n, Hkv, D] bf16 into the
+ * positions prefix_len[b] + j, j < n (positions outside [0, S) are not
+ * written).  Per block: scale = max |x| / (6 unit) rounded to e4m3 (nearest,
+ * ties to even; at least 2^-9, at most 448), code = x / (scale unit) rounded
+ * to e2m1 (nearest, ties to even, at most 6).  A NaN makes its block's scale
+ * NaN (the block then reads as NaN); infinities saturate.
+ * spec_kv4_read: the values of positions start[b] + j as k, v [B, n, Hkv, D]
+ * bf16 (zeros for positions outside [0, S)).
+ * Errors: SPEC_ERR_SHAPE for B, n or S < 0, Hkv < 1 or sizes over the grid's
+ * limits; SPEC_ERR_ARG for a unit that is not a power of two in range, a NULL
+ * pointer (B, n > 0), k, v or codes not 16-byte aligned, scales not 8-byte or
+ * lengths not 4-byte aligned.  B == 0 or n == 0 does nothing.
+ */
+int spec_kv4_append(const void* k, const void* v, const int32_t* prefix_len,
+                    int B, int n, int Hkv, int D, int S, float k_unit,
+                    float v_unit, uint8_t* k_codes, uint8_t* k_scales,
+                    uint8_t* v_codes, uint8_t* v_scales, void* stream);
+int spec_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales,
+                  const uint8_t* v_codes, const uint8_t* v_scales,
+                  const int32_t* start, int B, int n, int Hkv, int D, int S,
+                  float k_unit, float v_unit, void* k, void* v, void* stream);
+
+/*
+ * spec_tree_attention over a 4-bit cache; N = 1 with mask bit 0 set is plain
+ * single-token decoding.  The same visible keys, layouts of q, out and
+ * mask_bits, and clamp of prefix_len; softmax and accumulation in float32, the
+ * cache's values exact, the output rounded to bf16.  D is 64 or 128.
+ * lse [B, N, Hq] float32 (out, may be NULL): each row's base-2 log normaliser
+ *     log2 sum_s 2^(log2(e) scale q . k_s) over its visible keys.
+ * A row that sees nothing (prefix 0 and no mask bit) gives zeros and lse =
+ * -inf.  What cache positions behind prefix_len + N hold does not matter; a
+ * NaN block of a drafted position reaches only the rows that see it.
+ * Workspace: spec_tree_attention_kv4_workspace_bytes(B, N, Hq, Hkv, D, S) bytes,
+ * 256-byte aligned, uninitialised (0 = invalid sizes).
+ * Errors: SPEC_ERR_SHAPE unless 1 <= N <= 64, Hq % Hkv == 0, S >= N and
+ * B <= 65535, or when B * Hkv * ceil(N Hq / Hkv / 16) reaches 2^31;
+ * SPEC_ERR_UNSUPPORTED unless D is 64 or 128; SPEC_ERR_ARG for scale <= 0 or
+ * not finite, a bad unit, a NULL pointer (B > 0), q, out or codes not 16-byte
+ * aligned, scales or mask_bits not 8-byte aligned, prefix_len or lse not
+ * 4-byte aligned; SPEC_ERR_WORKSPACE.  B == 0 does nothing.
+ */
+size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv,
+                                               int D, int S);
+int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
+                            const uint8_t* k_scales, const uint8_t* v_codes,
+                            const uint8_t* v_scales, const int32_t* prefix_len,
+                            const uint64_t* mask_bits, int B, int N, int Hq,
+                            int Hkv, int D, int S, float scale, float k_unit,
+                            float v_unit, void* out, float* lse,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Accumulated attention weight of cached positions (what eviction ranks them
+ * by).  After a verification step, per key/value head h and position s,
+ *
+ *   out[b,h,s] = weights[b,h,s] + sum_{t, g} p(t, g, s),
+ *   p(t, g, s) = 2^(log2(e) scale q[b, path_nodes[b,t], h G + g] . k[b,h,s]
+ *                    - lse[b, path_nodes[b,t], h G + g]),
+ *
+ * over the accepted nodes t < path_len[b] that see s, s <= P + t, and the G =
+ * Hq / Hkv query heads of head h; P = prefix_len[b] is the length before the
+ * commit and the accepted drafts' keys are already at P + t
+ * (spec_kv_commit has run).  Positions P .. P + path_len[b] - 1 are new: their
+ * entry of `weights` is not read.  Positions behind them are not written.
+ *
+ * q [B, N, Hq, D] bf16 and lse [B, N, Hq] float32 as the attention call took
+ * and returned them (a row with lse = -inf saw nothing and adds nothing).
+ * path_nodes [B, N] int32, or NULL: the first path_len[b] rows (a chain, or
+ * N = 1).  A path whose length is outside [0, N] or which names a node outside
+ * [0, N) adds nothing (path_len then counts as 0).  prefix_len is clamped to
+ * [0, S - N].
+ * k: the key cache, bf16 [B, Hkv, S, D] when k_scales is NULL (k_unit must be
+ * 1), else the codes of a 4-bit cache.  weights [B, Hkv, S] float32 (NULL =
+ * zeros), out [B, Hkv, S] float32; they may be the same array.
+ * Each position's sum has a fixed order (no atomics).
+ * Errors: as spec_tree_attention_kv4 (q and k 16-byte, k_scales 8-byte, the
+ * rest 4-byte aligned), Hkv <= 65535.
+ */
+int spec_kv_weights(const void* q, const void* k, const uint8_t* k_scales,
+                    const float* lse, const int32_t* prefix_len,
+                    const int32_t* path_len, const int32_t* path_nodes, int B,
+                    int N, int Hq, int Hkv, int D, int S, float scale,
+                    float k_unit, const float* weights, float* out,
+                    void* stream);
+
+/*
+ * Eviction: cut every (sequence, key/value head)'s cache to `budget`
+ * positions, keeping the `recent` last ones and, of the others, the budget -
+ * recent with the largest weights[b,h,s] (ties: the lowest position; NaN
+ * counts as -inf).  The kept positions stay in order and move to 0, 1, ...
+ * together with their weights.  A sequence no longer than the budget keeps
+ * everything.
+ * weights [B, Hkv, S] float32, length [B] int32 (clamped to [0, S]).
+ * planes: n_planes host pointers to device arrays [B, Hkv, S, row_bytes[i]]
+ *     (keys, values, codes, scales, ...); planes_out [B, Hkv, S_out,
+ *     row_bytes[i]] receive the kept rows.  planes_out[i] == planes[i] (with
+ *     S_out == S) moves in place; otherwise the two must not overlap.
+ * weights_out [B, Hkv, S_out] (may be NULL, or equal weights if S_out == S).
+ * kept [B, Hkv, budget] int32 (out): the kept positions, ascending, -1 padded.
+ * new_len [B] int32 (out) = min(length, budget).
+ * Rows behind the new length keep what they held.
+ * Errors: SPEC_ERR_SHAPE for negative sizes, Hkv < 1, budget outside
+ * [1, S_out], recent outside [0, budget], n_planes outside
+ * [0, SPEC_EVICT_MAX_PLANES], row_bytes outside [1, 65536]; SPEC_ERR_ARG for
+ * a NULL pointer (B > 0), a float or int array not 4-byte aligned, or an array
+ * given in place with S_out != S.  B == 0 does nothing.
+ */
+#define SPEC_EVICT_MAX_PLANES 8
+int spec_kv_evict(const float* weights, const int32_t* length, int B, int Hkv,
+                  int S, int budget, int recent, int n_planes,
+                  const void* const* planes, void* const* planes_out,
+                  const int* row_bytes, int S_out, float* weights_out,
+                  int32_t* kept, int32_t* new_len, void* stream);
+
+/*
  * The uniforms the kernels draw: out[i] = u(b[i], idx[i], slot[i]) for the
  * given seed and offset (all arrays device, length n).  Lets callers and
  * tests check the device generator bit for bit.

@@ -68,6 +68,7 @@ class SpecParams(ctypes.Structure):
 assert ctypes.sizeof(SpecParams) == 40
 
 SPEC_STATS_MAX_BINS = 1024
+SPEC_EVICT_MAX_PLANES = 8
 STATS_FIELDS = ("len_hist", "node_tested", "node_accepted", "depth_tested",
                 "depth_accepted", "calib_tested", "calib_accepted",
                 "calib_conf_sum", "invalid")
@@ -79,6 +80,7 @@ class SpecAcceptStats(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
 _SIGNATURES = {
@@ -113,6 +115,19 @@ _SIGNATURES = {
                                ctypes.POINTER(SpecAcceptStats), _P]),
     "spec_tree_attention": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                  ctypes.c_float, _P, _P]),
+    "spec_kv4_append": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P, _P,
+                             _P, _P, _P]),
+    "spec_kv4_read": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P,
+                           _P, _P]),
+    "spec_tree_attention_kv4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "spec_tree_attention_kv4": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I,
+                                     _I, _I, _I, _F, _F, _F, _P, _P, _P, _SZ,
+                                     _P]),
+    "spec_kv_weights": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                             _I, _F, _F, _P, _P, _P]),
+    "spec_kv_evict": (_I, [_P, _P, _I, _I, _I, _I, _I, _I,
+                           ctypes.POINTER(_P), ctypes.POINTER(_P),
+                           ctypes.POINTER(_I), _I, _P, _P, _P, _P]),
     "spec_profile_enable": (_I, [_I]),
     "spec_profile_read": (_I, [_I, ctypes.POINTER(ctypes.c_double),
                                ctypes.POINTER(ctypes.c_int)]),
@@ -162,7 +177,7 @@ def load(path: str = LIB_PATH):
 def call(name: str, *args) -> int:
     """Call an entry point; raise SpecError on a non-zero return code."""
     rc = getattr(load(), name)(*args)
-    if name not in ("spec_workspace_bytes", "spec_error_string") and rc != 0:
+    if not name.endswith(("workspace_bytes", "error_string")) and rc != 0:
         raise SpecError(name, rc)
     return rc
 

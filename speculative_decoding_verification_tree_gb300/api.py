@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -376,6 +377,220 @@ def spec_tree_attention(q, k_cache, v_cache, prefix_len, mask_bits, *,
                   _ptr(v_cache), _ptr(prefix_len), _ptr(mask_bits), B, N, Hq,
                   Hkv, D, S, float(scale), _ptr(out), _stream(stream))
     return out
+
+
+class KV4Cache(NamedTuple):
+    """A 4-bit cache: codes [B, Hkv, S, D/2] and scales [B, Hkv, S, D/16]
+    (uint8) of the keys and of the values."""
+    k: torch.Tensor
+    k_scale: torch.Tensor
+    v: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv4_cache(B, Hkv, S, D=128, device=None) -> KV4Cache:
+    """A zeroed 4-bit cache."""
+    dev = device or torch.cuda.current_device()
+    z = lambda w: torch.zeros(B, Hkv, S, w, dtype=torch.uint8, device=dev)
+    return KV4Cache(z(D // 2), z(D // 16), z(D // 2), z(D // 16))
+
+
+def _kv4(cache, B, Hkv, S, D):
+    """Shape check of the arrays of a 4-bit cache."""
+    for name, t in zip(KV4Cache._fields, cache, strict=True):
+        w = D // 16 if name.endswith("scale") else D // 2
+        _want(t, torch.uint8, (B, Hkv, S, w), name)
+
+
+def _alloc(dev, stream):
+    """Allocate under the call's stream, so that memory the wrapper frees on
+    return is reused in that stream's order."""
+    if stream is None or dev.type != "cuda":
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream)
+
+
+def spec_kv4_append(k, v, prefix_len, cache, *, k_unit=1.0, v_unit=1.0,
+                    stream=None):
+    """Round k, v [B, n, Hkv, D] bf16 into positions prefix_len[b] + j of a
+    4-bit cache (KV4Cache; see the C declaration for the format).  The units
+    are powers of two.  Returns the cache."""
+    B, n, Hkv, D = k.shape
+    S = cache[0].shape[2]
+    _want(k, torch.bfloat16, (B, n, Hkv, D), "k")
+    _want(v, torch.bfloat16, (B, n, Hkv, D), "v")
+    _want(prefix_len, torch.int32, (B,), "prefix_len")
+    _kv4(cache, B, Hkv, S, D)
+    dev = _device(k, v, prefix_len, *cache, stream=stream)
+    with _on(dev):
+        _lib.call("spec_kv4_append", _ptr(k), _ptr(v), _ptr(prefix_len), B, n,
+                  Hkv, D, S, float(k_unit), float(v_unit),
+                  *[_ptr(t) for t in cache], _stream(stream))
+    return cache
+
+
+def spec_kv4_read(cache, start, n, *, k_unit=1.0, v_unit=1.0, out=None,
+                  stream=None):
+    """The values of positions start[b] + j, j < n, of a 4-bit cache: (k, v)
+    [B, n, Hkv, D] bf16 (exact; zeros outside the cache)."""
+    B, Hkv, S, half = cache[0].shape
+    D = 2 * half
+    _kv4(cache, B, Hkv, S, D)
+    _want(start, torch.int32, (B,), "start")
+    dev = _device(start, *cache, *(out or ()), stream=stream)
+    if out is None:
+        with _alloc(dev, stream):
+            out = tuple(torch.empty(B, n, Hkv, D, dtype=torch.bfloat16,
+                                    device=dev) for _ in range(2))
+    _want(out[0], torch.bfloat16, (B, n, Hkv, D), "k")
+    _want(out[1], torch.bfloat16, (B, n, Hkv, D), "v")
+    with _on(dev):
+        _lib.call("spec_kv4_read", *[_ptr(t) for t in cache], _ptr(start), B,
+                  n, Hkv, D, S, float(k_unit), float(v_unit), _ptr(out[0]),
+                  _ptr(out[1]), _stream(stream))
+    return tuple(out)
+
+
+def spec_tree_attention_kv4(q, cache, prefix_len, mask_bits, *, scale=None,
+                            k_unit=1.0, v_unit=1.0, lse=False, out=None,
+                            ws=None, stream=None):
+    """spec_tree_attention over a 4-bit cache (KV4Cache): q [B, N, Hq, D]
+    bf16, D 64 or 128; N = 1 is single-token decoding.  lse: True, or a
+    [B, N, Hq] float32 tensor, for the rows' base-2 log normalisers.  Returns
+    (out [B, N, Hq, D] bf16, lse or None)."""
+    B, N, Hq, D = q.shape
+    _, Hkv, S, _ = cache[0].shape
+    _want(q, torch.bfloat16, (B, N, Hq, D), "q")
+    _kv4(cache, B, Hkv, S, D)
+    _want(prefix_len, torch.int32, (B,), "prefix_len")
+    _want(mask_bits, torch.int64, (B, N), "mask_bits")
+    dev = _device(q, *cache, prefix_len, mask_bits, out, ws,
+                  lse if torch.is_tensor(lse) else None, stream=stream)
+    with _on(dev), _alloc(dev, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if lse is True:
+            lse = torch.empty(B, N, Hq, dtype=torch.float32, device=dev)
+        elif lse is False:
+            lse = None
+        if ws is None:
+            nbytes = int(_lib.call("spec_tree_attention_kv4_workspace_bytes",
+                                   B, N, Hq, Hkv, D, S))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _want(out, torch.bfloat16, (B, N, Hq, D), "out")
+    if lse is not None:
+        _want(lse, torch.float32, (B, N, Hq), "lse")
+    if scale is None:
+        scale = D ** -0.5
+    with _on(dev):
+        _lib.call("spec_tree_attention_kv4", _ptr(q), *[_ptr(t) for t in cache],
+                  _ptr(prefix_len), _ptr(mask_bits), B, N, Hq, Hkv, D, S,
+                  float(scale), float(k_unit), float(v_unit), _ptr(out),
+                  _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
+    return out, lse
+
+
+def spec_kv_weights(q, k_cache, lse, prefix_len, path_len, path_nodes=None, *,
+                    scale=None, k_unit=1.0, weights=None, out=None,
+                    stream=None):
+    """Add the accepted rows' attention weights to the positions' accumulated
+    ones (see the C declaration; call it after spec_kv_commit).  q
+    [B, N, Hq, D] bf16 and lse [B, N, Hq] float32 of the attention call;
+    k_cache: a bf16 key cache [B, Hkv, S, D], or the (codes, scales) of a
+    4-bit one; path_len [B], path_nodes [B, N] int32 or None (chain).
+    weights [B, Hkv, S] float32 or None (zeros).  Returns out [B, Hkv, S]
+    (which may be `weights`)."""
+    B, N, Hq, D = q.shape
+    k, ks = (k_cache, None) if torch.is_tensor(k_cache) else k_cache[:2]
+    _, Hkv, S, _ = k.shape
+    _want(q, torch.bfloat16, (B, N, Hq, D), "q")
+    if ks is None:
+        _want(k, torch.bfloat16, (B, Hkv, S, D), "k_cache")
+    else:
+        _want(k, torch.uint8, (B, Hkv, S, D // 2), "k_cache codes")
+        _want(ks, torch.uint8, (B, Hkv, S, D // 16), "k_cache scales")
+    _want(lse, torch.float32, (B, N, Hq), "lse")
+    _want(prefix_len, torch.int32, (B,), "prefix_len")
+    _want(path_len, torch.int32, (B,), "path_len")
+    if path_nodes is not None:
+        _want(path_nodes, torch.int32, (B, N), "path_nodes")
+    if weights is not None:
+        _want(weights, torch.float32, (B, Hkv, S), "weights")
+    dev = _device(q, k, ks, lse, prefix_len, path_len, path_nodes, weights,
+                  out, stream=stream)
+    if out is None:
+        # zeros: positions behind the sequences are not written
+        with _on(dev), _alloc(dev, stream):
+            out = torch.zeros(B, Hkv, S, dtype=torch.float32, device=dev)
+    _want(out, torch.float32, (B, Hkv, S), "out")
+    if scale is None:
+        scale = D ** -0.5
+    with _on(dev):
+        _lib.call("spec_kv_weights", _ptr(q), _ptr(k), _ptr(ks), _ptr(lse),
+                  _ptr(prefix_len), _ptr(path_len), _ptr(path_nodes), B, N, Hq,
+                  Hkv, D, S, float(scale), float(k_unit), _ptr(weights),
+                  _ptr(out), _stream(stream))
+    return out
+
+
+def spec_kv_evict(weights, length, planes, *, budget, recent, planes_out=None,
+                  weights_out=None, kept=None, new_len=None, stream=None):
+    """Keep, per (sequence, key/value head), the `recent` last positions and
+    the budget - recent heaviest others (see the C declaration).  weights
+    [B, Hkv, S] float32, length [B] int32, planes: the cache's arrays
+    [B, Hkv, S, ...] (any dtype).  planes_out None: the rows and the weights
+    move in place; else arrays [B, Hkv, S_out, ...] receive them, and
+    weights_out (if given) the weights.  Returns (kept [B, Hkv, budget] int32,
+    -1 padded, new_len [B] int32)."""
+    B, Hkv, S = weights.shape
+    _want(weights, torch.float32, (B, Hkv, S), "weights")
+    _want(length, torch.int32, (B,), "length")
+    planes = tuple(planes)
+    if planes_out is None:
+        if weights_out is not None and weights_out is not weights:
+            raise ValueError("in place (planes_out None) the weights move in "
+                             "place too")
+        planes_out, weights_out = planes, weights
+    planes_out = tuple(planes_out)
+    if len(planes_out) != len(planes):
+        raise ValueError("planes and planes_out must pair up")
+    S_out = planes_out[0].shape[2] if planes_out else (
+        S if weights_out is None else weights_out.shape[2])
+    n = len(planes)
+    if n > _lib.SPEC_EVICT_MAX_PLANES:
+        raise ValueError(f"at most {_lib.SPEC_EVICT_MAX_PLANES} planes")
+    for i, (a, o) in enumerate(zip(planes, planes_out)):
+        _want(a, a.dtype, (B, Hkv, S) + tuple(a.shape[3:]), f"planes[{i}]")
+        _want(o, a.dtype, (B, Hkv, S_out) + tuple(a.shape[3:]),
+              f"planes_out[{i}]")
+    if weights_out is not None:
+        _want(weights_out, torch.float32, (B, Hkv, S_out), "weights_out")
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    dev = _device(weights, length, *planes, *planes_out, weights_out, kept,
+                  new_len, stream=stream)
+    with _on(dev), _alloc(dev, stream):
+        if kept is None:
+            kept = torch.empty(B, Hkv, budget, dtype=torch.int32, device=dev)
+        if new_len is None:
+            new_len = torch.empty(B, dtype=torch.int32, device=dev)
+    _want(kept, torch.int32, (B, Hkv, budget), "kept")
+    _want(new_len, torch.int32, (B,), "new_len")
+    rows = []
+    for a in planes:
+        r = a.element_size()
+        for d in a.shape[3:]:
+            r *= d
+        rows.append(r)
+    src = (ctypes.c_void_p * max(n, 1))(*[_ptr(t).value for t in planes])
+    dst = (ctypes.c_void_p * max(n, 1))(*[_ptr(t).value for t in planes_out])
+    rb = (ctypes.c_int * max(n, 1))(*rows)
+    with _on(dev):
+        _lib.call("spec_kv_evict", _ptr(weights), _ptr(length), B, Hkv, S,
+                  int(budget), int(recent), n, src, dst, rb, S_out,
+                  _ptr(weights_out), _ptr(kept), _ptr(new_len),
+                  _stream(stream))
+    return kept, new_len
 
 
 def spec_get_status(ws, stream=None) -> int:

@@ -172,4 +172,7 @@ cudaError_t launch_eagle2(const void* draft, int B, int V, int dtype, int depth,
                           float* draft_lse, Eagle2Cand* cand, uint32_t* status,
                           cudaStream_t st);
 
+// A 4-bit cache's unit: a power of two in [2^-64, 2^64].
+bool kv4_unit_ok(float u);
+
 }  // namespace sv

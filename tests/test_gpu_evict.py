@@ -1,0 +1,329 @@
+"""Accumulated attention weights and eviction on the GPU vs the oracle.
+
+Weights: a probability is 2^(x), x = f s - lse in float32.  With mag =
+log2(e) scale sum_d |q_d k_d| the score errs by at most 2^-17 mag (see
+test_gpu_kv4.py; bf16 caches multiply bf16 operands, also exact), the FMA by
+2^-24 (|f s| + |lse|) <= 2^-23 (mag + |lse|), the exponential by 2^-22
+relative; the sum over rows adds 2^-24 per term.  Eviction is exact.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import evict, kv4
+from oracle.kv import kv_commit
+from oracle.tree import tree_mask
+from tests._parity import lib_ready, np64
+from tests.test_gpu_kv4 import (_gen, _i32, _words, api, check_attention,
+                                make_cache, random_parent)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    lib_ready()
+
+
+def _weight_bound(q, k, lse, prefix, lens, nodes, scale, ref, G):
+    """Tolerance of the accumulated weights (rows as the oracle took them)."""
+    tol = np.abs(ref) * 2.0 ** -23
+    B, Hkv = ref.shape[:2]
+    for b in range(B):
+        P = int(prefix[b])
+        n = lens[b] - P
+        for t in range(n):
+            i = t if nodes is None else int(nodes[b][t])
+            for g in range(Hkv * G):
+                if not np.isfinite(lse[b, i, g]):
+                    continue
+                h, L = g // G, P + t + 1
+                s = scale * np.log2(np.e) * (k[b, h, :L] @ q[b, i, g])
+                mag = scale * np.log2(np.e) * (np.abs(k[b, h, :L])
+                                               @ np.abs(q[b, i, g]))
+                w = 2.0 ** (s - lse[b, i, g])
+                e = (2.0 ** -17 * mag + 2.0 ** -23 * (mag + abs(lse[b, i, g]))
+                     + 2.0 ** -22)
+                tol[b, h, :L] += w * (e + n * G * 2.0 ** -24)
+    return tol
+
+
+def _paths(rng, parent):
+    B, N = parent.shape
+    nodes = np.full((B, N), -1, dtype=np.int32)
+    lens = np.zeros(B, dtype=np.int32)
+    for b in range(B):
+        cur = -1
+        while True:
+            kids = np.flatnonzero(parent[b] == cur)
+            if kids.size == 0 or (lens[b] and rng.random() < 0.2):
+                break
+            cur = int(rng.choice(kids))
+            nodes[b, lens[b]] = cur
+            lens[b] += 1
+    return nodes, lens
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("kind", ["kv4", "bf16"])
+@pytest.mark.parametrize("N,Hq,Hkv,prefix", [
+    (1, 4, 4, [0, 31, 1025]),
+    (1, 16, 2, [1023, 5, 96]),
+    (9, 8, 2, [100, 0, 2047]),
+    (40, 12, 1, [64, 700, 3]),      # 12 heads on one: more rows than a stage
+])
+def test_weights_match_oracle(kind, N, Hq, Hkv, prefix, D):
+    rng = np.random.default_rng(N * 10 + Hq + D)
+    B, G = len(prefix), Hq // Hkv
+    S = max(prefix) + N + 5
+    parent = random_parent(rng, B, N)
+    if N == 40:  # a chain: all 40 nodes accepted in one sequence
+        parent[1] = np.arange(-1, N - 1)
+    nodes, lens = _paths(rng, parent)
+    if N == 40:
+        nodes[1], lens[1] = np.arange(N), N
+    q = torch.randn(B, N, Hq, D, generator=_gen(N), device="cuda").bfloat16()
+    used = [p + int(n) for p, n in zip(prefix, lens)]
+    if kind == "kv4":
+        cache, (k, _) = make_cache(N, B, Hkv, S, D, used=used)
+        kc = cache[:2]
+    else:
+        kc = torch.randn(B, Hkv, S, D, generator=_gen(D), device="cuda").bfloat16()
+        k = np64(kc)
+        for b in range(B):
+            kc[b, :, used[b]:] = float("nan")
+    # normalisers of the rows over what they see after the commit
+    scale = 0.2
+    lse = np.full((B, N, Hq), -np.inf)
+    for b in range(B):
+        for t in range(lens[b]):
+            for h in range(Hq):
+                s = scale * (k[b, h // G, :prefix[b] + t + 1]
+                             @ np64(q)[b, nodes[b, t], h])
+                lse[b, nodes[b, t], h] = np.log2(np.exp(s - s.max()).sum()
+                                                 ) + s.max() * np.log2(np.e)
+    lse32 = torch.from_numpy(lse).float()
+    w0 = torch.rand(B, Hkv, S, generator=_gen(4), device="cuda")
+    got = torch.full_like(w0, -7.0)
+    args = (q, kc, lse32.cuda(), _i32(prefix), _i32(lens), _i32(nodes))
+    api().spec_kv_weights(*args, scale=scale, weights=w0, out=got)
+    torch.cuda.synchronize()
+    ref, L = evict.add_weights(np64(w0), np64(q), k, lse32.double().numpy(),
+                               prefix, lens, nodes, scale)
+    tol = _weight_bound(np64(q), k, lse32.double().numpy(), prefix, L, nodes,
+                        scale, np.nan_to_num(ref), G)
+    g = got.double().cpu().numpy()
+    for b in range(B):
+        assert (g[b, :, L[b]:] == -7.0).all()   # behind the sequence
+        assert (np.abs(g[b, :, :L[b]] - ref[b, :, :L[b]])
+                <= tol[b, :, :L[b]]).all()
+    # in place, and without a previous record
+    w1 = w0.clone()
+    api().spec_kv_weights(*args, scale=scale, weights=w1, out=w1)
+    zero = api().spec_kv_weights(*args, scale=scale)
+    torch.cuda.synchronize()
+    for b in range(B):
+        assert torch.equal(w1[b, :, :L[b]], got[b, :, :L[b]])
+        assert torch.equal(w1[b, :, L[b]:], w0[b, :, L[b]:])
+        assert (zero[b, :, L[b]:] == 0).all()
+        new = slice(prefix[b], L[b])
+        assert torch.equal(zero[b, :, new], got[b, :, new])
+
+
+def test_weights_invalid_paths_and_empty_rows():
+    B, N, Hq, Hkv, D, S = 5, 4, 2, 1, 64, 50
+    cache, _ = make_cache(1, B, Hkv, S, D)
+    q = torch.randn(B, N, Hq, D, generator=_gen(1), device="cuda").bfloat16()
+    lse = torch.zeros(B, N, Hq, device="cuda")
+    lse[4] = float("-inf")
+    w0 = torch.rand(B, Hkv, S, device="cuda")
+    nodes = _i32([[0, 1, -1, -1], [0, 4, -1, -1], [0, 1, 2, 3], [0] * 4,
+                  [0, 1, 2, 3]])
+    out = api().spec_kv_weights(q, cache[:2], lse, _i32([10, 10, 10, 10, 10]),
+                                _i32([-1, 2, 5, 0, 2]), nodes, weights=w0,
+                                out=w0.clone())
+    torch.cuda.synchronize()
+    assert torch.equal(out[:4], w0[:4])
+    assert torch.equal(out[4, :, :10], w0[4, :, :10])
+    assert (out[4, :, 10:12] == 0).all()
+    assert torch.equal(out[4, :, 12:], w0[4, :, 12:])
+
+
+# ------------------------------------------------------------------ evict
+def _weights(rng, B, Hkv, S, kind):
+    if kind == "ties":
+        w = rng.integers(0, 4, size=(B, Hkv, S)).astype(np.float32)
+    elif kind == "special":
+        w = rng.normal(size=(B, Hkv, S)).astype(np.float32)
+        pick = rng.random((B, Hkv, S))
+        w[pick < 0.2] = np.nan
+        w[(pick >= 0.2) & (pick < 0.3)] = -np.inf
+        w[(pick >= 0.3) & (pick < 0.4)] = np.inf
+        w[(pick >= 0.4) & (pick < 0.5)] = 0.0
+        w[(pick >= 0.5) & (pick < 0.6)] = -0.0
+        w[(pick >= 0.6) & (pick < 0.7)] = 1e-42
+    else:
+        w = np.exp(2 * rng.normal(size=(B, Hkv, S))).astype(np.float32)
+    return w
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("kind", ["plain", "ties", "special"])
+@pytest.mark.parametrize("B,Hkv,S,length,budget,recent", [
+    (1, 1, 1, [1], 1, 0),
+    (2, 3, 40, [40, 17], 16, 16),
+    (4, 2, 300, [300, 0, 16, 299], 16, 3),
+    (3, 2, 1111, [1111, 700, 513], 512, 0),
+    (1, 2, 9000, [8999], 7001, 640),
+    (2, 1, 70001, [70001, 40000], 3001, 100),
+])
+def test_evict_matches_oracle(B, Hkv, S, length, budget, recent, kind, in_place):
+    rng = np.random.default_rng(S + budget)
+    w = _weights(rng, B, Hkv, S, kind)
+    if kind == "special":  # an index row decides among every NaN and -inf
+        w[0, 0, :] = np.where(rng.random(S) < 0.5, np.nan, -np.inf)
+    planes = [torch.randint(0, 256, (B, Hkv, S, r), dtype=torch.uint8,
+                            device="cuda") for r in (64, 8, 5)]
+    planes.append(torch.randn(B, Hkv, S, 3, 8, device="cuda").bfloat16())
+    before = [p.cpu() for p in planes]
+    wt = torch.from_numpy(w).cuda()
+    a = api()
+    if in_place:
+        outs, wo, S_out = planes, wt, S
+        kept, new_len = a.spec_kv_evict(wt, _i32(length), planes,
+                                        budget=budget, recent=recent)
+    else:
+        S_out = budget + 3
+        outs = [torch.zeros(B, Hkv, S_out, *p.shape[3:], dtype=p.dtype,
+                            device="cuda") for p in planes]
+        wo = torch.zeros(B, Hkv, S_out, device="cuda")
+        kept, new_len = a.spec_kv_evict(wt, _i32(length), planes,
+                                        budget=budget, recent=recent,
+                                        planes_out=outs, weights_out=wo)
+    torch.cuda.synchronize()
+    assert new_len.tolist() == [min(n, budget) for n in length]
+    kept = kept.cpu().numpy()
+    for b in range(B):
+        for h in range(Hkv):
+            want = evict.kept_positions(w[b, h], length[b], budget, recent)
+            n = len(want)
+            assert kept[b, h, :n].tolist() == want
+            assert (kept[b, h, n:] == -1).all()
+            for p, o in zip(before, outs):
+                assert torch.equal(o[b, h, :n].cpu(), p[b, h, want])
+                tail = p[b, h, n:] if in_place else torch.zeros_like(
+                    o[b, h, n:]).cpu()
+                assert torch.equal(o[b, h, n:].cpu(), tail)
+            assert np.array_equal(wo[b, h, :n].cpu().numpy(), w[b, h, want],
+                                  equal_nan=True)
+
+
+def test_evict_without_planes_and_empty_batch():
+    a = api()
+    w = torch.tensor([[[3.0, 1.0, 2.0, 0.0]]], device="cuda")
+    kept, n = a.spec_kv_evict(w, _i32([4]), (), budget=2, recent=1)
+    assert kept.tolist() == [[[0, 3]]] and n.tolist() == [2]
+    assert w[0, 0, :2].tolist() == [3.0, 0.0]
+    z = torch.empty(0, 2, 8, device="cuda")
+    kept, n = a.spec_kv_evict(z, torch.empty(0, dtype=torch.int32,
+                                             device="cuda"), (),
+                              budget=2, recent=1)
+    assert kept.shape == (0, 2, 2) and n.numel() == 0
+
+
+# -------------------------------------------------- the operators together
+def test_a_verification_step_on_an_evicted_4_bit_cache():
+    """append -> attention -> commit -> weights -> evict -> attention, each
+    checked against the oracle run on what the step before returned."""
+    rng = np.random.default_rng(8)
+    B, N, Hq, Hkv, D, S = 3, 12, 8, 2, 128, 400
+    G, scale = Hq // Hkv, 128 ** -0.5
+    a = api()
+    g = _gen(8)
+    pre = [300, 12, 257]
+    cache = a.kv4_cache(B, Hkv, S, D)
+    mk = lambda n: [torch.randn(B, n, Hkv, D, generator=g, device="cuda"
+                                ).bfloat16() for _ in range(2)]
+    a.spec_kv4_append(*mk(300), _i32([0] * B), cache)
+    weights = torch.rand(B, Hkv, S, generator=g, device="cuda")
+    for step in range(2):
+        parent = random_parent(rng, B, N)
+        _, words = tree_mask(parent)
+        nodes, lens = _paths(rng, parent)
+        q = torch.randn(B, N, Hq, D, generator=g, device="cuda").bfloat16()
+        tpre = _i32(pre)
+        a.spec_kv4_append(*mk(N), tpre, cache)
+        out, lse = a.spec_tree_attention_kv4(q, cache, tpre, _words(words),
+                                             lse=True)
+        torch.cuda.synchronize()
+        host = [t.cpu().numpy() for t in cache]
+        vals = (kv4.values(host[0], host[1]), kv4.values(host[2], host[3]))
+        check_attention(out, lse, q, vals, pre, words, scale)
+        for t in cache:  # the accepted path's rows, plane by plane
+            row = t.shape[-1]
+            new_len = a.spec_kv_commit(
+                t, tpre, _i32(lens), _i32(nodes), row_bytes=row, N=N,
+                layout=(1, Hkv, Hkv * S * row, 0, S * row, row))
+        torch.cuda.synchronize()
+        host = [kv_commit(x.transpose(0, 2, 1, 3), pre, lens, nodes)[0]
+                .transpose(0, 2, 1, 3) for x in host]
+        for t, x in zip(cache, host):
+            assert np.array_equal(t.cpu().numpy(), x)
+        k = kv4.values(host[0], host[1])
+        w0 = np64(weights)
+        a.spec_kv_weights(q, cache, lse, tpre, _i32(lens), _i32(nodes),
+                          weights=weights, out=weights)
+        torch.cuda.synchronize()
+        l64 = lse.double().cpu().numpy()
+        ref, L = evict.add_weights(w0, np64(q), k, l64, pre, lens, nodes, scale)
+        tol = _weight_bound(np64(q), k, l64, pre, L, nodes, scale,
+                            np.nan_to_num(ref), G)
+        got = np64(weights)
+        assert L.tolist() == new_len.tolist()
+        for b in range(B):
+            assert (np.abs(got[b, :, :L[b]] - ref[b, :, :L[b]])
+                    <= tol[b, :, :L[b]]).all()
+        w32 = weights.cpu().numpy()
+        kept, nl = a.spec_kv_evict(weights, new_len, cache, budget=100,
+                                   recent=30)
+        torch.cuda.synchronize()
+        pre = nl.tolist()
+        for b in range(B):
+            for h in range(Hkv):
+                want = evict.kept_positions(w32[b, h], int(L[b]), 100, 30)
+                assert kept[b, h, :len(want)].tolist() == want
+                for t, x in zip(cache, host):
+                    assert np.array_equal(t[b, h, :len(want)].cpu().numpy(),
+                                          x[b, h, want])
+
+
+def test_eviction_replays_in_a_graph():
+    B, Hkv, S, D = 2, 2, 600, 64
+    cache, _ = make_cache(5, B, Hkv, S, D)
+    a = api()
+    w = torch.rand(B, Hkv, S, generator=_gen(6), device="cuda")
+    n = _i32([600, 580])
+    out = a.kv4_cache(B, Hkv, 128, D)
+    wo = torch.zeros(B, Hkv, 128, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    call = lambda: a.spec_kv_evict(w, n, cache, budget=128, recent=16,
+                                   planes_out=out, weights_out=wo)
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept, new_len = call()
+    w.copy_(w.flip(-1))
+    n.copy_(_i32([99, 600]))
+    graph.replay()
+    torch.cuda.synchronize()
+    moved = [t.clone() for t in out]
+    wh = w.cpu().numpy()
+    for b, h in ((0, 0), (0, 1), (1, 0), (1, 1)):
+        want = evict.kept_positions(wh[b, h], int(n[b]), 128, 16)
+        assert kept[b, h, :len(want)].tolist() == want
+        for t, o in zip(cache, moved):
+            assert torch.equal(o[b, h, :len(want)], t[b, h, want])
