@@ -176,8 +176,8 @@ def load(path: str = LIB_PATH):
 
 def call(name: str, *args) -> int:
     """Call an entry point; raise SpecError on a non-zero return code."""
-    rc = getattr(load(), name)(*args)
-    if not name.endswith(("workspace_bytes", "error_string")) and rc != 0:
+    rc = getattr(_lib or load(), name)(*args)
+    if rc != 0 and not name.endswith(("workspace_bytes", "error_string")):
         raise SpecError(name, rc)
     return rc
 

@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
+import math
 from typing import NamedTuple
 
 import torch
@@ -395,19 +397,60 @@ def kv4_cache(B, Hkv, S, D=128, device=None) -> KV4Cache:
     return KV4Cache(z(D // 2), z(D // 16), z(D // 2), z(D // 16))
 
 
-def _kv4(cache, B, Hkv, S, D):
-    """Shape check of the arrays of a 4-bit cache."""
-    for name, t in zip(KV4Cache._fields, cache, strict=True):
-        w = D // 16 if name.endswith("scale") else D // 2
-        _want(t, torch.uint8, (B, Hkv, S, w), name)
+# The wrappers below run once per layer and decoding step, on kernels of a few
+# microseconds: each argument is checked and turned into an address in one
+# step, and the device is only switched when it has to be.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _alloc(dev, stream):
+def _addr(t):
+    if not t.is_cuda:
+        raise ValueError("device tensors are required")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _arg(t, dtype, shape, dev, name):
+    """Address of an argument, after the checks of _want, _device and _ptr."""
+    if t.dtype is not dtype or t.shape != shape:
+        _want(t, dtype, shape, name)
+    if t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}; got one on "
+                         f"{t.device}")
+    return _addr(t)
+
+
+def _kv4_args(cache, B, Hkv, S, D, dev):
+    """Addresses of the arrays of a 4-bit cache."""
+    k, ks, v, vs = cache
+    codes, scales = (B, Hkv, S, D // 2), (B, Hkv, S, D // 16)
+    u8 = torch.uint8
+    return (_arg(k, u8, codes, dev, "k codes"),
+            _arg(ks, u8, scales, dev, "k scales"),
+            _arg(v, u8, codes, dev, "v codes"),
+            _arg(vs, u8, scales, dev, "v scales"))
+
+
+def _alloc(shape, dtype, dev, stream, make=torch.empty):
     """Allocate under the call's stream, so that memory the wrapper frees on
     return is reused in that stream's order."""
-    if stream is None or dev.type != "cuda":
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream)
+    if stream is None:
+        return make(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=dev)
+
+
+def _enqueue(name, dev, stream, *args):
+    """Call an entry point (without its last argument, the stream) on `dev`."""
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _lib.call(name, *args, stream.cuda_stream if stream
+                             is not None else _raw_stream(dev.index))
+    return _lib.call(name, *args, stream.cuda_stream if stream is not None
+                     else _raw_stream(dev.index))
 
 
 def spec_kv4_append(k, v, prefix_len, cache, *, k_unit=1.0, v_unit=1.0,
@@ -415,17 +458,14 @@ def spec_kv4_append(k, v, prefix_len, cache, *, k_unit=1.0, v_unit=1.0,
     """Round k, v [B, n, Hkv, D] bf16 into positions prefix_len[b] + j of a
     4-bit cache (KV4Cache; see the C declaration for the format).  The units
     are powers of two.  Returns the cache."""
-    B, n, Hkv, D = k.shape
+    B, n, Hkv, D = shape = k.shape
     S = cache[0].shape[2]
-    _want(k, torch.bfloat16, (B, n, Hkv, D), "k")
-    _want(v, torch.bfloat16, (B, n, Hkv, D), "v")
-    _want(prefix_len, torch.int32, (B,), "prefix_len")
-    _kv4(cache, B, Hkv, S, D)
-    dev = _device(k, v, prefix_len, *cache, stream=stream)
-    with _on(dev):
-        _lib.call("spec_kv4_append", _ptr(k), _ptr(v), _ptr(prefix_len), B, n,
-                  Hkv, D, S, float(k_unit), float(v_unit),
-                  *[_ptr(t) for t in cache], _stream(stream))
+    dev = k.device
+    _enqueue("spec_kv4_append", dev, stream,
+             _arg(k, torch.bfloat16, shape, dev, "k"),
+             _arg(v, torch.bfloat16, shape, dev, "v"),
+             _arg(prefix_len, torch.int32, (B,), dev, "prefix_len"), B, n, Hkv,
+             D, S, k_unit, v_unit, *_kv4_args(cache, B, Hkv, S, D, dev))
     return cache
 
 
@@ -435,20 +475,23 @@ def spec_kv4_read(cache, start, n, *, k_unit=1.0, v_unit=1.0, out=None,
     [B, n, Hkv, D] bf16 (exact; zeros outside the cache)."""
     B, Hkv, S, half = cache[0].shape
     D = 2 * half
-    _kv4(cache, B, Hkv, S, D)
-    _want(start, torch.int32, (B,), "start")
-    dev = _device(start, *cache, *(out or ()), stream=stream)
-    if out is None:
-        with _alloc(dev, stream):
-            out = tuple(torch.empty(B, n, Hkv, D, dtype=torch.bfloat16,
-                                    device=dev) for _ in range(2))
-    _want(out[0], torch.bfloat16, (B, n, Hkv, D), "k")
-    _want(out[1], torch.bfloat16, (B, n, Hkv, D), "v")
-    with _on(dev):
-        _lib.call("spec_kv4_read", *[_ptr(t) for t in cache], _ptr(start), B,
-                  n, Hkv, D, S, float(k_unit), float(v_unit), _ptr(out[0]),
-                  _ptr(out[1]), _stream(stream))
-    return tuple(out)
+    dev = start.device
+    args = _kv4_args(cache, B, Hkv, S, D, dev)
+    shape = (B, n, Hkv, D)
+    k, v = out if out is not None else (
+        _alloc(shape, torch.bfloat16, dev, stream),
+        _alloc(shape, torch.bfloat16, dev, stream))
+    _enqueue("spec_kv4_read", dev, stream, *args,
+             _arg(start, torch.int32, (B,), dev, "start"), B, n, Hkv, D, S,
+             k_unit, v_unit, _arg(k, torch.bfloat16, shape, dev, "k"),
+             _arg(v, torch.bfloat16, shape, dev, "v"))
+    return k, v
+
+
+@functools.lru_cache(maxsize=256)
+def _kv4_workspace_bytes(B, N, Hq, Hkv, D, S):
+    return int(_lib.call("spec_tree_attention_kv4_workspace_bytes", B, N, Hq,
+                         Hkv, D, S))
 
 
 def spec_tree_attention_kv4(q, cache, prefix_len, mask_bits, *, scale=None,
@@ -458,35 +501,30 @@ def spec_tree_attention_kv4(q, cache, prefix_len, mask_bits, *, scale=None,
     bf16, D 64 or 128; N = 1 is single-token decoding.  lse: True, or a
     [B, N, Hq] float32 tensor, for the rows' base-2 log normalisers.  Returns
     (out [B, N, Hq, D] bf16, lse or None)."""
-    B, N, Hq, D = q.shape
+    B, N, Hq, D = shape = q.shape
     _, Hkv, S, _ = cache[0].shape
-    _want(q, torch.bfloat16, (B, N, Hq, D), "q")
-    _kv4(cache, B, Hkv, S, D)
-    _want(prefix_len, torch.int32, (B,), "prefix_len")
-    _want(mask_bits, torch.int64, (B, N), "mask_bits")
-    dev = _device(q, *cache, prefix_len, mask_bits, out, ws,
-                  lse if torch.is_tensor(lse) else None, stream=stream)
-    with _on(dev), _alloc(dev, stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        if lse is True:
-            lse = torch.empty(B, N, Hq, dtype=torch.float32, device=dev)
-        elif lse is False:
-            lse = None
-        if ws is None:
-            nbytes = int(_lib.call("spec_tree_attention_kv4_workspace_bytes",
-                                   B, N, Hq, Hkv, D, S))
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _want(out, torch.bfloat16, (B, N, Hq, D), "out")
-    if lse is not None:
-        _want(lse, torch.float32, (B, N, Hq), "lse")
+    dev = q.device
+    args = (_arg(q, torch.bfloat16, shape, dev, "q"),
+            *_kv4_args(cache, B, Hkv, S, D, dev),
+            _arg(prefix_len, torch.int32, (B,), dev, "prefix_len"),
+            _arg(mask_bits, torch.int64, (B, N), dev, "mask_bits"))
+    if out is None:
+        out = _alloc(shape, torch.bfloat16, dev, stream)
+    if lse is True:
+        lse = _alloc((B, N, Hq), torch.float32, dev, stream)
+    elif lse is False:
+        lse = None
+    if ws is None:
+        ws = _alloc(_kv4_workspace_bytes(B, N, Hq, Hkv, D, S), torch.uint8,
+                    dev, stream)
     if scale is None:
         scale = D ** -0.5
-    with _on(dev):
-        _lib.call("spec_tree_attention_kv4", _ptr(q), *[_ptr(t) for t in cache],
-                  _ptr(prefix_len), _ptr(mask_bits), B, N, Hq, Hkv, D, S,
-                  float(scale), float(k_unit), float(v_unit), _ptr(out),
-                  _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
+    _enqueue("spec_tree_attention_kv4", dev, stream, *args, B, N, Hq, Hkv, D,
+             S, scale, k_unit, v_unit,
+             _arg(out, torch.bfloat16, shape, dev, "out"),
+             None if lse is None else _arg(lse, torch.float32, (B, N, Hq), dev,
+                                           "lse"),
+             _arg(ws, torch.uint8, ws.shape, dev, "ws"), ws.numel())
     return out, lse
 
 
@@ -500,36 +538,33 @@ def spec_kv_weights(q, k_cache, lse, prefix_len, path_len, path_nodes=None, *,
     4-bit one; path_len [B], path_nodes [B, N] int32 or None (chain).
     weights [B, Hkv, S] float32 or None (zeros).  Returns out [B, Hkv, S]
     (which may be `weights`)."""
-    B, N, Hq, D = q.shape
-    k, ks = (k_cache, None) if torch.is_tensor(k_cache) else k_cache[:2]
-    _, Hkv, S, _ = k.shape
-    _want(q, torch.bfloat16, (B, N, Hq, D), "q")
-    if ks is None:
-        _want(k, torch.bfloat16, (B, Hkv, S, D), "k_cache")
+    B, N, Hq, D = shape = q.shape
+    dev = q.device
+    if torch.is_tensor(k_cache):
+        _, Hkv, S, _ = k_cache.shape
+        ka = _arg(k_cache, torch.bfloat16, (B, Hkv, S, D), dev, "k_cache")
+        sa = None
     else:
-        _want(k, torch.uint8, (B, Hkv, S, D // 2), "k_cache codes")
-        _want(ks, torch.uint8, (B, Hkv, S, D // 16), "k_cache scales")
-    _want(lse, torch.float32, (B, N, Hq), "lse")
-    _want(prefix_len, torch.int32, (B,), "prefix_len")
-    _want(path_len, torch.int32, (B,), "path_len")
-    if path_nodes is not None:
-        _want(path_nodes, torch.int32, (B, N), "path_nodes")
-    if weights is not None:
-        _want(weights, torch.float32, (B, Hkv, S), "weights")
-    dev = _device(q, k, ks, lse, prefix_len, path_len, path_nodes, weights,
-                  out, stream=stream)
+        k, ks = k_cache[:2]
+        _, Hkv, S, _ = k.shape
+        ka = _arg(k, torch.uint8, (B, Hkv, S, D // 2), dev, "k_cache codes")
+        sa = _arg(ks, torch.uint8, (B, Hkv, S, D // 16), dev, "k_cache scales")
+    args = (_arg(q, torch.bfloat16, shape, dev, "q"), ka, sa,
+            _arg(lse, torch.float32, (B, N, Hq), dev, "lse"),
+            _arg(prefix_len, torch.int32, (B,), dev, "prefix_len"),
+            _arg(path_len, torch.int32, (B,), dev, "path_len"),
+            None if path_nodes is None
+            else _arg(path_nodes, torch.int32, (B, N), dev, "path_nodes"))
+    per_pos = (B, Hkv, S)
+    wa = (None if weights is None
+          else _arg(weights, torch.float32, per_pos, dev, "weights"))
     if out is None:
         # zeros: positions behind the sequences are not written
-        with _on(dev), _alloc(dev, stream):
-            out = torch.zeros(B, Hkv, S, dtype=torch.float32, device=dev)
-    _want(out, torch.float32, (B, Hkv, S), "out")
+        out = _alloc(per_pos, torch.float32, dev, stream, torch.zeros)
     if scale is None:
         scale = D ** -0.5
-    with _on(dev):
-        _lib.call("spec_kv_weights", _ptr(q), _ptr(k), _ptr(ks), _ptr(lse),
-                  _ptr(prefix_len), _ptr(path_len), _ptr(path_nodes), B, N, Hq,
-                  Hkv, D, S, float(scale), float(k_unit), _ptr(weights),
-                  _ptr(out), _stream(stream))
+    _enqueue("spec_kv_weights", dev, stream, *args, B, N, Hq, Hkv, D, S, scale,
+             k_unit, wa, _arg(out, torch.float32, per_pos, dev, "out"))
     return out
 
 
@@ -542,54 +577,44 @@ def spec_kv_evict(weights, length, planes, *, budget, recent, planes_out=None,
     move in place; else arrays [B, Hkv, S_out, ...] receive them, and
     weights_out (if given) the weights.  Returns (kept [B, Hkv, budget] int32,
     -1 padded, new_len [B] int32)."""
-    B, Hkv, S = weights.shape
-    _want(weights, torch.float32, (B, Hkv, S), "weights")
-    _want(length, torch.int32, (B,), "length")
-    planes = tuple(planes)
+    B, Hkv, S = shape = weights.shape
+    dev = weights.device
     if planes_out is None:
         if weights_out is not None and weights_out is not weights:
             raise ValueError("in place (planes_out None) the weights move in "
                              "place too")
         planes_out, weights_out = planes, weights
-    planes_out = tuple(planes_out)
-    if len(planes_out) != len(planes):
-        raise ValueError("planes and planes_out must pair up")
-    S_out = planes_out[0].shape[2] if planes_out else (
-        S if weights_out is None else weights_out.shape[2])
     n = len(planes)
+    if len(planes_out) != n:
+        raise ValueError("planes and planes_out must pair up")
     if n > _lib.SPEC_EVICT_MAX_PLANES:
         raise ValueError(f"at most {_lib.SPEC_EVICT_MAX_PLANES} planes")
-    for i, (a, o) in enumerate(zip(planes, planes_out)):
-        _want(a, a.dtype, (B, Hkv, S) + tuple(a.shape[3:]), f"planes[{i}]")
-        _want(o, a.dtype, (B, Hkv, S_out) + tuple(a.shape[3:]),
-              f"planes_out[{i}]")
-    if weights_out is not None:
-        _want(weights_out, torch.float32, (B, Hkv, S_out), "weights_out")
     if budget < 1:
         raise ValueError("budget must be at least 1")
-    dev = _device(weights, length, *planes, *planes_out, weights_out, kept,
-                  new_len, stream=stream)
-    with _on(dev), _alloc(dev, stream):
-        if kept is None:
-            kept = torch.empty(B, Hkv, budget, dtype=torch.int32, device=dev)
-        if new_len is None:
-            new_len = torch.empty(B, dtype=torch.int32, device=dev)
-    _want(kept, torch.int32, (B, Hkv, budget), "kept")
-    _want(new_len, torch.int32, (B,), "new_len")
-    rows = []
-    for a in planes:
-        r = a.element_size()
-        for d in a.shape[3:]:
-            r *= d
-        rows.append(r)
-    src = (ctypes.c_void_p * max(n, 1))(*[_ptr(t).value for t in planes])
-    dst = (ctypes.c_void_p * max(n, 1))(*[_ptr(t).value for t in planes_out])
-    rb = (ctypes.c_int * max(n, 1))(*rows)
-    with _on(dev):
-        _lib.call("spec_kv_evict", _ptr(weights), _ptr(length), B, Hkv, S,
-                  int(budget), int(recent), n, src, dst, rb, S_out,
-                  _ptr(weights_out), _ptr(kept), _ptr(new_len),
-                  _stream(stream))
+    S_out = planes_out[0].shape[2] if n else (
+        S if weights_out is None else weights_out.shape[2])
+    src, dst, rows = [], [], []
+    for i in range(n):
+        a, o = planes[i], planes_out[i]
+        tail = a.shape[3:]
+        src.append(_arg(a, a.dtype, shape + tail, dev, f"planes[{i}]"))
+        dst.append(_arg(o, a.dtype, (B, Hkv, S_out) + tail, dev,
+                        f"planes_out[{i}]"))
+        rows.append(math.prod(tail) * a.element_size())
+    wa = _arg(weights, torch.float32, shape, dev, "weights")
+    wo = (None if weights_out is None
+          else _arg(weights_out, torch.float32, (B, Hkv, S_out), dev,
+                    "weights_out"))
+    if kept is None:
+        kept = _alloc((B, Hkv, budget), torch.int32, dev, stream)
+    if new_len is None:
+        new_len = _alloc((B,), torch.int32, dev, stream)
+    _enqueue("spec_kv_evict", dev, stream, wa,
+             _arg(length, torch.int32, (B,), dev, "length"), B, Hkv, S,
+             int(budget), int(recent), n, (ctypes.c_void_p * n)(*src),
+             (ctypes.c_void_p * n)(*dst), (ctypes.c_int * n)(*rows), S_out, wo,
+             _arg(kept, torch.int32, (B, Hkv, budget), dev, "kept"),
+             _arg(new_len, torch.int32, (B,), dev, "new_len"))
     return kept, new_len
 
 

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/specverify.h"
 
 namespace sv {
@@ -171,6 +173,19 @@ cudaError_t launch_eagle2(const void* draft, int B, int V, int dtype, int depth,
                           int32_t* parent, int32_t* q_row, float* value, uint8_t* mask,
                           float* draft_lse, Eagle2Cand* cand, uint32_t* status,
                           cudaStream_t st);
+
+// Raises a kernel's dynamic shared memory limit, once per device (`done` is
+// that kernel's own flag word, one bit per device ordinal).
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // A 4-bit cache's unit: a power of two in [2^-64, 2^64].
 bool kv4_unit_ok(float u);

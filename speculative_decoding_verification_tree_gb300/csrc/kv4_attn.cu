@@ -607,8 +607,8 @@ template <int D, int RT>
 cudaError_t launch_rows(RowsParams p, cudaStream_t st) {
   constexpr int smem = (int)sizeof(RowsSmem<D, RT>);
   p.nrt = (p.R + RT - 1) / RT;
-  cudaError_t e =
-      cudaFuncSetAttribute(kv4_rows<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem((const void*)kv4_rows<D, RT>, smem, done);
   if (e != cudaSuccess) return e;
   // no more CTAs than pieces of the smallest size could fill
   const int64_t most = (int64_t)p.B * p.Hkv * p.nrt * ((p.S + kKeys - 1) / kKeys);

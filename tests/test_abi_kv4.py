@@ -186,8 +186,9 @@ def test_wrappers_match_their_signatures(monkeypatch):
         calls.append(name)
         return 256
     monkeypatch.setattr(_lib, "call", fake)
-    monkeypatch.setattr(api, "_ptr", lambda t: None if t is None else FAKE)
-    monkeypatch.setattr(api, "_stream", lambda s: ctypes.c_void_p(0))
+    monkeypatch.setattr(api, "_addr", lambda t: FAKE.value)
+    monkeypatch.setattr(api, "_raw_stream", lambda i: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
     B, N, Hq, Hkv, D, S = 2, 3, 4, 2, 64, 16
     cache = api.kv4_cache(B, Hkv, S, D, device="cpu")
     k = torch.zeros(B, N, Hkv, D, dtype=torch.bfloat16)
