@@ -15,23 +15,29 @@
 // eleven bits for every key within 2^-21 of the reference.  Scores, sums
 // and outputs are float32.
 //
-// Kernel kv4_rows (16 query rows a tile, or 8): warp-level m16n8k16 products whose
-// operands are converted in registers, so the cache crosses shared memory
-// once, as codes.  Each warp owns a ring of 32-key stages filled with cp.async
-// and needs no other warp until its keys are done.
-//   S = Q K^T: lane (g, c) = (lane / 4, lane % 4) loads the contiguous
-//     quarter c of key g's row; the k index of the product is a permutation
-//     of the head dims, the same for Q.
-//   O = P V: the lane that holds P's columns of four keys loads their dims
-//     [D/8 g, D/8 (g + 1)); the codes of a key pair are interleaved by
-//     half bytes so that one conversion yields (v_s[d], v_s'[d]).
-//   The stage's rows are permuted (and their 16-byte chunks exchanged) so
-//     that neither read has bank conflicts.
+// Kernel kv4_rows (8, 16 or 32 query rows a tile): warp-level m16n8k16 products
+// with the cache as the 16-row operand, converted in registers, so that it
+// crosses shared memory once, as codes, and eight query rows waste nothing.
+// Each warp owns a ring of 32-key stages filled with cp.async and needs no
+// other warp until its keys are done.  Lane (g, c) = (lane / 4, lane % 4):
+//   S^T = K Q^T: the lane loads quarter c of key g's codes (16 bytes at D 128);
+//     the k index of the product is a permutation of the head dims, shared
+//     with Q;
+//   P^T changes from accumulator to operand layout by movmatrix;
+//   O^T = V^T P^T: the lane loads dims [D/8 g, D/8 (g + 1)) of four keys; the
+//     codes of two keys are interleaved by half bytes so that one conversion
+//     yields (v_s[d], v_s'[d]).
+// A conversion is one instruction per two codes, as is the product with the
+// block scale; those two are half of what the kernel issues.
+// Product row n of eight keys is key 4 (n & 1) + n / 2, and the stage's rows are
+// permuted (and their 16-byte chunks exchanged) so that neither read has bank
+// conflicts.
 // Work: the 32-key blocks of all (sequence, head, row tile) units form one
-// line, cut into equal pieces, one per CTA, whatever the sequences' lengths; a
+// line, cut into equal pieces, one per warp, whatever the sequences' lengths; a
 // unit cut by a piece border leaves partial (m, l, O) in the workspace, and
-// kv4_combine joins them.
+// kv4_combine joins them.  Warps never wait for one another.
 #include <cuda_runtime.h>
+#include <stddef.h>
 
 #include "kernels.h"
 #include "kv4.cuh"
@@ -40,12 +46,11 @@ namespace sv {
 namespace {
 
 constexpr int kKeys = 32;       // keys per stage
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
-constexpr int kMaxCtas = 304;   // two per SM
-constexpr int kMinBlocks = 8;   // a CTA's smallest piece: one block per warp
+constexpr int kMinBlocks = 2;   // a warp's smallest piece
 constexpr float kLift = 7.f;    // log2 of the factor that lifts P
+constexpr int kSms = 152;
+constexpr int kJoinWarps = 8;   // warps of a kv4_combine CTA
+constexpr int kJoinUnroll = 10; // 32-part groups read at once
 
 struct RowsParams {
   const uint16_t* q;
@@ -57,7 +62,10 @@ struct RowsParams {
   float v_unit;
   uint16_t* out;
   float* lse;    // or null
-  float* part;   // [2 * gridDim.x][rows per tile][D + 2]
+  float* part;       // [2 * warps][rows][D]: O of a unit's piece
+  float2* part_ml;   // [2 * warps][rows]: its reference and sum
+  int rows;          // rows of a part: min(R, rows per tile)
+  int warps;         // pieces of the line
 };
 
 __device__ __forceinline__ int clamped_prefix(const RowsParams& p, int b) {
@@ -68,10 +76,18 @@ __device__ __forceinline__ int seq_blocks(const RowsParams& p, int b) {
   return (clamped_prefix(p, b) + p.N + kKeys - 1) / kKeys;
 }
 
-// Inclusive scan over the CTA of each thread's value; `tmp` holds one value
-// per warp.  Returns the exclusive prefix; *total the sum.
-__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* tmp, int64_t* total) {
+// The line of blocks: sequences in order, each with `units` runs (heads x row
+// tiles) of seq_blocks.  Thread t sums sequences [t per, (t + 1) per); before[t]
+// = blocks before them, before[kThreads] = all blocks.  `before` and `tmp` (one
+// value per warp) lie in shared memory; ends with a barrier.
+template <int kThreads>
+__device__ __forceinline__ void scan_line(const RowsParams& p, int units, int64_t* before,
+                                          int64_t* tmp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int first = min(p.B, (int)threadIdx.x * per), last = min(p.B, first + per);
+  int64_t v = 0;
+  for (int b = first; b < last; ++b) v += (int64_t)seq_blocks(p, b) * units;
   int64_t s = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -80,36 +96,37 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* tmp, int64_t* to
   }
   if (lane == 31) tmp[warp] = s;
   __syncthreads();
-  int64_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int64_t x = tmp[w];
-    if (w < warp) before += x;
-    all += x;
-  }
+  int64_t base = 0;
+  for (int w = 0; w < warp; ++w) base += tmp[w];
+  before[threadIdx.x] = base + s - v;
+  if (threadIdx.x == kThreads - 1) before[kThreads] = base + s;
   __syncthreads();
-  *total = all;
-  return before + s - v;
 }
-
-// The line of blocks: sequences in order, each with `units` runs (heads x
-// row tiles) of seq_blocks.  Every thread sums a contiguous run of sequences.
-struct LineScan {
-  int64_t mine, total;  // blocks before this thread's sequences; all blocks
-  int first, last;      // this thread's sequences
-};
-__device__ __forceinline__ LineScan scan_line(const RowsParams& p, int units, int64_t* tmp) {
-  LineScan r;
+// The sequence that holds block `at` of the line and its first block (a warp's
+// lanes together, any `at` below the total).
+template <int kThreads>
+__device__ __forceinline__ int locate(const RowsParams& p, int units, const int64_t* before,
+                                      int64_t at, int64_t* start) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;  // threads whose sequences start at or before `at`
+  for (int i = lane; i < kThreads; i += 32) n += before[i] <= at;
+  n = __reduce_add_sync(0xffffffffu, n);
   const int per = (p.B + kThreads - 1) / kThreads;
-  r.first = min(p.B, (int)threadIdx.x * per);
-  r.last = min(p.B, r.first + per);
-  int64_t v = 0;
-  for (int b = r.first; b < r.last; ++b) v += (int64_t)seq_blocks(p, b) * units;
-  r.mine = cta_scan(v, tmp, &r.total);
-  return r;
+  // threads behind the last sequence start at the total, above `at`
+  int b = (n - 1) * per;
+  int64_t x = before[n - 1];
+  if (per > 1)
+    for (;;) {
+      const int64_t next = x + (int64_t)seq_blocks(p, b) * units;
+      if (at < next) break;
+      x = next;
+      ++b;
+    }
+  *start = x;
+  return b;
 }
-__device__ __forceinline__ int64_t piece_blocks(int64_t total, int ctas) {
-  const int64_t q = (total + ctas - 1) / ctas;
+__device__ __forceinline__ int64_t piece_blocks(int64_t total, int warps) {
+  const int64_t q = (total + warps - 1) / warps;
   return q < kMinBlocks ? kMinBlocks : q;
 }
 
@@ -130,181 +147,212 @@ struct Stage {
   }
 };
 
-template <int D, int RT>
-struct RowsSmem {
-  static constexpr int kRing = kWarps * kStages * Stage<D>::kBytes;
-  static constexpr int kPitch = D + 16;  // floats per row of the merge buffer
-  static constexpr int kMerge = kWarps * RT * kPitch * 4;
-  static_assert(kMerge + kWarps * RT * 8 <= kRing, "the merge buffers lie in the ring");
-  unsigned char ring[kRing];
-  uint32_t qf[(D / 16) * 32 * (RT / 4)];  // A fragments: a0 a2 (a1 a3) per lane and k step
-  float rowf[RT];
-  uint64_t rowmask[RT];
-  unsigned long long vnan[D / kKv4Block];  // drafted keys whose V block is NaN
-  int64_t scan[kWarps];
-  int64_t seg_start;
-  int seg_b;
+// Warps per CTA, CTAs per SM and ring stages by the number of row tiles of
+// eight, whose outputs take 32 registers each (D 128).
+template <int NT>
+struct RowsCfg {
+  static constexpr int kWarps = NT == 2 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM
+  static constexpr int kStages = NT == 4 ? 4 : 3;
+  static constexpr int kPieces = kSms * kCtas * kWarps;
 };
 
-// One 32-key stage of one warp.
-template <int D>
-__device__ __forceinline__ void fill_stage(const RowsParams& p, uint32_t st, int64_t row0, int key0,
-                                           int L, int lane) {
-  using G = Stage<D>;
-  constexpr int kChunks = G::kRow / 16;
-  const uint8_t* kc = p.kc + (row0 + key0) * G::kRow;
-  const uint8_t* vc = p.vc + (row0 + key0) * G::kRow;
-  const int left = L - key0;
-#pragma unroll
-  for (int r = 0; r < kChunks; ++r) {
-    const int id = r * 32 + lane;
-    const int key = id / kChunks, ch = id % kChunks;
-    const bool take = key < left;
-    const int64_t off = take ? (int64_t)id * 16 : 0;
-    const uint32_t dst = st + (uint32_t)G::at(key, ch);
-    cp_async<16>(dst + G::kK, kc + off, take);
-    cp_async<16>(dst + G::kV, vc + off, take);
-  }
-  const bool take = lane < left;
-  const int64_t off = (row0 + key0 + (take ? lane : 0)) * G::kSRow;
-  cp_async<G::kSRow>(st + G::kKS + (uint32_t)(lane * G::kSRow), p.ks + off, take);
-  cp_async<G::kSRow>(st + G::kVS + (uint32_t)(lane * G::kSRow), p.vs + off, take);
-}
+template <int D, int NT>
+struct RowsSmem {
+  static constexpr int kWarps = RowsCfg<NT>::kWarps;
+  static constexpr int kRing = kWarps * RowsCfg<NT>::kStages * Stage<D>::kBytes;
+  unsigned char ring[kRing];
+  uint2 qf[NT == 4 ? kWarps : 1][NT == 4 ? D / 16 : 1][NT][32];  // q's operand fragments
+  unsigned long long vnan[kWarps][D / kKv4Block];  // drafted keys whose V block is NaN
+  int64_t before[RowsCfg<NT>::kThreads + 1];
+  int64_t tmp[kWarps];
+};
 
-template <int D, int RT>
-__global__ void __launch_bounds__(kThreads, 2) kv4_rows(const RowsParams p) {
+// This lane's share of a stage: 16-byte chunks r * 32 + lane of the codes and
+// key `lane`'s scales.  The addresses of a full stage differ from the lane's
+// bases by constants.
+template <int D>
+struct LaneFill {
   using G = Stage<D>;
-  using Sm = RowsSmem<D, RT>;
-  constexpr int kHalves = RT / 8;     // row halves a lane holds
-  constexpr int kNT = D / 8;          // n tiles of O
+  static constexpr int kChunks = G::kRow / 16;
+  uint32_t dst, dst_s;  // within the stage
+  int64_t codes, scales;  // byte offsets of this lane within the cache, stage at key 0
+  __device__ __forceinline__ LaneFill(int64_t row0, int lane)
+      : dst((uint32_t)G::at(lane / kChunks, lane % kChunks)),
+        dst_s((uint32_t)(lane * G::kSRow)),
+        codes(row0 * G::kRow + lane * 16),
+        scales((row0 + lane) * G::kSRow) {}
+  __device__ __forceinline__ void issue(const RowsParams& p, uint32_t st, int key0, int L,
+                                        int lane) const {
+    const int64_t oc = codes + (int64_t)key0 * G::kRow, os = scales + (int64_t)key0 * G::kSRow;
+    const uint8_t *kc = p.kc + oc, *vc = p.vc + oc;
+    const int left = L - key0;
+    if (left >= kKeys) {
+#pragma unroll
+      for (int r = 0; r < kChunks; ++r) {
+        cp_async<16>(st + dst + G::kK + r * 512, kc + r * 512);
+        cp_async<16>(st + dst + G::kV + r * 512, vc + r * 512);
+      }
+      cp_async<G::kSRow>(st + dst_s + G::kKS, p.ks + os);
+      cp_async<G::kSRow>(st + dst_s + G::kVS, p.vs + os);
+    } else {  // keys behind the sequence are zeros, not read
+#pragma unroll
+      for (int r = 0; r < kChunks; ++r) {
+        const bool take = (r * 32 + lane) / kChunks < left;
+        cp_async_or_zero<16>(st + dst + G::kK + r * 512, take ? kc + r * 512 : p.kc, take);
+        cp_async_or_zero<16>(st + dst + G::kV + r * 512, take ? vc + r * 512 : p.vc, take);
+      }
+      const bool take = lane < left;
+      cp_async_or_zero<G::kSRow>(st + dst_s + G::kKS, take ? p.ks + os : p.ks, take);
+      cp_async_or_zero<G::kSRow>(st + dst_s + G::kVS, take ? p.vs + os : p.vs, take);
+    }
+  }
+};
+
+// A lane's share of one row tile of one (sequence, head).
+template <int D, int NT>
+struct Tile {
+  int b, kvh, rt, P;
+  __device__ __forceinline__ int row(int nt, int x) const {  // of the lane's, or -1
+    return rt * 8 * NT + nt * 8 + 2 * (int)(threadIdx.x & 3) + x;
+  }
+  __device__ __forceinline__ uint64_t mask(const RowsParams& p, int nt, int x) const {
+    const int r = row(nt, x);
+    return r < p.R ? p.mask_bits[(int64_t)b * p.N + r / (p.Hq / p.Hkv)] : 0ull;
+  }
+  __device__ __forceinline__ int64_t out_row(const RowsParams& p, int r) const {
+    const int Gq = p.Hq / p.Hkv;
+    return ((int64_t)b * p.N + r / Gq) * p.Hq + kvh * Gq + r % Gq;
+  }
+};
+// Its reference, sum (over the lane's own keys) and output.  m tile j, rows g
+// and g + 8 of the product are dims D/8 g + 2 j and + 2 j + 1, so the lane holds
+// D/8 contiguous dims of its rows: row x in o[j][nt][x] and o[j][nt][2 + x].
+template <int D, int NT>
+struct Acc {
+  float m[NT][2], l[NT][2], o[D / 16][NT][4];
+};
+
+// One warp over keys key0, key0 + step, ... (32 each) below kend.
+template <int D, int NT>
+__device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>& sm,
+                                           const Tile<D, NT>& t, int key0, int step, int kend,
+                                           Acc<D, NT>& a) {
+  using G = Stage<D>;
+  constexpr int RT = 8 * NT;
+  constexpr int kStages = RowsCfg<NT>::kStages;
+  constexpr int kSteps = D / 16;      // k steps of S
+  constexpr int kMT = D / 16;         // m tiles of O^T
   constexpr int kW = D / 32;          // code words a lane loads per key of K
-  extern __shared__ __align__(16) unsigned char raw[];
-  Sm& sm = *reinterpret_cast<Sm*>(raw);
+  constexpr bool kQReg = NT < 4;      // q's fragments stay in registers
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  launch_dependents();
+  const int b = t.b, kvh = t.kvh, rt = t.rt, P = t.P, L = P + p.N;
+  const int Gq = p.Hq / p.Hkv;
+  const uint32_t ring = smem_u32(sm.ring) + (uint32_t)(warp * kStages * G::kBytes);
+  const unsigned char* ringp = sm.ring + warp * kStages * G::kBytes;
+  unsigned long long* vnan = sm.vnan[warp];
+  const LaneFill<D> fill(((int64_t)b * p.Hkv + kvh) * p.S, lane);
+  __syncwarp();  // the tile before is done with the ring
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    const int k = key0 + i * step;
+    if (k < kend) fill.issue(p, ring + (uint32_t)(i * G::kBytes), k, L, lane);
+    cp_async_commit();
+  }
+  if (lane < D / kKv4Block) vnan[lane] = 0ull;
 
-  const int units = p.Hkv * p.nrt;
-  const LineScan ls = scan_line(p, units, sm.scan);
-  const int64_t piece = piece_blocks(ls.total, (int)gridDim.x);
-  int64_t at = (int64_t)blockIdx.x * piece;
-  const int64_t end = min(ls.total, at + piece);
-  if (at >= ls.total) return;
-  {  // the sequence that holds block `at`: one thread's run contains it
-    int64_t x = ls.mine;
-    for (int b = ls.first; b < ls.last; ++b) {
-      const int64_t n = (int64_t)seq_blocks(p, b) * units;
-      if (at >= x && at < x + n) {
-        sm.seg_b = b;
-        sm.seg_start = x;
-      }
-      x += n;
+  // q rows -> fp16 fragments, each scaled by a power of two: operand
+  // registers b0, b1 of k step s are dims 4 s .. 4 s + 3 of quarter c of row g
+  float f[NT][2];  // of this lane's rows 8 nt + 2 c + x
+  uint2 qr[kSteps][NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = rt * RT + nt * 8 + g;
+    const bool valid = r < p.R;
+    const int node = valid ? r / Gq : 0;
+    const int hq = kvh * Gq + (valid ? r % Gq : 0);
+    const uint2* src = reinterpret_cast<const uint2*>(
+        p.q + (((int64_t)b * p.N + node) * p.Hq + hq) * D + c * (D / 4));
+    uint2 w[kSteps];
+    float mx = 0.f;
+#pragma unroll
+    for (int x = 0; x < kSteps; ++x) {
+      w[x] = valid ? src[x] : make_uint2(0, 0);
+      mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf16_lo(w[x].x)), fabsf(bf16_hi(w[x].x))),
+                           fmaxf(fabsf(bf16_lo(w[x].y)), fabsf(bf16_hi(w[x].y)))));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    int e = (int)(__float_as_uint(mx) >> 23) - 127;
+    if (mx == 0.f || e == 128) e = 0;  // a zero row; an infinite one stays as it is
+    e = max(-126, min(126, e));
+    const float dn = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int x = 0; x < kSteps; ++x) {
+      const uint2 h = make_uint2(pack_half2(bf16_lo(w[x].x) * dn, bf16_hi(w[x].x) * dn),
+                                 pack_half2(bf16_lo(w[x].y) * dn, bf16_hi(w[x].y) * dn));
+      if constexpr (kQReg)
+        qr[x][nt] = h;
+      else
+        sm.qf[warp][x][nt][lane] = h;  // read back by this lane alone
+    }
+    const float fg = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      f[nt][x] = __shfl_sync(0xffffffffu, fg, 4 * (2 * c + x));
+      a.m[nt][x] = neg_inf();
+      a.l[nt][x] = 0.f;
     }
   }
-  __syncthreads();
-  int b = sm.seg_b;
-  int64_t seq_start = sm.seg_start;
-  const int Gq = p.Hq / p.Hkv;
-
-  while (at < end) {
-    // ---------------------------------------------------- this segment
-    const int P = clamped_prefix(p, b), L = P + p.N;
-    const int nblk = (L + kKeys - 1) / kKeys;
-    const int unit = (int)((at - seq_start) / nblk);
-    const int64_t unit_start = seq_start + (int64_t)unit * nblk;
-    const int k0 = (int)(at - unit_start);
-    const int k1 = (int)min((int64_t)nblk, end - unit_start);
-    const int kvh = unit / p.nrt, rt = unit % p.nrt;
-    const int64_t row0 = ((int64_t)b * p.Hkv + kvh) * p.S;
-
-    const uint32_t ring = smem_u32(sm.ring) + (uint32_t)(warp * kStages * G::kBytes);
-    const unsigned char* ringp = sm.ring + warp * kStages * G::kBytes;
-    const int mine = (k1 - k0 - warp + kWarps - 1) / kWarps;  // blocks k0 + warp + 8 i
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < mine)
-        fill_stage<D>(p, ring + (uint32_t)(i * G::kBytes), row0, (k0 + warp + kWarps * i) * kKeys,
-                      L, lane);
+  for (int j = 0; j < kMT; ++j)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) a.o[j][nt][0] = a.o[j][nt][1] = a.o[j][nt][2] = a.o[j][nt][3] = 0.f;
+  // what the lane's rows may see of the drafted keys (up to 16 rows: read
+  // early, off the path of the last blocks)
+  uint64_t masks[NT][2];
+  if constexpr (NT <= 2) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      masks[nt][0] = kend > P ? t.mask(p, nt, 0) : 0ull;
+      masks[nt][1] = kend > P ? t.mask(p, nt, 1) : 0ull;
+    }
+  }
+  auto row_mask = [&](int nt, int x) -> uint64_t {
+    if constexpr (NT <= 2)
+      return masks[nt][x];
+    else
+      return t.mask(p, nt, x);
+  };
+
+  int slot = 0;  // stage that holds key0's block
+  for (; key0 < kend; key0 += step) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    {
+      const int k = key0 + (kStages - 1) * step;
+      const int to = slot == 0 ? kStages - 1 : slot - 1;
+      if (k < kend) fill.issue(p, ring + (uint32_t)(to * G::kBytes), k, L, lane);
       cp_async_commit();
     }
+    const unsigned char* st = ringp + slot * G::kBytes;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    const bool tail = key0 + kKeys > P;
 
-    // q rows -> fp16 fragments, each scaled by a power of two
+    // ---------------------------------------------------- S^T = K Q^T
+    // accumulators [16-key tile][row tile]: keys g, g, g + 8, g + 8 x rows
+    // 2 c, 2 c + 1
+    float s[2][NT][4];
 #pragma unroll
-    for (int hf = 0; hf < kHalves; ++hf) {
-      const int row = hf * 8 + warp;  // kWarps == 8 rows per half
-      const int r = rt * RT + row;
-      const bool valid = r < p.R;
-      const int node = valid ? r / Gq : 0;
-      const int hq = kvh * Gq + (valid ? r % Gq : 0);
-      const uint16_t* src = p.q + (((int64_t)b * p.N + node) * p.Hq + hq) * D;
-      float x[D / 32];
-      if constexpr (D == 128) {
-        const uint2 w = valid ? *reinterpret_cast<const uint2*>(src + 4 * lane) : make_uint2(0, 0);
-        x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-      } else {
-        const uint32_t w = valid ? *reinterpret_cast<const uint32_t*>(src + 2 * lane) : 0u;
-        x[0] = bf16_lo(w); x[1] = bf16_hi(w);
-      }
-      float mx = 0.f;
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) mx = fmaxf(mx, fabsf(x[i]));
-      mx = warp_max(mx);
-      int e = (int)(__float_as_uint(mx) >> 23) - 127;
-      if (mx == 0.f || e == 128) e = 0;  // a zero row; an infinite one stays as it is
-      e = max(-126, min(126, e));
-      const float dn = __uint_as_float((uint32_t)(127 - e) << 23);
+      for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+      uint32_t kw[2][kW], ksc[2];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) x[i] *= dn;
-      // dims 4 s .. 4 s + 3 of quarter c: the a0 / a2 pair of k step s
-      uint32_t* dst;
-      if constexpr (D == 128) {
-        dst = sm.qf + ((lane & 7) * 32 + warp * 4 + (lane >> 3)) * (RT / 4) + 2 * hf;
-        dst[0] = pack_half2(x[0], x[1]);
-        dst[1] = pack_half2(x[2], x[3]);
-      } else {
-        dst = sm.qf + (((lane & 7) >> 1) * 32 + warp * 4 + (lane >> 3)) * (RT / 4) + 2 * hf;
-        dst[lane & 1] = pack_half2(x[0], x[1]);
-      }
-      if (lane == 0) {
-        sm.rowf[row] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-        sm.rowmask[row] = valid ? p.mask_bits[(int64_t)b * p.N + node] : 0ull;
-      }
-    }
-    if (threadIdx.x < D / kKv4Block) sm.vnan[threadIdx.x] = 0ull;
-    __syncthreads();
-
-    float f[kHalves], m[kHalves], l[kHalves];
-    float o[kNT][4];
-#pragma unroll
-    for (int hf = 0; hf < kHalves; ++hf) {
-      f[hf] = sm.rowf[hf * 8 + g];
-      m[hf] = neg_inf();
-      l[hf] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < kNT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-
-    for (int i = 0; i < mine; ++i) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      {
-        const int nx = i + kStages - 1;
-        if (nx < mine)
-          fill_stage<D>(p, ring + (uint32_t)((nx % kStages) * G::kBytes), row0,
-                        (k0 + warp + kWarps * nx) * kKeys, L, lane);
-        cp_async_commit();
-      }
-      const unsigned char* st = ringp + (i % kStages) * G::kBytes;
-      const int key0 = (k0 + warp + kWarps * i) * kKeys;
-      const bool tail = key0 + kKeys > P;
-
-      // ------------------------------------------------------ S = Q K^T
-      float s[4][4];
-      uint32_t kw[4][kW], ksc[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-        const int key = 8 * t + 4 * (g & 1) + (g >> 1);
+      for (int t = 0; t < 2; ++t) {
+        const int key = 16 * u + 8 * t + 4 * (g & 1) + (g >> 1);
         if constexpr (D == 128) {
           const uint4 w = *reinterpret_cast<const uint4*>(st + G::kK + G::at(key, c));
           kw[t][0] = w.x; kw[t][1] = w.y; kw[t][2] = w.z; kw[t][3] = w.w;
@@ -319,214 +367,235 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(const RowsParams p) {
       }
 #pragma unroll
       for (int w = 0; w < kW; ++w) {
-        uint32_t a[2][RT / 4];
+        uint32_t h[2][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t* src = sm.qf + ((2 * w + x) * 32 + lane) * (RT / 4);
-          if constexpr (RT == 16) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src);
-            a[x][0] = v.x; a[x][1] = v.y; a[x][2] = v.z; a[x][3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            a[x][0] = v.x; a[x][1] = v.y;
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          uint32_t h[4];
-          e2m1x8_to_half2(kw[t][w], h);
+        for (int t = 0; t < 2; ++t) {
+          e2m1x8_to_half2(kw[t][w], h[t]);
           const uint32_t sc = (D == 128 && w >= 2) ? dup_hi(ksc[t]) : dup_lo(ksc[t]);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) h[x] = hmul2(h[x], sc);
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            mma16816_f16(s[t], a[x][0], RT == 16 ? a[x][RT / 4 - 2] : 0u, a[x][1],
-                         RT == 16 ? a[x][RT / 4 - 1] : 0u, h[2 * x], h[2 * x + 1]);
+          for (int x = 0; x < 4; ++x) h[t][x] = hmul2(h[t][x], sc);
         }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 q = kQReg ? qr[2 * w + x][nt] : sm.qf[warp][2 * w + x][nt][lane];
+            mma16816_f16(s[u][nt], h[0][2 * x], h[1][2 * x], h[0][2 * x + 1], h[1][2 * x + 1],
+                         q.x, q.y);
+          }
       }
-      // ------------------------------------- running softmax, base 2
-      if (tail) {
+    }
+    // ------------------------------------------ running softmax, base 2
+    if (tail) {
 #pragma unroll
-        for (int hf = 0; hf < kHalves; ++hf) {
-          const uint64_t mb = sm.rowmask[hf * 8 + g];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+        for (int x = 0; x < 2; ++x) {
+          const uint64_t mb = row_mask(nt, x);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int d = key0 + 8 * t + 4 * x + c - P;
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int d = key0 + 16 * u + 8 * t + 4 * (g & 1) + (g >> 1) - P;
               const bool vis = d < 0 || (d < p.N && ((mb >> (d & 63)) & 1ull));
-              if (!vis) s[t][2 * hf + x] = neg_inf();
+              if (!vis) s[u][nt][2 * t + x] = neg_inf();
             }
         }
+    }
+    float bm[NT][2];
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        bm[nt][x] = fmaxf(fmax3f(s[0][nt][x], s[0][nt][2 + x], s[1][nt][x]), s[1][nt][2 + x]) *
+                    f[nt][x];
+        grow |= bm[nt][x] > a.m[nt][x] + 8.f;
       }
-      float bm[kHalves];
-      bool grow = false;
+    // the reference moves only when a row's maximum grows by more than 2^8
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-      for (int hf = 0; hf < kHalves; ++hf) {
-        float v = fmaxf(s[0][2 * hf], s[0][2 * hf + 1]);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int t = 1; t < 4; ++t) v = fmax3f(v, s[t][2 * hf], s[t][2 * hf + 1]);
-        bm[hf] = v * f[hf];
-        grow |= bm[hf] > m[hf] + 8.f;
-      }
-      // the reference moves only when a row's maximum grows by more than 2^8
-      if (__any_sync(0xffffffffu, grow)) {
+        for (int x = 0; x < 2; ++x) {
+          float v = fmaxf(bm[nt][x], __shfl_xor_sync(0xffffffffu, bm[nt][x], 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          const bool move = v > a.m[nt][x] + 8.f;
+          const float mn = move ? v : a.m[nt][x];
+          const float corr = move ? ex2(a.m[nt][x] - mn) : 1.f;  // 0 at the first visible key
+          a.m[nt][x] = mn;
+          a.l[nt][x] *= corr;
 #pragma unroll
-        for (int hf = 0; hf < kHalves; ++hf) {
-          float v = fmaxf(bm[hf], __shfl_xor_sync(0xffffffffu, bm[hf], 1));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-          const bool move = v > m[hf] + 8.f;
-          const float mn = move ? v : m[hf];
-          const float corr = move ? ex2(m[hf] - mn) : 1.f;  // 0 at the first visible key
-          m[hf] = mn;
-          l[hf] *= corr;
-#pragma unroll
-          for (int j = 0; j < kNT; ++j) {
-            o[j][2 * hf] *= corr;
-            o[j][2 * hf + 1] *= corr;
+          for (int j = 0; j < kMT; ++j) {
+            a.o[j][nt][x] *= corr;
+            a.o[j][nt][2 + x] *= corr;
           }
         }
-      }
-      uint32_t pa[4][kHalves];  // P as A fragments: [tile][half]
+    }
+    uint32_t pb[2][NT][2];  // P^T as operand: [16 keys][row tile][b0, b1]
 #pragma unroll
-      for (int hf = 0; hf < kHalves; ++hf) {
-        const float nm = m[hf] == neg_inf() ? kLift : kLift - m[hf];
+    for (int nt = 0; nt < NT; ++nt) {
+      const float n0 = a.m[nt][0] == neg_inf() ? kLift : kLift - a.m[nt][0];
+      const float n1 = a.m[nt][1] == neg_inf() ? kLift : kLift - a.m[nt][1];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float p0 = ex2(fmaf(s[t][2 * hf], f[hf], nm));
-          const float p1 = ex2(fmaf(s[t][2 * hf + 1], f[hf], nm));
-          l[hf] += p0 + p1;
-          pa[t][hf] = pack_half2(p0, p1);
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = ex2(fmaf(s[u][nt][2 * t], f[nt][0], n0));
+          const float p1 = ex2(fmaf(s[u][nt][2 * t + 1], f[nt][1], n1));
+          a.l[nt][0] += p0;
+          a.l[nt][1] += p1;
+          pb[u][nt][t] = transpose8x8(pack_half2(p0, p1));
+        }
+    }
+    // -------------------------------------------------- O^T += V^T P^T
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t vw[4][D / 64];
+      uint32_t sb[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int key = 16 * u + 4 * x + c;
+        if constexpr (D == 128) {
+          const uint2 w =
+              *reinterpret_cast<const uint2*>(st + G::kV + G::at(key, g >> 1) + 8 * (g & 1));
+          vw[x][0] = w.x; vw[x][1] = w.y;
+          sb[x] = st[G::kVS + key * G::kSRow + g];
+        } else {
+          vw[x][0] =
+              *reinterpret_cast<const uint32_t*>(st + G::kV + G::at(key, g >> 2) + 4 * (g & 3));
+          sb[x] = st[G::kVS + key * G::kSRow + (g >> 1)];
         }
       }
-      // ------------------------------------------------------ O += P V
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t vw[4][D / 64];
-        uint32_t sb[4];
+      if (tail) {
+        // a NaN block of a drafted key must reach the rows that see the
+        // key and no others: it is noted and its scale replaced by zero
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int key = 16 * u + 4 * x + c;
-          if constexpr (D == 128) {
-            const uint2 w =
-                *reinterpret_cast<const uint2*>(st + G::kV + G::at(key, g >> 1) + 8 * (g & 1));
-            vw[x][0] = w.x; vw[x][1] = w.y;
-            sb[x] = st[G::kVS + key * G::kSRow + g];
-          } else {
-            vw[x][0] =
-                *reinterpret_cast<const uint32_t*>(st + G::kV + G::at(key, g >> 2) + 4 * (g & 3));
-            sb[x] = st[G::kVS + key * G::kSRow + (g >> 1)];
+          const int d = key0 + 16 * u + 4 * x + c - P;
+          if (d >= 0 && d < p.N && (sb[x] & 0x7fu) == 0x7fu) {
+            atomicOr(&vnan[D == 128 ? g : (g >> 1)], 1ull << d);
+            sb[x] = 0;
           }
         }
-        if (tail) {
-          // a NaN block of a drafted key must reach the rows that see the
-          // key and no others: it is noted and its scale replaced by zero
+      }
+      const uint32_t s01 = e4m3x2_to_half2(sb[0] | (sb[1] << 8));
+      const uint32_t s23 = e4m3x2_to_half2(sb[2] | (sb[3] << 8));
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int d = key0 + 16 * u + 4 * x + c - P;
-            if (d >= 0 && d < p.N && (sb[x] & 0x7fu) == 0x7fu) {
-              atomicOr(&sm.vnan[D == 128 ? g : (g >> 1)], 1ull << d);
-              sb[x] = 0;
-            }
-          }
-        }
-        const uint32_t s01 = e4m3x2_to_half2(sb[0] | (sb[1] << 8));
-        const uint32_t s23 = e4m3x2_to_half2(sb[2] | (sb[3] << 8));
+      for (int w = 0; w < D / 64; ++w) {
+        constexpr uint32_t kLo = 0x0f0f0f0fu, kHi = 0xf0f0f0f0u;
+        uint32_t a0[4], a1[4], a2[4], a3[4];  // even / odd dims x keys 0, 1 / 2, 3
+        e2m1x8_to_half2((vw[0][w] & kLo) | ((vw[1][w] << 4) & kHi), a0);
+        e2m1x8_to_half2(((vw[0][w] >> 4) & kLo) | (vw[1][w] & kHi), a1);
+        e2m1x8_to_half2((vw[2][w] & kLo) | ((vw[3][w] << 4) & kHi), a2);
+        e2m1x8_to_half2(((vw[2][w] >> 4) & kLo) | (vw[3][w] & kHi), a3);
 #pragma unroll
-        for (int w = 0; w < D / 64; ++w) {
-          constexpr uint32_t kLo = 0x0f0f0f0fu, kHi = 0xf0f0f0f0u;
-          uint32_t b0[2][4], b1[2][4];  // [even / odd dim][pair of dims]
-          e2m1x8_to_half2((vw[0][w] & kLo) | ((vw[1][w] << 4) & kHi), b0[0]);
-          e2m1x8_to_half2(((vw[0][w] >> 4) & kLo) | (vw[1][w] & kHi), b0[1]);
-          e2m1x8_to_half2((vw[2][w] & kLo) | ((vw[3][w] << 4) & kHi), b1[0]);
-          e2m1x8_to_half2(((vw[2][w] >> 4) & kLo) | (vw[3][w] & kHi), b1[1]);
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t y0 = hmul2(a0[x], s01), y1 = hmul2(a1[x], s01);
+          const uint32_t y2 = hmul2(a2[x], s23), y3 = hmul2(a3[x], s23);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int od = 0; od < 2; ++od)
-              mma16816_f16(o[8 * w + 2 * x + od], pa[2 * u][0],
-                           kHalves == 2 ? pa[2 * u][kHalves - 1] : 0u, pa[2 * u + 1][0],
-                           kHalves == 2 ? pa[2 * u + 1][kHalves - 1] : 0u, hmul2(b0[od][x], s01),
-                           hmul2(b1[od][x], s23));
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816_f16(a.o[4 * w + x][nt], y0, y1, y2, y3, pb[u][nt][0], pb[u][nt][1]);
         }
       }
     }
+  }
 
-    // ------------------------------------------- the warps' parts joined
-    cp_async_wait<0>();
-    __syncthreads();  // every warp is done with its ring
-    float* mbuf = reinterpret_cast<float*>(sm.ring);
-    float2* ml = reinterpret_cast<float2*>(sm.ring + Sm::kMerge);  // [warp][row]: m, l
+  cp_async_wait<0>();
+  __syncwarp();  // every lane's notes of NaN blocks
+  // the sums over the eight lanes that share a row
 #pragma unroll
-    for (int hf = 0; hf < kHalves; ++hf) {
-      l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-      l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-      if (c == 0) ml[warp * RT + hf * 8 + g] = make_float2(m[hf], l[hf]);
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float v = a.l[nt][x];
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      a.l[nt][x] = v + __shfl_xor_sync(0xffffffffu, v, 16);
     }
-    // lane (g, c) holds dims [D/4 c, D/4 (c + 1)) of rows g (and g + 8): column
-    // even / odd of n tile j is dim D/8 (2 c) + j / D/8 (2 c + 1) + j.  16-byte
-    // chunk index XOR c and the pitch spread the stores over the banks.
+  const unsigned long long nan_keys = vnan[D == 128 ? g : (g >> 1)];
+  if (nan_keys != 0) {
 #pragma unroll
-    for (int hf = 0; hf < kHalves; ++hf) {
-      float4* dst =
-          reinterpret_cast<float4*>(mbuf + (int64_t)(warp * RT + hf * 8 + g) * Sm::kPitch);
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int x = 0; x < 2; ++x)
+        if (nan_keys & row_mask(nt, x)) {
 #pragma unroll
-        for (int j = 0; j < kNT; j += 4) {
-          const int chunk = (D / 16) * c + (x * kNT + j) / 4;
-          dst[chunk ^ c] = make_float4(o[j][2 * hf + x], o[j + 1][2 * hf + x],
-                                       o[j + 2][2 * hf + x], o[j + 3][2 * hf + x]);
+          for (int j = 0; j < kMT; ++j)
+            a.o[j][nt][x] = a.o[j][nt][2 + x] = __int_as_float(0x7fffffff);
         }
-    }
-    __syncthreads();
+  }
+}
+
+// Many or long sequences: pieces of the line, one per warp.
+template <int D, int NT>
+__global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
+    kv4_rows(const RowsParams p) {
+  using Sm = RowsSmem<D, NT>;
+  constexpr int kThreads = RowsCfg<NT>::kThreads;
+  constexpr int kMT = D / 16;
+  extern __shared__ __align__(16) unsigned char raw[];
+  Sm& sm = *reinterpret_cast<Sm*>(raw);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
+  launch_dependents();
+
+  const int units = p.Hkv * p.nrt;
+  scan_line<kThreads>(p, units, sm.before, sm.tmp);
+  const int64_t total = sm.before[kThreads];
+  const int64_t piece = piece_blocks(total, p.warps);
+  const int wid = blockIdx.x * RowsCfg<NT>::kWarps + warp;
+  int64_t at = (int64_t)wid * piece;
+  const int64_t end = min(total, at + piece);
+  if (at >= total) return;
+  int64_t seq_start;
+  int b = locate<kThreads>(p, units, sm.before, at, &seq_start);
+  bool first = true;  // the segment starts where the piece does
+
+  while (at < end) {
+    const int P = clamped_prefix(p, b);
+    const int nblk = (P + p.N + kKeys - 1) / kKeys;
+    const int unit = (int)((at - seq_start) / nblk);
+    const int64_t unit_start = seq_start + (int64_t)unit * nblk;
+    const int k0 = (int)(at - unit_start);
+    const int k1 = (int)min((int64_t)nblk, end - unit_start);
+    const Tile<D, NT> t = {b, unit / p.nrt, unit % p.nrt, P};
+    Acc<D, NT> a;
+    run_blocks<D, NT>(p, sm, t, k0 * kKeys, kKeys, k1 * kKeys, a);
+
     const bool whole = k0 == 0 && k1 == nblk;
-    float* part = p.part;
-    if (!whole)
-      part += ((int64_t)2 * blockIdx.x + (at == (int64_t)blockIdx.x * piece ? 0 : 1)) * RT *
-              (D + 2);
-    for (int e = threadIdx.x; e < RT * (D / 4); e += kThreads) {
-      const int row = e / (D / 4), pc = e % (D / 4);
-      const int chunk = pc ^ ((pc / (D / 16)) & 3);
-      const int r = rt * RT + row;
-      if (r >= p.R) continue;
-      float M = neg_inf();
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * RT + row].x);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 pw = ml[w * RT + row];
-        // a part whose reference never moved holds zeros, or NaN scores
-        const float k = pw.x == neg_inf() ? 1.f : ex2(pw.x - M);
-        const float4 v =
-            *reinterpret_cast<const float4*>(mbuf + (int64_t)(w * RT + row) * Sm::kPitch + 4 * pc);
-        acc.x += v.x * k;
-        acc.y += v.y * k;
-        acc.z += v.z * k;
-        acc.w += v.w * k;
-        sum += pw.y * k;
+      for (int x = 0; x < 2; ++x) {
+        const int r = t.row(nt, x);
+        if (r >= p.R) continue;
+        const float sum = a.l[nt][x];
+        if (whole) {
+          const int64_t orow = t.out_row(p, r);
+          const float inv = sum == 0.f ? 0.f : p.v_unit / sum;
+          uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + (D / 8) * g);
+#pragma unroll
+          for (int j = 0; j < kMT; j += 4)
+            dst[j / 4] =
+                make_uint4(pack_bf16x2(a.o[j][nt][x] * inv, a.o[j][nt][2 + x] * inv),
+                           pack_bf16x2(a.o[j + 1][nt][x] * inv, a.o[j + 1][nt][2 + x] * inv),
+                           pack_bf16x2(a.o[j + 2][nt][x] * inv, a.o[j + 2][nt][2 + x] * inv),
+                           pack_bf16x2(a.o[j + 3][nt][x] * inv, a.o[j + 3][nt][2 + x] * inv));
+          if (p.lse && g == 0)
+            p.lse[orow] = sum == 0.f ? neg_inf() : a.m[nt][x] + log2f(sum) - kLift;
+        } else {
+          const int64_t prow = ((int64_t)2 * wid + (first ? 0 : 1)) * p.rows + (r - t.rt * 8 * NT);
+          float4* dst = reinterpret_cast<float4*>(p.part + prow * D + (D / 8) * g);
+#pragma unroll
+          for (int j = 0; j < kMT; j += 2)
+            dst[j / 2] = make_float4(a.o[j][nt][x], a.o[j][nt][2 + x], a.o[j + 1][nt][x],
+                                     a.o[j + 1][nt][2 + x]);
+          if (g == 0) p.part_ml[prow] = make_float2(a.m[nt][x], sum);
+        }
       }
-      if (sm.vnan[chunk * 4 / kKv4Block] & sm.rowmask[row])
-        acc = make_float4(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff),
-                          __int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
-      if (whole) {
-        const int node = r / Gq, hq = kvh * Gq + r % Gq;
-        const int64_t orow = ((int64_t)b * p.N + node) * p.Hq + hq;
-        const float inv = sum == 0.f ? 0.f : p.v_unit / sum;
-        *reinterpret_cast<uint2*>(p.out + orow * D + 4 * chunk) =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (p.lse && chunk == 0) p.lse[orow] = sum == 0.f ? neg_inf() : M + log2f(sum) - kLift;
-      } else {
-        float* dst = part + (int64_t)row * (D + 2);
-        *reinterpret_cast<float2*>(dst + 4 * chunk) = make_float2(acc.x, acc.y);
-        *reinterpret_cast<float2*>(dst + 4 * chunk + 2) = make_float2(acc.z, acc.w);
-        if (chunk == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M, sum);
-      }
-    }
-    __syncthreads();
     at = unit_start + k1;
+    first = false;
     if (unit + 1 == units && k1 == nblk) {  // the next block belongs to the next sequence
       seq_start += (int64_t)units * nblk;
       ++b;
@@ -534,101 +603,314 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_rows(const RowsParams p) {
   }
 }
 
-// Joins the parts of a unit that several CTAs worked on.
-template <int D, int RT>
-__global__ void __launch_bounds__(kThreads) kv4_combine(const RowsParams p, int ctas) {
-  __shared__ int64_t tmp[kWarps];
-  __shared__ int64_t seq_start_s;
-  __shared__ float wgt[kMaxCtas][RT];
-  __shared__ float rowM[RT], rowL[RT];
-  const int units = p.Hkv * p.nrt;
-  const int b = (int)(blockIdx.x / units), unit = (int)(blockIdx.x % units);
-  const LineScan ls = scan_line(p, units, tmp);
-  if (b >= ls.first && b < ls.last) {
-    int64_t x = ls.mine;
-    for (int i = ls.first; i < b; ++i) x += (int64_t)seq_blocks(p, i) * units;
-    seq_start_s = x;
-  }
-  __syncthreads();
-  const int64_t piece = piece_blocks(ls.total, ctas);
-  const int nblk = seq_blocks(p, b);
-  const int64_t t0 = seq_start_s + (int64_t)unit * nblk, t1 = t0 + nblk;
-  const int c0 = (int)(t0 / piece), c1 = (int)((t1 - 1) / piece);
-  grid_dependency_wait();  // before any exit: this grid must not end first
-  if (c0 == c1) return;
-  const int n = c1 - c0 + 1;
-  const int kvh = unit / p.nrt, rt = unit % p.nrt;
-  const int Gq = p.Hq / p.Hkv;
-  const int first = 2 * c0 + (t0 == (int64_t)c0 * piece ? 0 : 1);
-  auto part = [&](int i, int row) {
-    const int64_t slot = i == 0 ? first : 2 * (c0 + i);
-    return p.part + (slot * RT + row) * (D + 2);
-  };
+// Few or short sequences: one cluster of CTAs per unit (p.warps = its size),
+// one launch, no workspace.  The warps' parts are joined in shared memory, then
+// the CTAs' over the cluster.
+template <int D, int NT>
+__global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
+    kv4_unit(const RowsParams p) {
+  using Sm = RowsSmem<D, NT>;
+  using Cfg = RowsCfg<NT>;
+  constexpr int RT = 8 * NT, kWarps = Cfg::kWarps, kThreads = Cfg::kThreads, kMT = D / 16;
+  constexpr int kMerge = kWarps * RT * D * 4;  // the warps' outputs
+  constexpr int kOwn = kMerge + kWarps * RT * 8;  // their m, l; then this CTA's output, m, l
+  static_assert(kOwn + RT * (D * 4 + 8) <= (int)offsetof(Sm, vnan), "joined in the ring (and qf)");
+  extern __shared__ __align__(16) unsigned char raw[];
+  Sm& sm = *reinterpret_cast<Sm*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int row = warp; row < RT; row += kWarps) {
-    if (rt * RT + row >= p.R) continue;
-    float M = neg_inf(), sum = 0.f;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, part(i, row)[D]);
-    M = warp_max(M);
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(part(i, row) + D);
-      const float k = ml.x == neg_inf() ? 1.f : ex2(ml.x - M);
-      wgt[i][row] = k;
-      sum += ml.y * k;
+  const int g = lane >> 2, c = lane & 3;
+  const int C = p.warps;
+  const int rank = blockIdx.x % C;
+  int unit = blockIdx.x / C;
+  Tile<D, NT> t;
+  t.rt = unit % p.nrt;
+  unit /= p.nrt;
+  t.kvh = unit % p.Hkv;
+  t.b = unit / p.Hkv;
+  t.P = clamped_prefix(p, t.b);
+  const int nblk = (t.P + p.N + kKeys - 1) / kKeys;
+  // blocks rank * kWarps + warp, + C * kWarps, ...
+  Acc<D, NT> a;
+  run_blocks<D, NT>(p, sm, t, (rank * kWarps + warp) * kKeys, C * kWarps * kKeys, nblk * kKeys, a);
+
+  __syncthreads();  // every warp is done with its ring
+  float* mbuf = reinterpret_cast<float*>(sm.ring);
+  float2* ml = reinterpret_cast<float2*>(sm.ring + kMerge);  // [warp][row]
+  float* own = reinterpret_cast<float*>(sm.ring + kOwn);     // [row][D]
+  float2* own_ml = reinterpret_cast<float2*>(own + RT * D);
+  const int rows = min(RT, p.R - t.rt * RT);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int row = nt * 8 + 2 * c + x;
+      if (row >= rows) continue;
+      if (g == 0) ml[warp * RT + row] = make_float2(a.m[nt][x], a.l[nt][x]);
+      // 16-byte chunks XOR c spread the stores over the banks
+      float4* dst = reinterpret_cast<float4*>(mbuf + (warp * RT + row) * D);
+#pragma unroll
+      for (int j = 0; j < kMT; j += 2)
+        dst[((D / 32) * g + j / 2) ^ c] = make_float4(
+            a.o[j][nt][x], a.o[j][nt][2 + x], a.o[j + 1][nt][x], a.o[j + 1][nt][2 + x]);
     }
-    sum = warp_sum(sum);
-    if (lane == 0) {
-      rowM[row] = M;
-      rowL[row] = sum;
-    }
-  }
   __syncthreads();
-  for (int e = threadIdx.x; e < RT * (D / 2); e += kThreads) {
-    const int row = e / (D / 2), x = e % (D / 2);
-    const int r = rt * RT + row;
-    if (r >= p.R) continue;
-    float2 acc = make_float2(0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-      const float2 v = *reinterpret_cast<const float2*>(part(i, row) + 2 * x);
-      const float k = wgt[i][row];
+  auto emit = [&](int row, int chunk, const float4& v, float M, float sum) {
+    const int64_t orow = t.out_row(p, t.rt * RT + row);
+    const float inv = sum == 0.f ? 0.f : p.v_unit / sum;
+    *reinterpret_cast<uint2*>(p.out + orow * D + 4 * chunk) =
+        make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+    if (p.lse && chunk == 0) p.lse[orow] = sum == 0.f ? neg_inf() : M + log2f(sum) - kLift;
+  };
+  for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
+    const int row = e / (D / 4), pc = e % (D / 4);
+    const int chunk = pc ^ ((row >> 1) & 3);
+    float M = neg_inf();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * RT + row].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 pw = ml[w * RT + row];
+      // a part whose reference never moved holds zeros, or NaN scores
+      const float k = pw.x == neg_inf() ? 1.f : ex2(pw.x - M);
+      const float4 v = *reinterpret_cast<const float4*>(mbuf + (w * RT + row) * D + 4 * pc);
       acc.x = fmaf(v.x, k, acc.x);
       acc.y = fmaf(v.y, k, acc.y);
+      acc.z = fmaf(v.z, k, acc.z);
+      acc.w = fmaf(v.w, k, acc.w);
+      sum = fmaf(pw.y, k, sum);
     }
-    const int node = r / Gq, hq = kvh * Gq + r % Gq;
-    const int64_t orow = ((int64_t)b * p.N + node) * p.Hq + hq;
-    const float sum = rowL[row];
-    const float inv = sum == 0.f ? 0.f : p.v_unit / sum;
-    *reinterpret_cast<uint32_t*>(p.out + orow * D + 2 * x) = pack_bf16x2(acc.x * inv, acc.y * inv);
-    if (p.lse && x == 0) p.lse[orow] = sum == 0.f ? neg_inf() : rowM[row] + log2f(sum) - kLift;
+    if (C == 1) {
+      emit(row, chunk, acc, M, sum);
+    } else {
+      *reinterpret_cast<float4*>(own + row * D + 4 * chunk) = acc;
+      if (chunk == 0) own_ml[row] = make_float2(M, sum);
+    }
+  }
+  if (C == 1) return;
+  cluster_sync();
+  for (int e = threadIdx.x * C + rank; e < rows * (D / 4); e += kThreads * C) {
+    const int row = e / (D / 4), chunk = e % (D / 4);
+    const uint32_t ao = smem_u32(own + row * D + 4 * chunk), am = smem_u32(own_ml + row);
+    float M = neg_inf(), sum = 0.f;
+    for (int i = 0; i < C; ++i) M = fmaxf(M, ld_dsmem_f32(mapa(am, i)));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < C; ++i) {
+      const float2 pw = ld_dsmem_v2(mapa(am, i));
+      const float4 v = ld_dsmem_v4(mapa(ao, i));
+      const float k = pw.x == neg_inf() ? 1.f : ex2(pw.x - M);
+      acc.x = fmaf(v.x, k, acc.x);
+      acc.y = fmaf(v.y, k, acc.y);
+      acc.z = fmaf(v.z, k, acc.z);
+      acc.w = fmaf(v.w, k, acc.w);
+      sum = fmaf(pw.y, k, sum);
+    }
+    emit(row, chunk, acc, M, sum);
+  }
+  cluster_sync();  // no CTA leaves while another reads its parts
+}
+
+// Joins the parts of a unit that several warps worked on: a CTA takes `per_cta`
+// rows of a unit, kJoinWarps / per_cta warps a row.  The units are all of
+// them, or, when there are more units than piece borders, those that hold a
+// border, each found from the first border inside it.
+template <int D, int RT>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    kv4_combine(const RowsParams p, bool by_border, int per_cta) {
+  constexpr int kThreads = kJoinWarps * 32;
+  __shared__ int64_t before[kThreads + 1], tmp[kJoinWarps];
+  __shared__ float acc_s[kJoinWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int units = p.Hkv * p.nrt;
+  scan_line<kThreads>(p, units, before, tmp);
+  grid_dependency_wait();  // before any exit: this grid must not end first
+  const int64_t total = before[kThreads];
+  const int64_t piece = piece_blocks(total, p.warps);
+  Tile<D, RT / 8> t;
+  int unit, nblk;
+  int64_t t0;  // the unit's first block
+  if (by_border) {
+    const int64_t pos = (int64_t)(blockIdx.x + 1) * piece;
+    if (pos >= total) return;
+    int64_t start;
+    t.b = locate<kThreads>(p, units, before, pos, &start);
+    nblk = seq_blocks(p, t.b);
+    unit = (int)((pos - start) / nblk);
+    t0 = start + (int64_t)unit * nblk;
+    if (t0 == pos || t0 < pos - piece) return;  // not inside, or not the first one inside
+  } else {
+    t.b = (int)(blockIdx.x / units);
+    unit = (int)(blockIdx.x % units);
+    nblk = seq_blocks(p, t.b);
+    const int per = (p.B + kThreads - 1) / kThreads;
+    t0 = before[t.b / per] + (int64_t)unit * nblk;
+    for (int i = t.b / per * per; i < t.b; ++i) t0 += (int64_t)seq_blocks(p, i) * units;
+  }
+  const int c0 = (int)(t0 / piece), c1 = (int)((t0 + nblk - 1) / piece);
+  if (c0 == c1) return;
+  t.kvh = unit / p.nrt;
+  t.rt = unit % p.nrt;
+  const int n = c1 - c0 + 1;
+  const int lead = t0 == (int64_t)c0 * piece ? 0 : 1;
+  const int wpr = max(1, kJoinWarps / per_cta);  // more than one: one row per warp group
+  const int last = min((int)(blockIdx.y + 1) * per_cta, min(RT, p.R - t.rt * RT));
+  const int sub = warp % wpr;
+  constexpr int kV = D / 32;  // floats per lane
+  for (int row = blockIdx.y * per_cta + warp / wpr; row < last || wpr > 1;
+       row += kJoinWarps / wpr) {
+    auto part = [&](int i) -> int64_t {
+      return ((int64_t)2 * (c0 + i) + (i == 0 ? lead : 0)) * p.rows + row;
+    };
+    float M = neg_inf(), sum = 0.f;  // every warp for itself
+    float acc[kV] = {};
+    if (row < last) {
+      float ls[kJoinUnroll], xs[kJoinUnroll];
+#pragma unroll
+      for (int u = 0; u < kJoinUnroll; ++u) {  // the first parts' loads in flight together
+        const int i = lane + 32 * u;
+        const float2 ml = i < n ? p.part_ml[part(i)] : make_float2(neg_inf(), 0.f);
+        xs[u] = ml.x;
+        ls[u] = ml.y;
+        M = fmaxf(M, ml.x);
+      }
+      for (int i = lane + 32 * kJoinUnroll; i < n; i += 32) M = fmaxf(M, p.part_ml[part(i)].x);
+      M = warp_max(M);
+      // a part whose reference never moved holds zeros, or NaN scores
+#pragma unroll
+      for (int u = 0; u < kJoinUnroll; ++u)
+        sum += ls[u] * (xs[u] == neg_inf() ? 1.f : ex2(xs[u] - M));
+      for (int i = lane + 32 * kJoinUnroll; i < n; i += 32) {
+        const float2 ml = p.part_ml[part(i)];
+        sum += ml.y * (ml.x == neg_inf() ? 1.f : ex2(ml.x - M));
+      }
+      sum = warp_sum(sum);
+#pragma unroll 8
+      for (int i = sub; i < n; i += wpr) {
+        const int64_t pr = part(i);
+        const float x = p.part_ml[pr].x;
+        const float k = x == neg_inf() ? 1.f : ex2(x - M);
+        const float* src = p.part + pr * D + lane * kV;
+        if constexpr (kV == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          acc[0] = fmaf(v.x, k, acc[0]);
+          acc[1] = fmaf(v.y, k, acc[1]);
+          acc[2] = fmaf(v.z, k, acc[2]);
+          acc[3] = fmaf(v.w, k, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          acc[0] = fmaf(v.x, k, acc[0]);
+          acc[1] = fmaf(v.y, k, acc[1]);
+        }
+      }
+    }
+    if (wpr > 1) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) acc_s[warp][lane * kV + i] = acc[i];
+      __syncthreads();
+      if (sub == 0)
+        for (int w = 1; w < wpr; ++w)
+#pragma unroll
+          for (int i = 0; i < kV; ++i) acc[i] += acc_s[warp + w][lane * kV + i];
+    }
+    if (sub == 0 && row < last) {
+      const int64_t orow = t.out_row(p, t.rt * RT + row);
+      const float inv = sum == 0.f ? 0.f : p.v_unit / sum;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kV);
+#pragma unroll
+      for (int i = 0; i < kV; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+      if (p.lse && lane == 0) p.lse[orow] = sum == 0.f ? neg_inf() : M + log2f(sum) - kLift;
+    }
+    if (wpr > 1) break;
   }
 }
 
-template <int D, int RT>
-cudaError_t launch_rows(RowsParams p, cudaStream_t st) {
-  constexpr int smem = (int)sizeof(RowsSmem<D, RT>);
-  p.nrt = (p.R + RT - 1) / RT;
+// Pieces (warps) a call uses: no more than its blocks could fill.
+template <int NT>
+int rows_warps(int B, int Hkv, int R, int S) {
+  const int64_t nrt = (R + 8 * NT - 1) / (8 * NT);
+  const int64_t blocks = (int64_t)B * Hkv * nrt * ((S + kKeys - 1) / kKeys);
+  const int64_t want = (blocks + kMinBlocks - 1) / kMinBlocks;
+  return (int)(want < RowsCfg<NT>::kPieces ? want : RowsCfg<NT>::kPieces);
+}
+size_t part_bytes(int warps, int rows, int D) {
+  return ((size_t)2 * warps * rows * (D + 2) * sizeof(float) + 255) / 256 * 256;
+}
+size_t rows_ws(int B, int Hkv, int R, int D, int S) {
+  if (R <= 8) return part_bytes(rows_warps<1>(B, Hkv, R, S), R, D);
+  if (R <= 16) return part_bytes(rows_warps<2>(B, Hkv, R, S), R, D);
+  return part_bytes(rows_warps<4>(B, Hkv, R, S), R < 32 ? R : 32, D);
+}
+
+// CTAs per cluster of kv4_unit, or 0 for pieces of the line.  Units leave
+// some of the resident CTAs idle, or the last wave part empty, for as many
+// 32-key blocks a warp as the longest unit may have; pieces cost the join's
+// launch and partial outputs.  Measured (32 / 8 heads, D 128): units 10.9 us,
+// pieces 15.1 us at one sequence of 1 K keys, 15.0 / 19.1 at 8 K, 27.3 / 25.2
+// at 32 K, 81 / 48 at 128 K; 32 sequences of up to 4 K 35.6 / 39.6, 64 of them
+// 62.1 / 61.1, 64 of 32 K 442 / 388.
+template <int NT>
+int unit_cluster(int64_t units, int S) {
+  constexpr int64_t slots = kSms * RowsCfg<NT>::kCtas;
+  constexpr double kIdleBlocks = 8;
+  int C = 1;
+  while (C < 8 && units * C * 2 <= slots) C *= 2;
+  const int64_t waves = (units * C + slots - 1) / slots;
+  const double idle = 1.0 - (double)(units * C) / (double)(waves * slots);
+  const double blocks = (double)S / kKeys / (C * RowsCfg<NT>::kWarps);
+  return idle * blocks * waves > kIdleBlocks ? 0 : C;
+}
+
+template <int D, int NT>
+cudaError_t launch_rows(RowsParams p, void* ws, cudaStream_t st) {
+  constexpr int RT = 8 * NT;
+  using Cfg = RowsCfg<NT>;
+  constexpr int smem = (int)sizeof(RowsSmem<D, NT>);
+  static_assert((smem + 1024) * Cfg::kCtas <= 228 * 1024, "the pieces are resident at once");
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem((const void*)kv4_rows<D, RT>, smem, done);
+  cudaError_t e = allow_smem((const void*)kv4_rows<D, NT>, smem, done);
   if (e != cudaSuccess) return e;
-  // no more CTAs than pieces of the smallest size could fill
-  const int64_t most = (int64_t)p.B * p.Hkv * p.nrt * ((p.S + kKeys - 1) / kKeys);
-  const int64_t want = (most + kMinBlocks - 1) / kMinBlocks;
-  const int ctas = (int)(want < kMaxCtas ? want : kMaxCtas);
-  prof_begin(SPEC_PROF_ATTN, st);
-  kv4_rows<D, RT><<<ctas, kThreads, smem, st>>>(p);
-  prof_end(SPEC_PROF_ATTN, st);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || ctas == 1) return e;
+  p.nrt = (p.R + RT - 1) / RT;
+  p.rows = p.R < RT ? p.R : RT;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.Hkv * p.nrt));
-  cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_combine<D, RT>, p, ctas);
+  const int64_t units = (int64_t)p.B * p.Hkv * p.nrt;
+  const int cluster = unit_cluster<NT>(units, p.S);
+  if (cluster > 0) {
+    static std::atomic<uint64_t> done_unit{0};
+    e = allow_smem((const void*)kv4_unit<D, NT>, smem, done_unit);
+    if (e != cudaSuccess) return e;
+    p.warps = cluster;
+    cfg.gridDim = dim3((unsigned)(units * cluster));
+    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    prof_begin(SPEC_PROF_ATTN, st);
+    e = cudaLaunchKernelEx(&cfg, kv4_unit<D, NT>, p);
+    prof_end(SPEC_PROF_ATTN, st);
+    return e;
+  }
+  p.warps = rows_warps<NT>(p.B, p.Hkv, p.R, p.S);
+  p.part = (float*)ws;
+  p.part_ml = (float2*)(p.part + (size_t)2 * p.warps * p.rows * D);
+  prof_begin(SPEC_PROF_ATTN, st);
+  kv4_rows<D, NT><<<(p.warps + Cfg::kWarps - 1) / Cfg::kWarps, Cfg::kThreads, smem, st>>>(p);
+  prof_end(SPEC_PROF_ATTN, st);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.warps == 1) return e;
+  const bool by_border = units > p.warps - 1;
+  const int64_t joins = by_border ? p.warps - 1 : units;
+  const int per_cta = joins * p.rows <= 2 * kSms ? 1 : p.rows;
+  cfg.gridDim = dim3((unsigned)joins, (unsigned)((p.rows + per_cta - 1) / per_cta));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, kv4_combine<D, RT>, p, by_border, per_cta);
 }
 
 }  // namespace
@@ -641,8 +923,9 @@ extern "C" size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, 
   if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N ||
       (D != 64 && D != 128))
     return 0;
-  const size_t bytes = (size_t)2 * kMaxCtas * 16 * (D + 2) * sizeof(float);
-  return (bytes + 255) / 256 * 256;
+  const int64_t R = (int64_t)N * (Hq / Hkv);
+  if ((int64_t)B * Hkv * ((R + 15) / 16) > 2147483647) return 0;
+  return rows_ws(B, Hkv, (int)R, D, S) + 256;
 }
 
 extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
@@ -688,12 +971,13 @@ extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
   p.v_unit = v_unit;
   p.out = (uint16_t*)out;
   p.lse = lse;
-  p.part = (float*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
   if (D == 128)
-    e = R <= 8 ? launch_rows<128, 8>(p, st) : launch_rows<128, 16>(p, st);
+    e = R <= 8 ? launch_rows<128, 1>(p, workspace, st)
+               : (R <= 16 ? launch_rows<128, 2>(p, workspace, st) : launch_rows<128, 4>(p, workspace, st));
   else
-    e = R <= 8 ? launch_rows<64, 8>(p, st) : launch_rows<64, 16>(p, st);
+    e = R <= 8 ? launch_rows<64, 1>(p, workspace, st)
+               : (R <= 16 ? launch_rows<64, 2>(p, workspace, st) : launch_rows<64, 4>(p, workspace, st));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
