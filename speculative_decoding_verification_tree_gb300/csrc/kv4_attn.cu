@@ -41,6 +41,7 @@
 
 #include "kernels.h"
 #include "kv4.cuh"
+#include "kv4_attn.h"
 
 namespace sv {
 namespace {
@@ -49,19 +50,12 @@ constexpr int kKeys = 32;       // keys per stage
 constexpr int kMinBlocks = 2;   // a warp's smallest piece
 constexpr float kLift = 7.f;    // log2 of the factor that lifts P
 constexpr int kSms = 152;
+constexpr int kRowsMax = 32;    // query rows up to which these kernels are used
 constexpr int kJoinWarps = 8;   // warps of a kv4_combine CTA
 constexpr int kJoinUnroll = 10; // 32-part groups read at once
 
-struct RowsParams {
-  const uint16_t* q;
-  const uint8_t *kc, *ks, *vc, *vs;
-  const int32_t* prefix_len;
-  const uint64_t* mask_bits;
-  int B, N, Hq, Hkv, S, R, nrt;
-  float scale_log2;  // scale * log2(e) * k_unit
-  float v_unit;
-  uint16_t* out;
-  float* lse;    // or null
+struct RowsParams : Kv4Attn {
+  int nrt;           // row tiles per (sequence, head)
   float* part;       // [2 * warps][rows][D]: O of a unit's piece
   float2* part_ml;   // [2 * warps][rows]: its reference and sum
   int rows;          // rows of a part: min(R, rows per tile)
@@ -839,7 +833,8 @@ size_t part_bytes(int warps, int rows, int D) {
 size_t rows_ws(int B, int Hkv, int R, int D, int S) {
   if (R <= 8) return part_bytes(rows_warps<1>(B, Hkv, R, S), R, D);
   if (R <= 16) return part_bytes(rows_warps<2>(B, Hkv, R, S), R, D);
-  return part_bytes(rows_warps<4>(B, Hkv, R, S), R < 32 ? R : 32, D);
+  if (R <= kRowsMax) return part_bytes(rows_warps<4>(B, Hkv, R, S), R, D);
+  return kv4_tc_ws(B, Hkv, R, D, S);
 }
 
 // CTAs per cluster of kv4_unit, or 0 for pieces of the line.  Units leave
@@ -862,7 +857,9 @@ int unit_cluster(int64_t units, int S) {
 }
 
 template <int D, int NT>
-cudaError_t launch_rows(RowsParams p, void* ws, cudaStream_t st) {
+cudaError_t launch_rows(const Kv4Attn& a, void* ws, cudaStream_t st) {
+  RowsParams p = {};
+  (Kv4Attn&)p = a;
   constexpr int RT = 8 * NT;
   using Cfg = RowsCfg<NT>;
   constexpr int smem = (int)sizeof(RowsSmem<D, NT>);
@@ -918,6 +915,9 @@ cudaError_t launch_rows(RowsParams p, void* ws, cudaStream_t st) {
 
 using namespace sv;
 
+// More than kRowsMax query rows per key/value head go to the tensor-core kernel
+// (kv4_attn_tc.cu).  Measured (32 sequences of 2 to 4 K keys, D 128): 32 rows
+// 78.5 us here, 92.8 us there; 36 rows 124 / 93 us.
 extern "C" size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D,
                                                           int S) {
   if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N ||
@@ -953,7 +953,7 @@ extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
   if (!workspace || (uintptr_t)workspace % 256 != 0 ||
       ws_bytes < spec_tree_attention_kv4_workspace_bytes(B, N, Hq, Hkv, D, S))
     return SPEC_ERR_WORKSPACE;
-  RowsParams p = {};
+  Kv4Attn p = {};
   p.q = (const uint16_t*)q;
   p.kc = k_codes;
   p.ks = k_scales;
@@ -973,11 +973,15 @@ extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
   p.lse = lse;
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e;
-  if (D == 128)
+  if (R > kRowsMax)
+    e = launch_kv4_tc(p, D, workspace, st);
+  else if (D == 128)
     e = R <= 8 ? launch_rows<128, 1>(p, workspace, st)
-               : (R <= 16 ? launch_rows<128, 2>(p, workspace, st) : launch_rows<128, 4>(p, workspace, st));
+               : (R <= 16 ? launch_rows<128, 2>(p, workspace, st)
+                          : launch_rows<128, 4>(p, workspace, st));
   else
     e = R <= 8 ? launch_rows<64, 1>(p, workspace, st)
-               : (R <= 16 ? launch_rows<64, 2>(p, workspace, st) : launch_rows<64, 4>(p, workspace, st));
+               : (R <= 16 ? launch_rows<64, 2>(p, workspace, st)
+                          : launch_rows<64, 4>(p, workspace, st));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
