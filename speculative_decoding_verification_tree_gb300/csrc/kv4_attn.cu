@@ -42,6 +42,7 @@
 #include "kernels.h"
 #include "kv4.cuh"
 #include "kv4_attn.h"
+#include "line.cuh"
 
 namespace sv {
 namespace {
@@ -71,54 +72,14 @@ __device__ __forceinline__ int seq_blocks(const RowsParams& p, int b) {
 }
 
 // The line of blocks: sequences in order, each with `units` runs (heads x row
-// tiles) of seq_blocks.  Thread t sums sequences [t per, (t + 1) per); before[t]
-// = blocks before them, before[kThreads] = all blocks.  `before` and `tmp` (one
-// value per warp) lie in shared memory; ends with a barrier.
-template <int kThreads>
-__device__ __forceinline__ void scan_line(const RowsParams& p, int units, int64_t* before,
-                                          int64_t* tmp) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int first = min(p.B, (int)threadIdx.x * per), last = min(p.B, first + per);
-  int64_t v = 0;
-  for (int b = first; b < last; ++b) v += (int64_t)seq_blocks(p, b) * units;
-  int64_t s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += u;
+// tiles) of seq_blocks.
+struct LineBlocks {
+  const RowsParams& p;
+  int units;
+  __device__ __forceinline__ int64_t operator()(int b) const {
+    return (int64_t)seq_blocks(p, b) * units;
   }
-  if (lane == 31) tmp[warp] = s;
-  __syncthreads();
-  int64_t base = 0;
-  for (int w = 0; w < warp; ++w) base += tmp[w];
-  before[threadIdx.x] = base + s - v;
-  if (threadIdx.x == kThreads - 1) before[kThreads] = base + s;
-  __syncthreads();
-}
-// The sequence that holds block `at` of the line and its first block (a warp's
-// lanes together, any `at` below the total).
-template <int kThreads>
-__device__ __forceinline__ int locate(const RowsParams& p, int units, const int64_t* before,
-                                      int64_t at, int64_t* start) {
-  const int lane = threadIdx.x & 31;
-  int n = 0;  // threads whose sequences start at or before `at`
-  for (int i = lane; i < kThreads; i += 32) n += before[i] <= at;
-  n = __reduce_add_sync(0xffffffffu, n);
-  const int per = (p.B + kThreads - 1) / kThreads;
-  // threads behind the last sequence start at the total, above `at`
-  int b = (n - 1) * per;
-  int64_t x = before[n - 1];
-  if (per > 1)
-    for (;;) {
-      const int64_t next = x + (int64_t)seq_blocks(p, b) * units;
-      if (at < next) break;
-      x = next;
-      ++b;
-    }
-  *start = x;
-  return b;
-}
+};
 __device__ __forceinline__ int64_t piece_blocks(int64_t total, int warps) {
   const int64_t q = (total + warps - 1) / warps;
   return q < kMinBlocks ? kMinBlocks : q;
@@ -535,7 +496,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   launch_dependents();
 
   const int units = p.Hkv * p.nrt;
-  scan_line<kThreads>(p, units, sm.before, sm.tmp);
+  const LineBlocks line = {p, units};
+  scan_line<kThreads>(p.B, line, sm.before, sm.tmp);
   const int64_t total = sm.before[kThreads];
   const int64_t piece = piece_blocks(total, p.warps);
   const int wid = blockIdx.x * RowsCfg<NT>::kWarps + warp;
@@ -543,7 +505,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   const int64_t end = min(total, at + piece);
   if (at >= total) return;
   int64_t seq_start;
-  int b = locate<kThreads>(p, units, sm.before, at, &seq_start);
+  int b = locate<kThreads>(p.B, line, sm.before, at, &seq_start);
   bool first = true;  // the segment starts where the piece does
 
   while (at < end) {
@@ -717,7 +679,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   __shared__ float acc_s[kJoinWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int units = p.Hkv * p.nrt;
-  scan_line<kThreads>(p, units, before, tmp);
+  const LineBlocks line = {p, units};
+  scan_line<kThreads>(p.B, line, before, tmp);
   grid_dependency_wait();  // before any exit: this grid must not end first
   const int64_t total = before[kThreads];
   const int64_t piece = piece_blocks(total, p.warps);
@@ -728,7 +691,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const int64_t pos = (int64_t)(blockIdx.x + 1) * piece;
     if (pos >= total) return;
     int64_t start;
-    t.b = locate<kThreads>(p, units, before, pos, &start);
+    t.b = locate<kThreads>(p.B, line, before, pos, &start);
     nblk = seq_blocks(p, t.b);
     unit = (int)((pos - start) / nblk);
     t0 = start + (int64_t)unit * nblk;
@@ -739,7 +702,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     nblk = seq_blocks(p, t.b);
     const int per = (p.B + kThreads - 1) / kThreads;
     t0 = before[t.b / per] + (int64_t)unit * nblk;
-    for (int i = t.b / per * per; i < t.b; ++i) t0 += (int64_t)seq_blocks(p, i) * units;
+    for (int i = t.b / per * per; i < t.b; ++i) t0 += line(i);
   }
   const int c0 = (int)(t0 / piece), c1 = (int)((t0 + nblk - 1) / piece);
   if (c0 == c1) return;

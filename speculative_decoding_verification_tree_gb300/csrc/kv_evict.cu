@@ -2,16 +2,19 @@
 // the most recent ones and, of the others, those of highest accumulated
 // attention weight; their rows move together, in order.
 //
-// evict_select, one CTA per (sequence, head): weights are mapped to unsigned
-// keys that order like them (NaN as -inf, -0 as +0), a radix select over four
-// 8-bit digits finds the smallest kept key and how many positions holding it
-// are kept (the lowest ones), and each warp writes the kept positions of its
-// run of the line, in order.
+// Weights are mapped to unsigned keys that order like them (NaN as -inf, -0 as
+// +0).  evict_pick, one cluster of CTAs per (sequence, head), reads each weight
+// once into a register: a radix select over four 8-bit digits (histograms with
+// a copy per lane residue, summed over the cluster) finds the smallest kept
+// key and how many positions holding it are kept (the lowest ones); then each
+// warp writes the kept positions, and their weights, of its run of the line, in
+// order.  Caches too long for a cluster's registers take evict_select, one CTA
+// that reads the weights from memory in every pass.
 // The gather: a plane is moved by one thread per word of a kept row when it
 // goes to another buffer; in place, a CTA takes a column slice of a (sequence,
 // head)'s rows and walks it in chunks, each read whole before it is written.
 // That is safe because kept[j] >= j, so a chunk's writes reach no position
-// that a later chunk still has to read.  The weights are one more plane.
+// that a later chunk still has to read.
 #include "kernels.h"
 #include "common.cuh"
 
@@ -20,7 +23,13 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kPickThreads = 512;
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickMost = 32;     // weights a thread holds
+constexpr int kCopies = 8;        // histogram copies
+constexpr int kMaxCluster = 16;
 constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 8;
 constexpr int kSweepUnroll = 4;
 constexpr int kMaxPlanes = 9;  // SPEC_EVICT_MAX_PLANES and the weights
 
@@ -134,72 +143,313 @@ __global__ void __launch_bounds__(kSelThreads)
   }
 }
 
+// The kept positions of one (sequence, head) and their weights.
+// weights_out may be weights: every weight is in a register before any is
+// written.
+template <int kPer>
+__global__ void __launch_bounds__(kPickThreads)
+    evict_pick(const float* weights, const int32_t* __restrict__ length, int Hkv, int S,
+               int budget, int recent, int64_t S_out, float* weights_out,
+               int32_t* __restrict__ kept, int32_t* __restrict__ new_len) {
+  launch_dependents();
+  __shared__ int hist[2][256];          // this CTA's, by pass parity (read by the cluster)
+  __shared__ int copies[256][kCopies];
+  __shared__ int total[256];
+  __shared__ int2 count_s;              // kept for sure, equal to the threshold (cluster)
+  __shared__ int2 wcount[kPickWarps];
+  __shared__ uint32_t prefix_s;
+  __shared__ int want_s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
+  const int64_t pair = blockIdx.x / C;
+  const int b = (int)(pair / Hkv), h = (int)(pair % Hkv);
+  const float* w = weights + pair * S;
+  float* wo = weights_out ? weights_out + pair * S_out : nullptr;
+  int32_t* kp = kept + pair * budget;
+  int len = length[b];
+  len = len < 0 ? 0 : (len > S ? S : len);
+  if (h == 0 && rank == 0 && threadIdx.x == 0) new_len[b] = min(len, budget);
+  if (len <= budget) {  // everything stays
+    for (int j = rank * kPickThreads + threadIdx.x; j < budget; j += C * kPickThreads) {
+      kp[j] = j < len ? j : -1;
+      if (wo && wo != w && j < len) wo[j] = w[j];
+    }
+    return;  // the whole cluster takes this way
+  }
+  const int m = len - recent;         // positions the weights decide about
+  const int need = budget - recent;   // of which this many stay
+  // this warp's run: positions lo + 32 k + lane, k < steps
+  const int steps = (len + C * kPickThreads - 1) / (C * kPickThreads);  // <= kPer
+  const int lo = ((rank * kPickWarps + warp) * steps) * 32 + lane;
+  float v[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k)
+    v[k] = k < steps && lo + 32 * k < len ? w[lo + 32 * k] : 0.f;
+
+  // radix select, most significant digit first: after digit d, `prefix` holds
+  // the top digits of the need-th largest key
+  uint32_t prefix = 0;
+  int want = need;  // how many of the keys that share the prefix are kept
+  for (int pass = 0; pass < 4 && need > 0; ++pass) {
+    const int shift = 24 - 8 * pass;
+    for (int i = threadIdx.x; i < 256 * kCopies; i += kPickThreads) (&copies[0][0])[i] = 0;
+    __syncthreads();
+    const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (k >= steps) break;
+      const uint32_t key = order_key(v[k]);
+      if (lo + 32 * k < m && (key & mask) == prefix)
+        atomicAdd(&copies[(key >> shift) & 255u][lane % kCopies], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      int sum = 0;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) sum += copies[threadIdx.x][(threadIdx.x + i) % kCopies];
+      (C > 1 ? hist[pass & 1] : total)[threadIdx.x] = sum;
+    }
+    if (C > 1) {
+      cluster_sync();
+      if (threadIdx.x < 256) {
+        const uint32_t at = smem_u32(&hist[pass & 1][threadIdx.x]);
+        int part[kMaxCluster];  // the loads in flight together
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          part[r] = r < C ? (int)ld_dsmem_u32(mapa(at, (uint32_t)r)) : 0;
+        int sum = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) sum += part[r];
+        total[threadIdx.x] = sum;
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // lane l holds digits 255 - 8 l .. 248 - 8 l, largest first
+      int cnt[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += cnt[i] = total[255 - 8 * lane - i];
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += u;
+      }
+      before -= sum;
+      if (before < want && want <= before + sum) {
+        int left = want - before;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (left > 0 && left <= cnt[i]) {
+            prefix_s = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
+            want_s = left;
+          }
+          left -= cnt[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix = prefix_s;
+    want = want_s;
+  }
+  if (need == 0) prefix = 0xffffffffu;  // above every key: nothing but the recent ones
+  // `want` of the positions whose key equals `prefix` are kept, lowest first
+  int sure = 0, eq = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (k >= steps) break;
+    const int i = lo + 32 * k;
+    const uint32_t key = order_key(v[k]);
+    sure += i < len && (i >= m || key > prefix) ? 1 : 0;
+    eq += i < m && key == prefix ? 1 : 0;
+  }
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) wcount[warp] = make_int2(sure, eq);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int2 t = make_int2(0, 0);
+    for (int x = 0; x < kPickWarps; ++x) {
+      t.x += wcount[x].x;
+      t.y += wcount[x].y;
+    }
+    count_s = t;
+  }
+  if (C > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  int at = 0, taken = 0;  // sure ones and equal ones before this warp's run
+  for (int r = 0; r < rank; ++r) {
+    const uint32_t a = mapa(smem_u32(&count_s), (uint32_t)r);
+    at += (int)ld_dsmem_u32(a);
+    taken += (int)ld_dsmem_u32(a + 4);
+  }
+  for (int x = 0; x < warp; ++x) {
+    at += wcount[x].x;
+    taken += wcount[x].y;
+  }
+  taken = min(taken, want);
+  at += taken;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (k >= steps) break;
+    const int i = lo + 32 * k;
+    const uint32_t key = order_key(v[k]);
+    const uint32_t eqm = __ballot_sync(0xffffffffu, i < m && key == prefix);
+    const bool on = i < len && (i >= m || key > prefix ||
+                                (key == prefix && taken + __popc(eqm & below) < want));
+    const uint32_t onm = __ballot_sync(0xffffffffu, on);
+    if (on) {
+      const int j = at + __popc(onm & below);
+      kp[j] = i;
+      if (wo) wo[j] = v[k];
+    }
+    at += __popc(onm);
+    taken = min(want, taken + __popc(eqm));
+  }
+  if (C > 1) cluster_sync();  // no CTA leaves while another reads its counts
+}
+
 struct MovePlane {
   const unsigned char* src;
   unsigned char* dst;
-  int words;  // words of this launch's width per row
+  int width;  // bytes of a word: 16, 8, 4 or 1
+  int words;  // words per row
 };
 struct MovePlanes {
   MovePlane p[kMaxPlanes];
 };
 
-// To another buffer: one thread per word of a kept row; blockIdx.y = plane.
+// A chunk of rows of one (sequence, head) to another buffer.
 template <typename W>
-__global__ void __launch_bounds__(kMoveThreads)
-    evict_gather(const MovePlanes planes, const int32_t* __restrict__ kept, int64_t rows,
-                 int budget, int64_t S, int64_t S_out) {
-  grid_dependency_wait();
-  const MovePlane pl = planes.p[blockIdx.y];
-  const int64_t total = rows * pl.words;
-  for (int64_t t = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; t < total;
-       t += (int64_t)gridDim.x * kMoveThreads) {
-    const int64_t r = t / pl.words;
-    const int w = (int)(t - r * pl.words);
-    const int from = kept[r];
-    if (from < 0) continue;
-    const int64_t pair = r / budget;
-    const int64_t j = r - pair * budget;
-    reinterpret_cast<W*>(pl.dst)[(pair * S_out + j) * pl.words + w] =
-        reinterpret_cast<const W*>(pl.src)[(pair * S + from) * pl.words + w];
+__device__ __forceinline__ void gather_rows(const MovePlane& pl, const int32_t* from, int rows,
+                                            const unsigned char* src0, unsigned char* dst0) {
+  const W* src = reinterpret_cast<const W*>(src0);
+  W* dst = reinterpret_cast<W*>(dst0);
+  const uint32_t words = (uint32_t)pl.words, total = (uint32_t)rows * words;
+  for (uint32_t t0 = threadIdx.x; t0 < total; t0 += kMoveThreads * kMoveUnroll) {
+    W v[kMoveUnroll];
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const uint32_t t = t0 + u * kMoveThreads;
+      if (t < total) {
+        const uint32_t r = t / words;
+        v[u] = src[(int64_t)from[r] * words + (t - r * words)];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const uint32_t t = t0 + u * kMoveThreads;
+      if (t < total) dst[t] = v[u];
+    }
   }
 }
-
-// In place: blockIdx.x = (sequence, head), blockIdx.y = plane, blockIdx.z = slice of
-// `width` words of the rows.
-template <typename W>
+// Rows a CTA moves: kMoveUnroll words a thread, and at least one row.
+__host__ __device__ constexpr int gather_chunk(int words) {
+  const int r = kMoveThreads * kMoveUnroll / words;
+  return r < 1 ? 1 : (r > kMoveThreads * 2 ? kMoveThreads * 2 : r);
+}
+// To another buffer: blockIdx.x = (sequence, head) x chunk, blockIdx.y = plane.
 __global__ void __launch_bounds__(kMoveThreads)
-    evict_sweep(const MovePlanes planes, const int32_t* __restrict__ kept, int budget, int64_t S,
-                int width) {
+    evict_gather(const MovePlanes planes, const int32_t* __restrict__ kept, int64_t pairs,
+                 int budget, int64_t S, int64_t S_out) {
+  __shared__ int32_t from[kMoveThreads * 2];
+  __shared__ int rows_s;
   grid_dependency_wait();
   const MovePlane pl = planes.p[blockIdx.y];
-  const int w0 = blockIdx.z * width;
-  const int nw = min(width, pl.words - w0);
+  const int chunk = gather_chunk(pl.words);
+  const int chunks = (budget + chunk - 1) / chunk;
+  const int64_t pair = blockIdx.x / chunks;
+  if (pair >= pairs) return;
+  const int j0 = (int)(blockIdx.x % chunks) * chunk;
+  const int most = min(chunk, budget - j0);
+  if (threadIdx.x == 0) rows_s = 0;
+  __syncthreads();
+  int mine = 0;
+  for (int j = threadIdx.x; j < most; j += kMoveThreads) {
+    const int f = kept[pair * budget + j0 + j];
+    from[j] = f;
+    mine += f >= 0;
+  }
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&rows_s, mine);  // kept rows come first
+  __syncthreads();
+  const int64_t row = (int64_t)pl.width * pl.words;
+  const unsigned char* src = pl.src + pair * S * row;
+  unsigned char* dst = pl.dst + (pair * S_out + j0) * row;
+  if (pl.width == 16)
+    gather_rows<uint4>(pl, from, rows_s, src, dst);
+  else if (pl.width == 8)
+    gather_rows<uint2>(pl, from, rows_s, src, dst);
+  else if (pl.width == 4)
+    gather_rows<uint32_t>(pl, from, rows_s, src, dst);
+  else
+    gather_rows<unsigned char>(pl, from, rows_s, src, dst);
+}
+
+// A slice of words w0 .. w0 + nw - 1 of one (sequence, head)'s rows, in place.
+template <typename W>
+__device__ __forceinline__ void sweep_rows(const MovePlane& pl, const int32_t* __restrict__ kp,
+                                           int budget, unsigned char* base0, int w0, int nw) {
+  W* base = reinterpret_cast<W*>(base0) + w0;
+  // thread t takes word t % nw of rows t / nw, + 256 / nw, ... of a chunk
+  const int rows = kMoveThreads / nw;
+  const int tr = threadIdx.x / nw, tw = threadIdx.x % nw;
+  W v[2][kSweepUnroll];
+  bool move[2][kSweepUnroll];
+  auto read = [&](int c, W (&x)[kSweepUnroll], bool (&mv)[kSweepUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kSweepUnroll; ++u) {
+      const int j = (c * kSweepUnroll + u) * rows + tr;
+      const int from = tr < rows && j < budget ? kp[j] : -1;
+      mv[u] = from >= 0 && from != j;
+      if (mv[u]) x[u] = base[(int64_t)from * pl.words + tw];
+    }
+  };
+  auto write = [&](int c, const W (&x)[kSweepUnroll], const bool (&mv)[kSweepUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kSweepUnroll; ++u)
+      if (mv[u]) base[(int64_t)((c * kSweepUnroll + u) * rows + tr) * pl.words + tw] = x[u];
+  };
+  // chunk c + 1 is read before chunk c is written: its sources lie above every
+  // position written until then
+  const int chunks = (budget + rows * kSweepUnroll - 1) / (rows * kSweepUnroll);
+  read(0, v[0], move[0]);
+  for (int c = 0; c < chunks; c += 2) {
+    if (c + 1 < chunks) read(c + 1, v[1], move[1]);
+    __syncthreads();  // chunk c is read whole
+    write(c, v[0], move[0]);
+    if (c + 1 >= chunks) break;
+    if (c + 2 < chunks) read(c + 2, v[0], move[0]);
+    __syncthreads();
+    write(c + 1, v[1], move[1]);
+  }
+}
+// In place: blockIdx.x = (sequence, head), blockIdx.y = plane, blockIdx.z = slice of
+// at most 32 bytes of the rows.
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_sweep(const MovePlanes planes, const int32_t* __restrict__ kept, int budget, int64_t S) {
+  grid_dependency_wait();
+  const MovePlane pl = planes.p[blockIdx.y];
+  const int per = pl.width == 1 ? 32 : 32 / pl.width;
+  const int w0 = blockIdx.z * per;
+  const int nw = min(per, pl.words - w0);
   if (nw <= 0) return;
   const int64_t pair = blockIdx.x;
   const int32_t* kp = kept + pair * budget;
-  W* base = reinterpret_cast<W*>(pl.dst) + pair * S * pl.words + w0;
-  // rows of this chunk: thread t takes word t % nw of rows t / nw, + 256 / nw, ...
-  const int rows = kMoveThreads / nw;
-  const int tr = threadIdx.x / nw, tw = threadIdx.x % nw;
-  for (int j0 = 0; j0 < budget; j0 += rows * kSweepUnroll) {
-    W v[kSweepUnroll];
-    int from[kSweepUnroll];
-#pragma unroll
-    for (int u = 0; u < kSweepUnroll; ++u) {
-      const int j = j0 + u * rows + tr;
-      from[u] = tr < rows && j < budget ? kp[j] : -1;
-      if (from[u] == j) from[u] = -1;  // already in place
-      if (from[u] >= 0) v[u] = base[(int64_t)from[u] * pl.words + tw];
-    }
-    __syncthreads();  // the chunk is read before any of it is written
-#pragma unroll
-    for (int u = 0; u < kSweepUnroll; ++u)
-      if (from[u] >= 0) base[(int64_t)(j0 + u * rows + tr) * pl.words + tw] = v[u];
-    // the next chunk's sources lie above every position written so far
-  }
+  unsigned char* base = pl.dst + pair * S * ((int64_t)pl.width * pl.words);
+  if (pl.width == 16)
+    sweep_rows<uint4>(pl, kp, budget, base, w0, nw);
+  else if (pl.width == 8)
+    sweep_rows<uint2>(pl, kp, budget, base, w0, nw);
+  else if (pl.width == 4)
+    sweep_rows<uint32_t>(pl, kp, budget, base, w0, nw);
+  else
+    sweep_rows<unsigned char>(pl, kp, budget, base, w0, nw);
 }
 
-template <typename W>
 cudaError_t launch_moves(const MovePlanes& out, int n_out, const MovePlanes& in, int n_in,
                          const int32_t* kept, int64_t pairs, int budget, int S, int S_out,
                          cudaStream_t st) {
@@ -213,23 +463,39 @@ cudaError_t launch_moves(const MovePlanes& out, int n_out, const MovePlanes& in,
   cfg.numAttrs = 1;
   cudaError_t e = cudaSuccess;
   if (n_out > 0) {
-    int most = 0;
-    for (int i = 0; i < n_out; ++i) most = most > out.p[i].words ? most : out.p[i].words;
-    const int64_t want = (pairs * budget * most + kMoveThreads - 1) / kMoveThreads;
-    const int64_t cap = 152 * 64;
-    cfg.gridDim = dim3((unsigned)(want < cap ? want : cap), (unsigned)n_out);
-    e = cudaLaunchKernelEx(&cfg, evict_gather<W>, out, kept, pairs * budget, budget, (int64_t)S,
+    int64_t most = 0;
+    for (int i = 0; i < n_out; ++i) {
+      const int chunk = gather_chunk(out.p[i].words);
+      const int64_t c = pairs * ((budget + chunk - 1) / chunk);
+      most = most > c ? most : c;
+    }
+    if (most > 2147483647) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3((unsigned)most, (unsigned)n_out);
+    e = cudaLaunchKernelEx(&cfg, evict_gather, out, kept, pairs, budget, (int64_t)S,
                            (int64_t)S_out);
     if (e != cudaSuccess) return e;
   }
   if (n_in > 0) {
-    int most = 0;
-    for (int i = 0; i < n_in; ++i) most = most > in.p[i].words ? most : in.p[i].words;
-    const int width = (int)(32 / sizeof(W));  // a 32-byte sector's words (rows: at most 65536 bytes)
-    cfg.gridDim = dim3((unsigned)pairs, (unsigned)n_in, (unsigned)((most + width - 1) / width));
-    e = cudaLaunchKernelEx(&cfg, evict_sweep<W>, in, kept, budget, (int64_t)S, width);
+    int most = 0;  // slices; rows have at most 65536 bytes
+    for (int i = 0; i < n_in; ++i) {
+      const int c = (in.p[i].width * in.p[i].words + 31) / 32;
+      most = most > c ? most : c;
+    }
+    cfg.gridDim = dim3((unsigned)pairs, (unsigned)n_in, (unsigned)most);
+    e = cudaLaunchKernelEx(&cfg, evict_sweep, in, kept, budget, (int64_t)S);
   }
   return e;
+}
+
+// CTAs per cluster of evict_pick for caches of S positions, or 0 (evict_select):
+// enough registers for the weights, and more CTAs, of at least 2048 weights
+// each, when there are few (sequence, head) pairs.
+int pick_cluster(int64_t pairs, int S) {
+  int C = 1;
+  while ((int64_t)C * kPickThreads * kPickMost < S && C < kMaxCluster) C *= 2;
+  if ((int64_t)C * kPickThreads * kPickMost < S) return 0;
+  while (C < 8 && pairs * C * 2 <= 152 && S / (2 * C) >= 2048) C *= 2;
+  return C;
 }
 
 }  // namespace
@@ -262,37 +528,51 @@ extern "C" int spec_kv_evict(const float* weights, const int32_t* length, int B,
   if (weights_out == weights && S_out != S) return SPEC_ERR_ARG;
   const int64_t pairs = (int64_t)B * Hkv;
   cudaStream_t st = (cudaStream_t)stream;
-  evict_select<<<(unsigned)pairs, kSelThreads, 0, st>>>(weights, length, Hkv, S, budget, recent,
-                                                        kept, new_len);
-  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
-  // planes by word width (16, 4 or 1 bytes), to another buffer or in place
-  MovePlanes out[3], in[3];
-  int n_out[3] = {0, 0, 0}, n_in[3] = {0, 0, 0};
-  const int width[3] = {16, 4, 1};
+  const int C = pick_cluster(pairs, S);
+  cudaError_t e;
+  if (C > 0 && pairs * C <= 2147483647) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(pairs * C));
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)C;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const int64_t per = (S + (int64_t)C * kPickThreads - 1) / ((int64_t)C * kPickThreads);
+    if (C > 8) {  // more than the portable cluster size
+      e = cudaFuncSetAttribute(evict_pick<kPickMost>, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                               1);
+      if (e != cudaSuccess) return SPEC_ERR_CUDA;
+    }
+    e = cudaLaunchKernelEx(&cfg, per <= 8 ? evict_pick<8> : (per <= 16 ? evict_pick<16> : evict_pick<kPickMost>),
+                           weights, length, Hkv,
+                           S, budget, recent, (int64_t)S_out, weights_out, kept, new_len);
+  } else {
+    evict_select<<<(unsigned)pairs, kSelThreads, 0, st>>>(weights, length, Hkv, S, budget, recent,
+                                                          kept, new_len);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return SPEC_ERR_CUDA;
+  // planes to another buffer and in place; the widest word that fits each
+  MovePlanes out, in;
+  int n_out = 0, n_in = 0;
   for (int i = 0; i <= n_planes; ++i) {
     const bool is_w = i == n_planes;
-    if (is_w && !weights_out) break;
+    if (is_w && (!weights_out || C > 0)) break;  // evict_pick has moved them
     const void* s = is_w ? (const void*)weights : planes[i];
     void* d = is_w ? (void*)weights_out : planes_out[i];
     const int bytes = is_w ? 4 : row_bytes[i];
     const uint64_t al = (uint64_t)(uintptr_t)s | (uint64_t)(uintptr_t)d | (uint64_t)bytes;
-    const int c = al % 16 == 0 ? 0 : (al % 4 == 0 ? 1 : 2);
-    const MovePlane pl = {(const unsigned char*)s, (unsigned char*)d, bytes / width[c]};
+    const int width = al % 16 == 0 ? 16 : (al % 8 == 0 ? 8 : (al % 4 == 0 ? 4 : 1));
+    const MovePlane pl = {(const unsigned char*)s, (unsigned char*)d, width, bytes / width};
     if (s == d)
-      in[c].p[n_in[c]++] = pl;
+      in.p[n_in++] = pl;
     else
-      out[c].p[n_out[c]++] = pl;
+      out.p[n_out++] = pl;
   }
-  cudaError_t e = cudaSuccess;
-  for (int c = 0; c < 3 && e == cudaSuccess; ++c) {
-    if (c == 0)
-      e = launch_moves<uint4>(out[c], n_out[c], in[c], n_in[c], kept, pairs, budget, S, S_out, st);
-    else if (c == 1)
-      e = launch_moves<uint32_t>(out[c], n_out[c], in[c], n_in[c], kept, pairs, budget, S, S_out,
-                                 st);
-    else
-      e = launch_moves<unsigned char>(out[c], n_out[c], in[c], n_in[c], kept, pairs, budget, S,
-                                      S_out, st);
-  }
+  e = launch_moves(out, n_out, in, n_in, kept, pairs, budget, S, S_out, st);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -9,25 +9,33 @@
 // keys suffices and no value row is read: the bound is the keys' bytes plus
 // eight bytes per position for in and out.
 //
-// A warp takes 32 keys: m16n8k16 products of the accepted rows (16 at a time,
-// fragments of q in shared memory) with the keys as the 8-wide operand, then
-// the column sums of the exponentials.  Keys are read straight from global
-// memory into operand registers (a 4-bit row's quarter, or the 16-byte chunks
-// c, c + 4, ... of a bf16 row, per lane (g, c)); the k index is a permutation of the head dims
-// that q shares.  Column 2 c + x of tile t is key 8 t + 4 x + c, so that the
-// sums end up in lane = key order.  Every position belongs to one warp and its
-// sum has a fixed order: no atomics.
+// A warp takes 32 keys: m16n8k16 products with the keys as the 16-row operand
+// and eight accepted rows (fragments of q in shared memory) as the other, then
+// the sums of the exponentials over the rows, most of them in registers.  Lane
+// (g, c) takes a quarter of key g's 4-bit row, or the 16-byte chunks c, c + 4,
+// ... of its bf16 row; the k index is a permutation of the head dims that q
+// shares.  bf16 keys go from global memory straight into operand registers
+// (8 KB a warp in flight); 4-bit keys are too small for that (2 KB), so each
+// warp keeps a ring of cp.async stages.  Every position belongs to one warp and
+// its sum has a fixed order: no atomics.
+// Work: the 256-key blocks (32 keys a warp) of all (sequence, head) pairs form
+// one line, cut into equal pieces, one per resident CTA.
+#include <type_traits>
+
 #include "kernels.h"
 #include "kv4.cuh"
+#include "line.cuh"
 
 namespace sv {
 namespace {
 
 constexpr int kWtWarps = 8;
 constexpr int kWtThreads = kWtWarps * 32;
-constexpr int kWtIters = 4;                            // 32-key blocks per warp
-constexpr int kWtKeys = kWtWarps * 32 * kWtIters;      // keys per CTA
-constexpr int kWtRows = 64;                            // query rows staged at a time
+constexpr int kWtKeys = kWtWarps * 32;  // keys of a CTA's iteration
+constexpr int kWtCtas = 2;              // per SM
+constexpr int kWtStages = 5;            // 32-key stages of a warp's ring (4-bit keys)
+constexpr int kWtRows = 64;             // query rows staged at a time
+constexpr int kWtNodes = 64;            // most accepted nodes (N)
 
 struct WeightParams {
   const uint16_t* q;
@@ -35,132 +43,217 @@ struct WeightParams {
   const uint8_t* ks;
   const float* lse;
   const int32_t *prefix_len, *path_len, *path_nodes;
-  int N, Hq, Hkv, S;
+  int B, N, Hq, Hkv, S;
   float scale_log2;
   const float* in;
   float* out;
 };
 
+__device__ __forceinline__ int wt_prefix(const WeightParams& p, int b) {
+  const int P = p.prefix_len[b];
+  return P < 0 ? 0 : (P > p.S - p.N ? p.S - p.N : P);
+}
+// 256-key blocks of sequence b, all heads (an invalid path is found later: it
+// may leave the last block empty).
+struct WeightBlocks {
+  const WeightParams& p;
+  __device__ __forceinline__ int64_t operator()(int b) const {
+    const int n = p.path_len[b];
+    const int L = wt_prefix(p, b) + (n < 0 || n > p.N ? 0 : n);
+    return (int64_t)((L + kWtKeys - 1) / kWtKeys) * p.Hkv;
+  }
+};
+
 template <int D, bool kKv4>
-__global__ void __launch_bounds__(kWtThreads, 2) kv_weights(const WeightParams p) {
+struct WtSmem {
+  static constexpr int kCodes = 32 * (D / 2), kStage = kCodes + 32 * (D / 16);
+  unsigned char ring[kKv4 ? kWtWarps * kWtStages * kStage : 16];
+  uint2 qf[kWtRows / 8][D / 16][32];  // operand registers b0, b1 per lane
+  float rowf[kWtRows], rowl[kWtRows];
+  int rowt[kWtRows], nodes[kWtNodes];
+  int64_t line[kWtThreads + 1], tmp[kWtWarps];
+};
+
+template <int D, bool kKv4>
+__global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightParams p) {
   constexpr int kSteps = D / 16;
-  __shared__ uint4 qf[kWtRows / 16][kSteps][32];  // a0 a2 a1 a3 per lane
-  __shared__ float rowf[kWtRows], rowl[kWtRows];
-  __shared__ int rowt[kWtRows];
-  __shared__ int bad;
+  using Sm = WtSmem<D, kKv4>;
+  extern __shared__ __align__(16) unsigned char raw_s[];
+  Sm& sm = *reinterpret_cast<Sm*>(raw_s);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int b = blockIdx.z, kvh = blockIdx.y;
-  const int64_t row0 = ((int64_t)b * p.Hkv + kvh) * p.S;
-  int P = p.prefix_len[b];
-  P = P < 0 ? 0 : (P > p.S - p.N ? p.S - p.N : P);
-  int n = p.path_len[b];
-  const int first = blockIdx.x * kWtKeys;
-  if (first >= P + p.N) return;
-  // an invalid path adds nothing
-  if (threadIdx.x == 0) bad = n < 0 || n > p.N;
-  __syncthreads();
-  if (!bad && p.path_nodes && threadIdx.x < n) {
-    const int v = p.path_nodes[(int64_t)b * p.N + threadIdx.x];
-    if (v < 0 || v >= p.N) bad = 1;
-  }
-  __syncthreads();
-  if (bad) n = 0;
-  const int L = P + n;
-  if (first >= L) return;
   const int Gq = p.Hq / p.Hkv;
-  const int R = n * Gq;
-  const int groups = (R + kWtRows - 1) / kWtRows;
-  const float* in = p.in ? p.in + row0 : nullptr;
-  float* out = p.out + row0;
+  const WeightBlocks blocks = {p};
+  scan_line<kWtThreads>(p.B, blocks, sm.line, sm.tmp);
+  const int64_t total = sm.line[kWtThreads];
+  const int64_t piece = (total + gridDim.x - 1) / gridDim.x;
+  int64_t line_at = (int64_t)blockIdx.x * piece;
+  const int64_t line_end = min(total, line_at + piece);
+  if (line_at >= total) return;
+  int64_t seq_start;
+  int b = locate<kWtThreads>(p.B, blocks, sm.line, line_at, &seq_start);
 
-  auto stage = [&](int grp) {
-    for (int i = warp; i < kWtRows; i += kWtWarps) {
-      const int r = grp * kWtRows + i;
-      if (i >= ((min(R - grp * kWtRows, kWtRows) + 15) & ~15)) break;
-      const bool valid = r < R;
-      const int t = valid ? r / Gq : 0;
-      const int hq = kvh * Gq + (valid ? r % Gq : 0);
-      const int node = valid && p.path_nodes ? p.path_nodes[(int64_t)b * p.N + t] : t;
-      const int64_t qrow = ((int64_t)b * p.N + node) * p.Hq + hq;
-      uint2 w = make_uint2(0, 0);
-      if (valid && lane < D / 4) w = *reinterpret_cast<const uint2*>(p.q + qrow * D + 4 * lane);
-      float up = 1.f;
-      uint32_t h0 = w.x, h1 = w.y;
-      int s, cc;
-      if constexpr (kKv4) {
-        // scaled by a power of two to [1, 2): exact in fp16 (see kv4_attn.cu)
-        const float x0 = bf16_lo(w.x), x1 = bf16_hi(w.x), x2 = bf16_lo(w.y), x3 = bf16_hi(w.y);
-        const float mx =
-            warp_max(fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3))));
-        int e = (int)(__float_as_uint(mx) >> 23) - 127;
-        if (mx == 0.f || e == 128) e = 0;
-        e = max(-126, min(126, e));
-        const float dn = __uint_as_float((uint32_t)(127 - e) << 23);
-        up = __uint_as_float((uint32_t)(127 + e) << 23);
-        h0 = pack_half2(x0 * dn, x1 * dn);
-        h1 = pack_half2(x2 * dn, x3 * dn);
-        cc = lane / (D / 16);
-        s = lane % (D / 16);
-      } else {
-        cc = (lane >> 1) & 3;
-        s = 2 * (lane >> 3) + (lane & 1);
+  while (line_at < line_end) {
+    const int64_t seq_blocks = blocks(b);
+    if (seq_blocks == 0) {  // nothing in this sequence
+      ++b;
+      continue;
+    }
+    // ---- the piece's share of one head's keys: first .. last
+    const int per_head = (int)(seq_blocks / p.Hkv);
+    const int kvh = (int)((line_at - seq_start) / per_head);
+    const int64_t head_start = seq_start + (int64_t)kvh * per_head;
+    const int k0 = (int)(line_at - head_start);
+    const int k1 = (int)min((int64_t)per_head, line_end - head_start);
+    const int64_t row0 = ((int64_t)b * p.Hkv + kvh) * p.S;
+    const int P = wt_prefix(p, b);
+    int n = p.path_len[b];
+    int node = threadIdx.x;
+    if (p.path_nodes && threadIdx.x < p.N) node = p.path_nodes[(int64_t)b * p.N + threadIdx.x];
+    if (threadIdx.x < kWtNodes) sm.nodes[threadIdx.x] = node;
+    // an invalid path adds nothing
+    const bool bad = n < 0 || n > p.N || ((int)threadIdx.x < n && (node < 0 || node >= p.N));
+    if (__syncthreads_or(bad)) n = 0;
+    const int L = P + n;
+    const int R = n * Gq;
+    const int groups = (R + kWtRows - 1) / kWtRows;
+    const float* in = p.in ? p.in + row0 : nullptr;
+    float* out = p.out + row0;
+    const int first = k0 * kWtKeys, last = min(L, k1 * kWtKeys);
+
+    // a stage of this warp's ring: 32 keys' codes, then their scales; keys behind
+    // the sequence are zeros, not read
+    const uint32_t ring = smem_u32(sm.ring) + (uint32_t)(warp * kWtStages * Sm::kStage);
+    auto fill = [&](int key0, int slot) {
+      constexpr int kChunks = D / 32;  // 16-byte chunks per key
+      const uint32_t st = ring + (uint32_t)(slot * Sm::kStage);
+      const uint8_t* codes = (const uint8_t*)p.k + (row0 + key0) * (D / 2) + lane * 16;
+      const uint8_t* scales = p.ks + (row0 + key0 + lane) * (D / 16);
+#pragma unroll
+      for (int r = 0; r < kChunks; ++r) {
+        const bool take = key0 + (r * 32 + lane) / kChunks < L;
+        cp_async_or_zero<16>(st + (uint32_t)(r * 512 + lane * 16),
+                             take ? codes + r * 512 : (const uint8_t*)p.k, take);
       }
-      if (lane < D / 4) {
-        uint32_t* dst = reinterpret_cast<uint32_t*>(&qf[i >> 4][s][4 * (i & 7) + cc]);
-        dst[(i & 8) ? 2 : 0] = h0;
-        dst[(i & 8) ? 3 : 1] = h1;
-      }
-      if (lane == 0) {
-        float l = valid ? p.lse[qrow] : neg_inf();
-        if (l == neg_inf()) l = -neg_inf();  // a row that saw nothing weighs nothing
-        rowf[i] = p.scale_log2 * up;
-        rowl[i] = l;
-        rowt[i] = valid ? P + t : -1;
+      const bool take = key0 + lane < L;
+      cp_async_or_zero<D / 16>(st + (uint32_t)(Sm::kCodes + lane * (D / 16)),
+                               take ? scales : p.ks, take);
+    };
+    if constexpr (kKv4) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kWtStages - 1; ++i) {
+        const int k = first + warp * 32 + i * kWtKeys;
+        if (k < last) fill(k, i);
+        cp_async_commit();
       }
     }
-  };
-  if (groups == 1) stage(0);
-  __syncthreads();
 
-  for (int it = 0; it < kWtIters; ++it) {
-    const int key0 = first + (it * kWtWarps + warp) * 32;
-    const bool live = key0 < L && groups > 0;
-    // the 32 keys' operand fragments: [tile][k step][b0, b1]
-    uint32_t kb[4][kSteps][2];
-    if (live) {
+    // the accepted rows of q as operand fragments, their scales, normalisers and
+    // last visible positions; every warp takes rows warp, warp + 8, ...
+    auto stage = [&](int grp) {
+      constexpr int kMine = kWtRows / kWtWarps;
+      const int rows = (min(R - grp * kWtRows, kWtRows) + 7) & ~7;
+      uint2 w[kMine];
+      float l[kMine];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int key = key0 + 8 * t + 4 * (g & 1) + (g >> 1);
-        const bool have = key < L;
-        const int64_t kr = row0 + (have ? key : key0);
+      for (int x = 0; x < kMine; ++x) {
+        const int i = warp + kWtWarps * x, r = grp * kWtRows + i;
+        w[x] = make_uint2(0, 0);
+        l[x] = neg_inf();
+        if (i < rows && r < R) {
+          const int t = r / Gq;
+          const int64_t qrow = ((int64_t)b * p.N + sm.nodes[t]) * p.Hq + kvh * Gq + (r - t * Gq);
+          if (lane < D / 4) w[x] = *reinterpret_cast<const uint2*>(p.q + qrow * D + 4 * lane);
+          l[x] = p.lse[qrow];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        const int i = warp + kWtWarps * x, r = grp * kWtRows + i;
+        if (i >= rows) break;
+        float up = 1.f;
+        uint32_t h0 = w[x].x, h1 = w[x].y;
+        int s, cc;
         if constexpr (kKv4) {
-          constexpr int kW = D / 32;
-          uint32_t w[kW];
-          uint32_t sc = 0;
-          const uint8_t* src = (const uint8_t*)p.k + kr * (D / 2) + 4 * kW * c;
-          if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src);
-            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-            sc = *reinterpret_cast<const uint16_t*>(p.ks + kr * (D / 16) + 2 * c);
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            w[0] = v.x; w[1] = v.y;
-            sc = p.ks[kr * (D / 16) + c];
-          }
-          const uint32_t s2 = e4m3x2_to_half2(sc);
-#pragma unroll
-          for (int x = 0; x < kW; ++x) {
-            uint32_t h[4];
-            e2m1x8_to_half2(w[x], h);
-            const uint32_t s1 = (D == 128 && x >= 2) ? dup_hi(s2) : dup_lo(s2);
-            kb[t][2 * x][0] = hmul2(h[0], s1);
-            kb[t][2 * x][1] = hmul2(h[1], s1);
-            kb[t][2 * x + 1][0] = hmul2(h[2], s1);
-            kb[t][2 * x + 1][1] = hmul2(h[3], s1);
-          }
+          // scaled by a power of two to [1, 2): exact in fp16 (see kv4_attn.cu)
+          const float x0 = bf16_lo(h0), x1 = bf16_hi(h0), x2 = bf16_lo(h1), x3 = bf16_hi(h1);
+          const float mx =
+              warp_max(fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3))));
+          int e = (int)(__float_as_uint(mx) >> 23) - 127;
+          if (mx == 0.f || e == 128) e = 0;
+          e = max(-126, min(126, e));
+          const float dn = __uint_as_float((uint32_t)(127 - e) << 23);
+          up = __uint_as_float((uint32_t)(127 + e) << 23);
+          h0 = pack_half2(x0 * dn, x1 * dn);
+          h1 = pack_half2(x2 * dn, x3 * dn);
+          cc = lane / (D / 16);
+          s = lane % (D / 16);
         } else {
-          const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.k + kr * D) + c;
+          cc = (lane >> 1) & 3;
+          s = 2 * (lane >> 3) + (lane & 1);
+        }
+        if (lane < D / 4) sm.qf[i >> 3][s][4 * (i & 7) + cc] = make_uint2(h0, h1);
+        if (lane == 0) {
+          sm.rowf[i] = p.scale_log2 * up;
+          sm.rowl[i] = l[x] == neg_inf() ? -l[x] : l[x];  // a row that saw nothing weighs nothing
+          sm.rowt[i] = r < R ? P + r / Gq : -1;
+        }
+      }
+    };
+    if (groups == 1) stage(0);
+    __syncthreads();
+
+    int slot = 0;
+    for (int at = first; at < last; at += kWtKeys) {
+      const int key0 = at + warp * 32;
+      const bool live = key0 < L && groups > 0;
+      const int key = key0 + 8 * c + g;  // the one this lane writes
+      const float before = in && key < P ? in[key] : 0.f;
+      // the 32 keys' operand fragments: [8 keys][k step][a0 / a1, a2 / a3]
+      uint32_t kb[4][kSteps][2];
+      if constexpr (kKv4) {
+        cp_async_wait<kWtStages - 2>();
+        __syncwarp();
+        const int next = key0 + (kWtStages - 1) * kWtKeys;
+        if (next < last) fill(next, slot == 0 ? kWtStages - 1 : slot - 1);
+        cp_async_commit();
+        const unsigned char* st = sm.ring + (warp * kWtStages + slot) * Sm::kStage;
+        slot = slot == kWtStages - 1 ? 0 : slot + 1;
+        if (live) {
+          constexpr int kW = D / 32;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const unsigned char* kr = st + (8 * t + g) * (D / 2) + 4 * kW * c;
+            const unsigned char* sr = st + Sm::kCodes + (8 * t + g) * (D / 16);
+            uint32_t w[kW], s2;
+            if constexpr (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kr);
+              w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+              s2 = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sr + 2 * c));
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(kr);
+              w[0] = v.x; w[1] = v.y;
+              s2 = e4m3x2_to_half2(sr[c]);
+            }
+#pragma unroll
+            for (int x = 0; x < kW; ++x) {
+              uint32_t h[4];
+              e2m1x8_to_half2(w[x], h);
+              const uint32_t s1 = (D == 128 && x >= 2) ? dup_hi(s2) : dup_lo(s2);
+              kb[t][2 * x][0] = hmul2(h[0], s1);
+              kb[t][2 * x][1] = hmul2(h[1], s1);
+              kb[t][2 * x + 1][0] = hmul2(h[2], s1);
+              kb[t][2 * x + 1][1] = hmul2(h[3], s1);
+            }
+          }
+        }
+      } else if (live) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int kk = key0 + 8 * t + g;
+          const uint4* src = reinterpret_cast<const uint4*>(
+                                 (const uint16_t*)p.k + (row0 + (kk < L ? kk : key0)) * D) + c;
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {
             const uint4 v = src[4 * x];
@@ -171,61 +264,92 @@ __global__ void __launch_bounds__(kWtThreads, 2) kv_weights(const WeightParams p
           }
         }
       }
-    }
-    float col[4][2] = {};
-    for (int grp = 0; grp < groups; ++grp) {
-      if (groups > 1) {
-        __syncthreads();
-        stage(grp);
-        __syncthreads();
-      }
-      const int tiles = (min(R - grp * kWtRows, kWtRows) + 15) / 16;
-      if (live) {
-        for (int mt = 0; mt < tiles; ++mt) {
-          float s[4][4] = {};
+      float2 col[4] = {};  // keys 8 t + g, summed over this lane's even and odd rows
+      for (int grp = 0; grp < groups; ++grp) {
+        if (groups > 1) {
+          __syncthreads();
+          stage(grp);
+          __syncthreads();
+        }
+        const int tiles = (min(R - grp * kWtRows, kWtRows) + 7) / 8;
+        if (live) {
+          // kTiles row tiles from nt on
+          auto tiles_of = [&](auto count, int nt) {
+            constexpr int kTiles = decltype(count)::value;
+            float s[kTiles][2][4] = {};
 #pragma unroll
-          for (int x = 0; x < kSteps; ++x) {
-            const uint4 a = qf[mt][x][lane];
+            for (int x = 0; x < kSteps; ++x)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              if constexpr (kKv4)
-                mma16816_f16(s[t], a.x, a.z, a.y, a.w, kb[t][x][0], kb[t][x][1]);
-              else
-                mma16816_bf16(s[t], a.x, a.z, a.y, a.w, kb[t][x][0], kb[t][x][1]);
-            }
-          }
+              for (int y = 0; y < kTiles; ++y) {
+                const uint2 q = sm.qf[nt + y][x][lane];
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const int i = mt * 16 + hf * 8 + g;
-            const float f = rowf[i], l = rowl[i];
-            const int lim = rowt[i];
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const float w = ex2(fmaf(s[t][2 * hf + x], f, -l));
-                col[t][x] += key0 + 8 * t + 4 * x + c <= lim ? w : 0.f;
+                for (int u = 0; u < 2; ++u) {
+                  if constexpr (kKv4)
+                    mma16816_f16(s[y][u], kb[2 * u][x][0], kb[2 * u + 1][x][0], kb[2 * u][x][1],
+                                 kb[2 * u + 1][x][1], q.x, q.y);
+                  else
+                    mma16816_bf16(s[y][u], kb[2 * u][x][0], kb[2 * u + 1][x][0], kb[2 * u][x][1],
+                                  kb[2 * u + 1][x][1], q.x, q.y);
+                }
               }
-          }
+#pragma unroll
+            for (int y = 0; y < kTiles; ++y) {
+              const int i = (nt + y) * 8 + 2 * c;  // this lane's rows i, i + 1
+              const float2 f = *reinterpret_cast<const float2*>(&sm.rowf[i]);
+              const float2 l = *reinterpret_cast<const float2*>(&sm.rowl[i]);
+              const int2 lim = *reinterpret_cast<const int2*>(&sm.rowt[i]);
+              const bool whole = key0 + 31 <= P && (nt + y) * 8 + 8 <= R - grp * kWtRows;
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                const float2 e = ffma2(
+                    make_float2(s[y][t >> 1][2 * (t & 1)], s[y][t >> 1][2 * (t & 1) + 1]), f,
+                    make_float2(-l.x, -l.y));
+                float2 w = make_float2(ex2(e.x), ex2(e.y));
+                if (!whole) {
+                  const int k = key0 + 8 * t + g;
+                  if (k > lim.x) w.x = 0.f;
+                  if (k > lim.y) w.y = 0.f;
+                }
+                col[t] = fadd2(col[t], w);
+              }
+            }
+          };
+          int nt = 0;  // pairs of tiles: four independent chains of products
+          for (; nt + 1 < tiles; nt += 2) tiles_of(std::integral_constant<int, 2>(), nt);
+          if (nt < tiles) tiles_of(std::integral_constant<int, 1>(), nt);
         }
       }
-    }
-    if (key0 < L) {
-      float mine = 0.f;
+      if (key0 < L) {
+        float mine = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float v = col[t][x];
-          v += __shfl_xor_sync(0xffffffffu, v, 4);
-          v += __shfl_xor_sync(0xffffffffu, v, 8);
-          v += __shfl_xor_sync(0xffffffffu, v, 16);
-          if (g == 2 * t + x) mine = v;
+        for (int t = 0; t < 4; ++t) {
+          float v = col[t].x + col[t].y;
+          v += __shfl_xor_sync(0xffffffffu, v, 1);
+          v += __shfl_xor_sync(0xffffffffu, v, 2);
+          if (c == t) mine = v;
         }
-      const int key = key0 + lane;  // 8 t + 4 x + c with g = 2 t + x
-      if (key < L) out[key] = (in && key < P ? in[key] : 0.f) + mine;
+        if (key < L) out[key] = before + mine;
+      }
+    }
+    if constexpr (kKv4) cp_async_wait<0>();
+    __syncthreads();  // the next share stages its own rows
+    line_at = head_start + k1;
+    if (line_at == seq_start + seq_blocks) {
+      seq_start = line_at;
+      ++b;
     }
   }
+}
+
+template <int D, bool kKv4>
+cudaError_t launch_weights(const WeightParams& p, int grid, cudaStream_t st) {
+  constexpr int smem = (int)sizeof(WtSmem<D, kKv4>);
+  static_assert((smem + 1024) * kWtCtas <= 228 * 1024, "the pieces are resident at once");
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem((const void*)kv_weights<D, kKv4>, smem, done);
+  if (e != cudaSuccess) return e;
+  kv_weights<D, kKv4><<<grid, kWtThreads, smem, st>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -267,18 +391,15 @@ extern "C" int spec_kv_weights(const void* q, const void* k, const uint8_t* k_sc
   p.scale_log2 = scale * kLog2e * k_unit;
   p.in = weights;
   p.out = out;
-  const dim3 grid((unsigned)((S + kWtKeys - 1) / kWtKeys), (unsigned)Hkv, (unsigned)B);
+  p.B = B;
+  // one CTA per piece; no more pieces than blocks
+  const int64_t most = (((int64_t)S + kWtKeys - 1) / kWtKeys) * B * Hkv;
+  const int grid = (int)(most < kWtCtas * 152 ? most : kWtCtas * 152);
   cudaStream_t st = (cudaStream_t)stream;
-  if (k_scales) {
-    if (D == 128)
-      kv_weights<128, true><<<grid, kWtThreads, 0, st>>>(p);
-    else
-      kv_weights<64, true><<<grid, kWtThreads, 0, st>>>(p);
-  } else {
-    if (D == 128)
-      kv_weights<128, false><<<grid, kWtThreads, 0, st>>>(p);
-    else
-      kv_weights<64, false><<<grid, kWtThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  cudaError_t e;
+  if (k_scales)
+    e = D == 128 ? launch_weights<128, true>(p, grid, st) : launch_weights<64, true>(p, grid, st);
+  else
+    e = D == 128 ? launch_weights<128, false>(p, grid, st) : launch_weights<64, false>(p, grid, st);
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -177,6 +177,8 @@ def _weights(rng, B, Hkv, S, kind):
     (3, 2, 1111, [1111, 700, 513], 512, 0),
     (1, 2, 9000, [8999], 7001, 640),
     (2, 1, 70001, [70001, 40000], 3001, 100),
+    (1, 1, 131073, [131073], 4000, 7),       # a cluster of sixteen
+    (1, 2, 262145, [262145], 60000, 60),     # more than a cluster holds
 ])
 def test_evict_matches_oracle(B, Hkv, S, length, budget, recent, kind, in_place):
     rng = np.random.default_rng(S + budget)
