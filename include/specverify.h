@@ -473,7 +473,8 @@ int spec_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales,
  * -inf.  What cache positions behind prefix_len + N hold does not matter; a
  * NaN block of a drafted position reaches only the rows that see it.
  * Workspace: spec_tree_attention_kv4_workspace_bytes(B, N, Hq, Hkv, D, S) bytes,
- * 256-byte aligned, uninitialised (0 = invalid sizes).
+ * 256-byte aligned, uninitialised (0: none is needed, or the sizes are
+ * invalid).
  * Errors: SPEC_ERR_SHAPE unless 1 <= N <= 64, Hq % Hkv == 0, S >= N and
  * B <= 65535, or when B * Hkv * ceil(N Hq / Hkv / 16) reaches 2^31;
  * SPEC_ERR_UNSUPPORTED unless D is 64 or 128; SPEC_ERR_ARG for scale <= 0 or

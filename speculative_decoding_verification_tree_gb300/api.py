@@ -401,24 +401,27 @@ def kv4_cache(B, Hkv, S, D=128, device=None) -> KV4Cache:
 # microseconds: each argument is checked and turned into an address in one
 # step, and the device is only switched when it has to be.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _addr(t):
-    if not t.is_cuda:
+def _index(t):
+    """Ordinal of the CUDA device that holds `t`."""
+    i = t.get_device()
+    if i < 0:
         raise ValueError("device tensors are required")
-    if not t.is_contiguous():
-        raise ValueError("tensors must be contiguous")
-    return t.data_ptr()
+    return i
 
 
 def _arg(t, dtype, shape, dev, name):
     """Address of an argument, after the checks of _want, _device and _ptr."""
-    if t.dtype is not dtype or t.shape != shape:
-        _want(t, dtype, shape, name)
-    if t.device != dev:
-        raise ValueError(f"all tensors must be on {dev}; got one on "
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _want(t, dtype, shape, name)
+    if t.get_device() != dev:
+        raise ValueError(f"all tensors must be on cuda:{dev}; got one on "
                          f"{t.device}")
-    return _addr(t)
+    raise ValueError("tensors must be contiguous")
 
 
 def _kv4_args(cache, B, Hkv, S, D, dev):
@@ -433,8 +436,8 @@ def _kv4_args(cache, B, Hkv, S, D, dev):
 
 
 def _alloc(shape, dtype, dev, stream, make=torch.empty):
-    """Allocate under the call's stream, so that memory the wrapper frees on
-    return is reused in that stream's order."""
+    """Allocate on cuda:`dev` under the call's stream, so that memory the
+    wrapper frees on return is reused in that stream's order."""
     if stream is None:
         return make(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
@@ -442,15 +445,19 @@ def _alloc(shape, dtype, dev, stream, make=torch.empty):
 
 
 def _enqueue(name, dev, stream, *args):
-    """Call an entry point (without its last argument, the stream) on `dev`."""
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _lib.call(name, *args, stream.cuda_stream if stream
-                             is not None else _raw_stream(dev.index))
-    return _lib.call(name, *args, stream.cuda_stream if stream is not None
-                     else _raw_stream(dev.index))
+    """Call an entry point (without its last argument, the stream) on
+    cuda:`dev`."""
+    if stream is None:
+        handle = _raw_stream(dev)
+    elif stream.device_index == dev:
+        handle = stream.cuda_stream
+    else:
+        raise ValueError(f"stream is on {stream.device}, tensors on "
+                         f"cuda:{dev}")
+    if dev == _current_device():
+        return _lib.call(name, *args, handle)
+    with torch.cuda.device(dev):
+        return _lib.call(name, *args, handle)
 
 
 def spec_kv4_append(k, v, prefix_len, cache, *, k_unit=1.0, v_unit=1.0,
@@ -460,7 +467,7 @@ def spec_kv4_append(k, v, prefix_len, cache, *, k_unit=1.0, v_unit=1.0,
     are powers of two.  Returns the cache."""
     B, n, Hkv, D = shape = k.shape
     S = cache[0].shape[2]
-    dev = k.device
+    dev = _index(k)
     _enqueue("spec_kv4_append", dev, stream,
              _arg(k, torch.bfloat16, shape, dev, "k"),
              _arg(v, torch.bfloat16, shape, dev, "v"),
@@ -475,7 +482,7 @@ def spec_kv4_read(cache, start, n, *, k_unit=1.0, v_unit=1.0, out=None,
     [B, n, Hkv, D] bf16 (exact; zeros outside the cache)."""
     B, Hkv, S, half = cache[0].shape
     D = 2 * half
-    dev = start.device
+    dev = _index(start)
     args = _kv4_args(cache, B, Hkv, S, D, dev)
     shape = (B, n, Hkv, D)
     k, v = out if out is not None else (
@@ -503,7 +510,7 @@ def spec_tree_attention_kv4(q, cache, prefix_len, mask_bits, *, scale=None,
     (out [B, N, Hq, D] bf16, lse or None)."""
     B, N, Hq, D = shape = q.shape
     _, Hkv, S, _ = cache[0].shape
-    dev = q.device
+    dev = _index(q)
     args = (_arg(q, torch.bfloat16, shape, dev, "q"),
             *_kv4_args(cache, B, Hkv, S, D, dev),
             _arg(prefix_len, torch.int32, (B,), dev, "prefix_len"),
@@ -514,9 +521,11 @@ def spec_tree_attention_kv4(q, cache, prefix_len, mask_bits, *, scale=None,
         lse = _alloc((B, N, Hq), torch.float32, dev, stream)
     elif lse is False:
         lse = None
+    nbytes = 0 if ws is None else ws.numel()
     if ws is None:
-        ws = _alloc(_kv4_workspace_bytes(B, N, Hq, Hkv, D, S), torch.uint8,
-                    dev, stream)
+        nbytes = _kv4_workspace_bytes(B, N, Hq, Hkv, D, S)
+        if nbytes:
+            ws = _alloc(nbytes, torch.uint8, dev, stream)
     if scale is None:
         scale = D ** -0.5
     _enqueue("spec_tree_attention_kv4", dev, stream, *args, B, N, Hq, Hkv, D,
@@ -524,7 +533,8 @@ def spec_tree_attention_kv4(q, cache, prefix_len, mask_bits, *, scale=None,
              _arg(out, torch.bfloat16, shape, dev, "out"),
              None if lse is None else _arg(lse, torch.float32, (B, N, Hq), dev,
                                            "lse"),
-             _arg(ws, torch.uint8, ws.shape, dev, "ws"), ws.numel())
+             None if ws is None else _arg(ws, torch.uint8, (nbytes,), dev,
+                                          "ws"), nbytes)
     return out, lse
 
 
@@ -539,7 +549,7 @@ def spec_kv_weights(q, k_cache, lse, prefix_len, path_len, path_nodes=None, *,
     weights [B, Hkv, S] float32 or None (zeros).  Returns out [B, Hkv, S]
     (which may be `weights`)."""
     B, N, Hq, D = shape = q.shape
-    dev = q.device
+    dev = _index(q)
     if torch.is_tensor(k_cache):
         _, Hkv, S, _ = k_cache.shape
         ka = _arg(k_cache, torch.bfloat16, (B, Hkv, S, D), dev, "k_cache")
@@ -578,7 +588,7 @@ def spec_kv_evict(weights, length, planes, *, budget, recent, planes_out=None,
     weights_out (if given) the weights.  Returns (kept [B, Hkv, budget] int32,
     -1 padded, new_len [B] int32)."""
     B, Hkv, S = shape = weights.shape
-    dev = weights.device
+    dev = _index(weights)
     if planes_out is None:
         if weights_out is not None and weights_out is not weights:
             raise ValueError("in place (planes_out None) the weights move in "

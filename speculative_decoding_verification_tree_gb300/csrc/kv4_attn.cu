@@ -790,16 +790,6 @@ int rows_warps(int B, int Hkv, int R, int S) {
   const int64_t want = (blocks + kMinBlocks - 1) / kMinBlocks;
   return (int)(want < RowsCfg<NT>::kPieces ? want : RowsCfg<NT>::kPieces);
 }
-size_t part_bytes(int warps, int rows, int D) {
-  return ((size_t)2 * warps * rows * (D + 2) * sizeof(float) + 255) / 256 * 256;
-}
-size_t rows_ws(int B, int Hkv, int R, int D, int S) {
-  if (R <= 8) return part_bytes(rows_warps<1>(B, Hkv, R, S), R, D);
-  if (R <= 16) return part_bytes(rows_warps<2>(B, Hkv, R, S), R, D);
-  if (R <= kRowsMax) return part_bytes(rows_warps<4>(B, Hkv, R, S), R, D);
-  return kv4_tc_ws(B, Hkv, R, D, S);
-}
-
 // CTAs per cluster of kv4_unit, or 0 for pieces of the line.  Units leave
 // some of the resident CTAs idle, or the last wave part empty, for as many
 // 32-key blocks a warp as the longest unit may have; pieces cost the join's
@@ -817,6 +807,21 @@ int unit_cluster(int64_t units, int S) {
   const double idle = 1.0 - (double)(units * C) / (double)(waves * slots);
   const double blocks = (double)S / kKeys / (C * RowsCfg<NT>::kWarps);
   return idle * blocks * waves > kIdleBlocks ? 0 : C;
+}
+
+// Bytes of the pieces' partial results: 0 when clusters do without.
+template <int NT>
+size_t part_bytes(int B, int Hkv, int R, int D, int S) {
+  const int64_t units = (int64_t)B * Hkv * ((R + 8 * NT - 1) / (8 * NT));
+  if (unit_cluster<NT>(units, S) > 0) return 0;
+  const int rows = R < 8 * NT ? R : 8 * NT;
+  return (size_t)2 * rows_warps<NT>(B, Hkv, R, S) * rows * (D + 2) * sizeof(float);
+}
+size_t attn_ws(int B, int Hkv, int R, int D, int S) {
+  if (R <= 8) return part_bytes<1>(B, Hkv, R, D, S);
+  if (R <= 16) return part_bytes<2>(B, Hkv, R, D, S);
+  if (R <= kRowsMax) return part_bytes<4>(B, Hkv, R, D, S);
+  return kv4_tc_ws(B, Hkv, R, D, S);
 }
 
 template <int D, int NT>
@@ -887,8 +892,8 @@ extern "C" size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, 
       (D != 64 && D != 128))
     return 0;
   const int64_t R = (int64_t)N * (Hq / Hkv);
-  if ((int64_t)B * Hkv * ((R + 15) / 16) > 2147483647) return 0;
-  return rows_ws(B, Hkv, (int)R, D, S) + 256;
+  if (B == 0 || (int64_t)B * Hkv * ((R + 15) / 16) > 2147483647) return 0;
+  return (attn_ws(B, Hkv, (int)R, D, S) + 255) / 256 * 256;
 }
 
 extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
@@ -913,8 +918,8 @@ extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
   const int64_t R = (int64_t)N * (Hq / Hkv);
   const int64_t tiles = (R + 15) / 16;
   if ((int64_t)B * Hkv * tiles > 2147483647 || (double)B * Hkv * S > 4.0e15) return SPEC_ERR_SHAPE;
-  if (!workspace || (uintptr_t)workspace % 256 != 0 ||
-      ws_bytes < spec_tree_attention_kv4_workspace_bytes(B, N, Hq, Hkv, D, S))
+  const size_t need = attn_ws(B, Hkv, (int)R, D, S);
+  if (need > 0 && (!workspace || (uintptr_t)workspace % 256 != 0 || ws_bytes < need))
     return SPEC_ERR_WORKSPACE;
   Kv4Attn p = {};
   p.q = (const uint16_t*)q;

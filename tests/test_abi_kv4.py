@@ -50,8 +50,12 @@ def test_append_and_read_argument_errors(lib, name):
 
 
 def test_attention_argument_errors(lib):
-    f = lib.raw("spec_tree_attention_kv4_workspace_bytes", 2, 8, 8, 2, 128, 64)
+    # one long sequence leaves partial results; short ones need no workspace
+    f = lib.raw("spec_tree_attention_kv4_workspace_bytes", 1, 1, 8, 2, 128,
+                1 << 18)
     assert f > 0 and f % 256 == 0
+    assert lib.raw("spec_tree_attention_kv4_workspace_bytes", 2, 8, 8, 2, 128,
+                   64) == 0
     for bad in ((-1, 8, 8, 2, 128, 64), (2, 0, 8, 2, 128, 64),
                 (2, 65, 8, 2, 128, 64), (2, 8, 7, 2, 128, 64),
                 (2, 8, 8, 2, 96, 64), (2, 8, 8, 2, 128, 7)):
@@ -75,8 +79,9 @@ def test_attention_argument_errors(lib):
                dict(ks=ODD4), dict(vs=ODD4), dict(mb=ODD4), dict(pre=ODD2),
                dict(lse=ODD2)):
         assert call(**kw) == lib.SPEC_ERR_ARG, kw
-    for kw in (dict(ws=None), dict(ws=ODD), dict(nbytes=f - 1)):
-        assert call(**kw) == lib.SPEC_ERR_WORKSPACE, kw
+    long = dict(B=1, N=1, S=1 << 18)
+    for kw in (dict(ws=None), dict(ws=ODD), dict(nbytes=f - 256)):
+        assert call(**long, **kw) == lib.SPEC_ERR_WORKSPACE, kw
     assert call(B=0, q=None, ws=None, nbytes=0) == lib.SPEC_OK
 
 
@@ -186,9 +191,12 @@ def test_wrappers_match_their_signatures(monkeypatch):
         calls.append(name)
         return 256
     monkeypatch.setattr(_lib, "call", fake)
-    monkeypatch.setattr(api, "_addr", lambda t: FAKE.value)
+    monkeypatch.setattr(api, "_index", lambda t: 0)
+    monkeypatch.setattr(api, "_arg", lambda *a: FAKE.value)
     monkeypatch.setattr(api, "_raw_stream", lambda i: 0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(api, "_current_device", lambda: 0)
+    monkeypatch.setattr(api, "_alloc", lambda shape, dtype, dev, stream,
+                        make=torch.empty: make(shape, dtype=dtype))
     B, N, Hq, Hkv, D, S = 2, 3, 4, 2, 64, 16
     cache = api.kv4_cache(B, Hkv, S, D, device="cpu")
     k = torch.zeros(B, N, Hkv, D, dtype=torch.bfloat16)
