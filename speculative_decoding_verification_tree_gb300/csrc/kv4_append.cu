@@ -14,8 +14,10 @@
 // before the conversion, which puts equal ones back on the border and moves
 // none across it.
 //
-// One thread takes one block: 32 bytes in, 9 out.  Pure streaming, bound by
-// HBM; a warp reads four contiguous 256-byte rows (D 128).
+// One thread takes one block at a time: 32 bytes in, 9 out.  Pure streaming,
+// bound by HBM.  A CTA's rows are consecutive positions of a head (the next
+// head's after the last), so that the codes and scales it writes are contiguous
+// while each row it reads is a whole 128- or 256-byte line.
 #include "kernels.h"
 #include "kv4.cuh"
 
@@ -23,119 +25,162 @@ namespace sv {
 namespace {
 
 constexpr int kAppThreads = 256;
+constexpr int kAppUnroll = 2;  // blocks per thread
+
+// One call's geometry.  A sequence's rows are (head, position) pairs, head
+// first; a CTA takes kAppThreads * kAppUnroll consecutive blocks of one
+// sequence (blockIdx.x = sequence x chunk), of K or V (blockIdx.y).
+struct AppShape {
+  int n, Hkv, log_nb;  // 2^log_nb blocks per row
+  uint32_t chunks;     // CTAs per sequence
+  uint32_t blocks;     // blocks per sequence
+  int64_t S;
+};
+// Where block t of sequence b lies in the [B, n, Hkv, nb] rows and in the
+// cache (-1: its position is outside).
+__device__ __forceinline__ void place(const AppShape& a, int b, int64_t start, uint32_t t,
+                                      int64_t* in, int64_t* out) {
+  const uint32_t blk = t & ((1u << a.log_nb) - 1u), r = t >> a.log_nb;
+  const uint32_t h = r / (uint32_t)a.n, j = r - h * (uint32_t)a.n;
+  *in = ((((int64_t)b * a.n + j) * a.Hkv + h) << a.log_nb) + blk;
+  const int64_t pos = start + j;
+  *out = pos < 0 || pos >= a.S ? -1
+                               : ((((int64_t)b * a.Hkv + h) * a.S + pos) << a.log_nb) + blk;
+}
 
 __global__ void __launch_bounds__(kAppThreads)
     kv4_append(const uint4* __restrict__ k, const uint4* __restrict__ v,
-               const int32_t* __restrict__ prefix_len, int64_t blocks, int n, int Hkv, int nb,
-               int64_t S, float k_unit, float v_unit, uint8_t* __restrict__ kc,
-               uint8_t* __restrict__ ks, uint8_t* __restrict__ vc, uint8_t* __restrict__ vs) {
-  const int64_t t = (int64_t)blockIdx.x * kAppThreads + threadIdx.x;
-  if (t >= blocks) return;
+               const int32_t* __restrict__ prefix_len, const AppShape a, float k_unit,
+               float v_unit, uint8_t* __restrict__ kc, uint8_t* __restrict__ ks,
+               uint8_t* __restrict__ vc, uint8_t* __restrict__ vs) {
   const bool is_v = blockIdx.y != 0;
-  // block t of the [B, n, Hkv, nb] input
-  const uint4* src = (is_v ? v : k) + 2 * t;
-  const uint4 a = __ldg(src), c = __ldg(src + 1);
-  const int blk = (int)(t % nb);
-  int64_t r = t / nb;
-  const int h = (int)(r % Hkv);
-  r /= Hkv;
-  const int j = (int)(r % n);
-  const int b = (int)(r / n);
-  const int64_t pos = (int64_t)prefix_len[b] + j;
-  if (pos < 0 || pos >= S) return;
-  const int64_t row = ((int64_t)b * Hkv + h) * S + pos;
+  const int b = (int)(blockIdx.x / a.chunks);
+  const uint32_t t0 = (blockIdx.x - b * a.chunks) * (kAppThreads * kAppUnroll) + threadIdx.x;
+  const int64_t start = prefix_len[b];
+  const uint4* src = is_v ? v : k;
   const float unit = is_v ? v_unit : k_unit;
   const float inv_unit = 1.f / unit;  // exact: a power of two
-
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-  uint32_t mx = 0;  // largest magnitude: bf16 magnitudes order like their bits
+  uint4 lo[kAppUnroll], hi[kAppUnroll];
+  int64_t to[kAppUnroll];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
-  mx = max(mx & 0xffffu, mx >> 16);
-  const float amax = __uint_as_float(mx << 16);
-  uint32_t sb = f32_to_e4m3(__fdiv_rn(amax * inv_unit, 6.f));  // NaN stays NaN
-  if (sb == 0) sb = 1;                                         // 2^-9
-  const float s = half2_to_f32(e4m3x2_to_half2(sb)).x;
-  const float inv = __frcp_rn(s * unit);
-  uint32_t code[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = bf16_lo(w[4 * i + e]) * inv;
-      x[2 * e + 1] = bf16_hi(w[4 * i + e]) * inv;
+  for (int u = 0; u < kAppUnroll; ++u) {
+    const uint32_t t = t0 + u * kAppThreads;
+    to[u] = -1;
+    if (t < a.blocks) {
+      int64_t in;
+      place(a, b, start, t, &in, &to[u]);
+      if (to[u] >= 0) {
+        lo[u] = __ldcs(src + 2 * in);
+        hi[u] = __ldcs(src + 2 * in + 1);
+      }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      x[e] = __uint_as_float((__float_as_uint(x[e]) + 0x800u) & 0xfffff000u);
-    code[i] = f32x8_to_e2m1(x);
   }
-  uint8_t* cp = (is_v ? vc : kc) + (row * nb + blk) * 8;
-  *reinterpret_cast<uint2*>(cp) = make_uint2(code[0], code[1]);
-  (is_v ? vs : ks)[row * nb + blk] = (uint8_t)sb;
+#pragma unroll
+  for (int u = 0; u < kAppUnroll; ++u) {
+    if (to[u] < 0) continue;
+    const uint32_t w[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+    uint32_t mx = 0;  // largest magnitude: bf16 magnitudes order like their bits
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = __vmaxu2(mx, w[i] & 0x7fff7fffu);
+    mx = max(mx & 0xffffu, mx >> 16);
+    const float amax = __uint_as_float(mx << 16);
+    uint32_t sb = f32_to_e4m3(__fdiv_rn(amax * inv_unit, 6.f));  // NaN stays NaN
+    if (sb == 0) sb = 1;                                         // 2^-9
+    const float s = half2_to_f32(e4m3x2_to_half2(sb)).x;
+    const float inv = __frcp_rn(s * unit);
+    uint32_t code[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = bf16_lo(w[4 * i + e]) * inv;
+        x[2 * e + 1] = bf16_hi(w[4 * i + e]) * inv;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = __uint_as_float((__float_as_uint(x[e]) + 0x800u) & 0xfffff000u);
+      code[i] = f32x8_to_e2m1(x);
+    }
+    *reinterpret_cast<uint2*>((is_v ? vc : kc) + to[u] * 8) = make_uint2(code[0], code[1]);
+    (is_v ? vs : ks)[to[u]] = (uint8_t)sb;
+  }
 }
 
 __global__ void __launch_bounds__(kAppThreads)
     kv4_read(const uint8_t* __restrict__ kc, const uint8_t* __restrict__ ks,
              const uint8_t* __restrict__ vc, const uint8_t* __restrict__ vs,
-             const int32_t* __restrict__ start, int64_t blocks, int n, int Hkv, int nb, int64_t S,
-             float k_unit, float v_unit, uint4* __restrict__ k, uint4* __restrict__ v) {
-  const int64_t t = (int64_t)blockIdx.x * kAppThreads + threadIdx.x;
-  if (t >= blocks) return;
+             const int32_t* __restrict__ start_pos, const AppShape a, float k_unit, float v_unit,
+             uint4* __restrict__ k, uint4* __restrict__ v) {
   const bool is_v = blockIdx.y != 0;
-  const int blk = (int)(t % nb);
-  int64_t r = t / nb;
-  const int h = (int)(r % Hkv);
-  r /= Hkv;
-  const int j = (int)(r % n);
-  const int b = (int)(r / n);
-  const int64_t pos = (int64_t)start[b] + j;
-  uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (pos >= 0 && pos < S) {
-    const int64_t row = ((int64_t)b * Hkv + h) * S + pos;
-    const uint2 c =
-        *reinterpret_cast<const uint2*>((is_v ? vc : kc) + (row * nb + blk) * 8);
-    const float s = half2_to_f32(e4m3x2_to_half2((is_v ? vs : ks)[row * nb + blk])).x *
-                    (is_v ? v_unit : k_unit);
-    uint32_t q[4];
-    e2m1x8_to_half2(c.x, q);
+  const int b = (int)(blockIdx.x / a.chunks);
+  const uint32_t t0 = (blockIdx.x - b * a.chunks) * (kAppThreads * kAppUnroll) + threadIdx.x;
+  const int64_t start = start_pos[b];
+  const float unit = is_v ? v_unit : k_unit;
+  uint2 code[kAppUnroll];
+  uint32_t sb[kAppUnroll];
+  int64_t to[kAppUnroll];
+#pragma unroll
+  for (int u = 0; u < kAppUnroll; ++u) {
+    const uint32_t t = t0 + u * kAppThreads;
+    to[u] = -1;
+    code[u] = make_uint2(0, 0);
+    sb[u] = 0;
+    if (t < a.blocks) {
+      int64_t from;
+      place(a, b, start, t, &to[u], &from);
+      if (from >= 0) {
+        code[u] = *reinterpret_cast<const uint2*>((is_v ? vc : kc) + from * 8);
+        sb[u] = (is_v ? vs : ks)[from];
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kAppUnroll; ++u) {
+    if (to[u] < 0) continue;
+    const float s = half2_to_f32(e4m3x2_to_half2(sb[u])).x * unit;
+    uint32_t q[4], o[8];
+    e2m1x8_to_half2(code[u].x, q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = half2_to_f32(q[i]);
       o[i] = pack_bf16x2(f.x * s, f.y * s);  // exact: six significant bits
     }
-    e2m1x8_to_half2(c.y, q);
+    e2m1x8_to_half2(code[u].y, q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = half2_to_f32(q[i]);
       o[4 + i] = pack_bf16x2(f.x * s, f.y * s);
     }
+    uint4* dst = (is_v ? v : k) + 2 * to[u];
+    __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
+    __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
   }
-  uint4* dst = (is_v ? v : k) + 2 * t;
-  dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Checks shared by the two entry points; *grid_x = CTAs for the blocks.
+// Checks shared by the two entry points; sets the geometry and *ctas (0: nothing
+// to do).
 int check_kv4(const void* k, const void* v, const int32_t* at, int B, int n, int Hkv, int D, int S,
               float k_unit, float v_unit, const void* kc, const void* ks, const void* vc,
-              const void* vs, int64_t* blocks) {
+              const void* vs, AppShape* a, unsigned* ctas) {
   if (B < 0 || n < 0 || Hkv < 1 || S < 0) return SPEC_ERR_SHAPE;
   if (D != 64 && D != 128) return SPEC_ERR_UNSUPPORTED;
   if (!kv4_unit_ok(k_unit) || !kv4_unit_ok(v_unit)) return SPEC_ERR_ARG;
-  *blocks = 0;
+  *ctas = 0;
   if (B == 0 || n == 0) return SPEC_OK;
-  // [B, n, Hkv] rows and [B, Hkv, S] cache rows are counted in 64 bits; the
-  // grid's x dimension holds 2^31 - 1 CTAs
-  const double rows = (double)B * n * Hkv;
-  if (rows * (D / kKv4Block) / kAppThreads > 2147483000.0) return SPEC_ERR_SHAPE;
-  if ((double)B * Hkv * S > 4.0e15) return SPEC_ERR_SHAPE;
+  // a sequence's blocks are counted in 32 bits, the CTAs by the grid's x
+  // dimension, everything else in 64 bits
+  const double blocks = (double)n * Hkv * (D / kKv4Block);
+  if (blocks > 2147480000.0 || (double)B * Hkv * S > 4.0e15) return SPEC_ERR_SHAPE;
+  constexpr int kCta = kAppThreads * kAppUnroll;
+  const int64_t chunks = ((int64_t)blocks + kCta - 1) / kCta;
+  if (chunks * B > 2147483647) return SPEC_ERR_SHAPE;
   if (!k || !v || !at || !kc || !ks || !vc || !vs) return SPEC_ERR_ARG;
   if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)kc | (uintptr_t)vc) % 16 != 0 ||
       ((uintptr_t)ks | (uintptr_t)vs) % 8 != 0 || (uintptr_t)at % 4 != 0)
     return SPEC_ERR_ARG;
-  *blocks = (int64_t)B * n * Hkv * (D / kKv4Block);
+  *a = {n, Hkv, D == 128 ? 3 : 2, (uint32_t)chunks, (uint32_t)blocks, S};
+  *ctas = (unsigned)(chunks * B);
   return SPEC_OK;
 }
 
@@ -160,14 +205,14 @@ extern "C" int spec_kv4_append(const void* k, const void* v, const int32_t* pref
                                int n, int Hkv, int D, int S, float k_unit, float v_unit,
                                uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
                                uint8_t* v_scales, void* stream) {
-  int64_t blocks;
+  AppShape a;
+  unsigned ctas;
   const int rc = check_kv4(k, v, prefix_len, B, n, Hkv, D, S, k_unit, v_unit, k_codes, k_scales,
-                           v_codes, v_scales, &blocks);
-  if (rc != SPEC_OK || blocks == 0) return rc;
-  const dim3 grid((unsigned)((blocks + kAppThreads - 1) / kAppThreads), 2);
-  kv4_append<<<grid, kAppThreads, 0, (cudaStream_t)stream>>>(
-      (const uint4*)k, (const uint4*)v, prefix_len, blocks, n, Hkv, D / kKv4Block, S, k_unit,
-      v_unit, k_codes, k_scales, v_codes, v_scales);
+                           v_codes, v_scales, &a, &ctas);
+  if (rc != SPEC_OK || ctas == 0) return rc;
+  kv4_append<<<dim3(ctas, 2), kAppThreads, 0, (cudaStream_t)stream>>>(
+      (const uint4*)k, (const uint4*)v, prefix_len, a, k_unit, v_unit, k_codes, k_scales, v_codes,
+      v_scales);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
@@ -175,13 +220,12 @@ extern "C" int spec_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales,
                              const uint8_t* v_codes, const uint8_t* v_scales, const int32_t* start,
                              int B, int n, int Hkv, int D, int S, float k_unit, float v_unit,
                              void* k, void* v, void* stream) {
-  int64_t blocks;
+  AppShape a;
+  unsigned ctas;
   const int rc = check_kv4(k, v, start, B, n, Hkv, D, S, k_unit, v_unit, k_codes, k_scales,
-                           v_codes, v_scales, &blocks);
-  if (rc != SPEC_OK || blocks == 0) return rc;
-  const dim3 grid((unsigned)((blocks + kAppThreads - 1) / kAppThreads), 2);
-  kv4_read<<<grid, kAppThreads, 0, (cudaStream_t)stream>>>(
-      k_codes, k_scales, v_codes, v_scales, start, blocks, n, Hkv, D / kKv4Block, S, k_unit,
-      v_unit, (uint4*)k, (uint4*)v);
+                           v_codes, v_scales, &a, &ctas);
+  if (rc != SPEC_OK || ctas == 0) return rc;
+  kv4_read<<<dim3(ctas, 2), kAppThreads, 0, (cudaStream_t)stream>>>(
+      k_codes, k_scales, v_codes, v_scales, start, a, k_unit, v_unit, (uint4*)k, (uint4*)v);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
