@@ -302,8 +302,6 @@ __device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>&
     float s[2][NT][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
       uint32_t kw[2][kW], ksc[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -335,8 +333,11 @@ __device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>&
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 q = kQReg ? qr[2 * w + x][nt] : sm.qf[warp][2 * w + x][nt][lane];
-            mma16816_f16(s[u][nt], h[0][2 * x], h[1][2 * x], h[0][2 * x + 1], h[1][2 * x + 1],
-                         q.x, q.y);
+            if (w == 0 && x == 0)
+              mma16816_f16_first(s[u][nt], h[0][0], h[1][0], h[0][1], h[1][1], q.x, q.y);
+            else
+              mma16816_f16(s[u][nt], h[0][2 * x], h[1][2 * x], h[0][2 * x + 1], h[1][2 * x + 1],
+                           q.x, q.y);
           }
       }
     }

@@ -69,7 +69,7 @@ struct WtSmem {
   static constexpr int kCodes = 32 * (D / 2), kStage = kCodes + 32 * (D / 16);
   unsigned char ring[kKv4 ? kWtWarps * kWtStages * kStage : 16];
   uint2 qf[kWtRows / 8][D / 16][32];  // operand registers b0, b1 per lane
-  float rowf[kWtRows], rowl[kWtRows];
+  float rowf[kWtRows], rowl[kWtRows];  // scale, and the normaliser negated
   int rowt[kWtRows], nodes[kWtNodes];
   int64_t line[kWtThreads + 1], tmp[kWtWarps];
 };
@@ -122,31 +122,40 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
     const int first = k0 * kWtKeys, last = min(L, k1 * kWtKeys);
 
     // a stage of this warp's ring: 32 keys' codes, then their scales; keys behind
-    // the sequence are zeros, not read
+    // the sequence are zeros, not read.  The source pointers run ahead of the
+    // loop by kWtStages - 1 blocks.
+    constexpr int kChunks = D / 32;  // 16-byte chunks per key
     const uint32_t ring = smem_u32(sm.ring) + (uint32_t)(warp * kWtStages * Sm::kStage);
-    auto fill = [&](int key0, int slot) {
-      constexpr int kChunks = D / 32;  // 16-byte chunks per key
-      const uint32_t st = ring + (uint32_t)(slot * Sm::kStage);
-      const uint8_t* codes = (const uint8_t*)p.k + (row0 + key0) * (D / 2) + lane * 16;
-      const uint8_t* scales = p.ks + (row0 + key0 + lane) * (D / 16);
+    const uint32_t lane_dst = ring + (uint32_t)(lane * 16);
+    const uint32_t lane_dst_s = ring + (uint32_t)(Sm::kCodes + lane * (D / 16));
+    int fill_key = first + warp * 32;
+    const uint8_t* codes = (const uint8_t*)p.k + (row0 + fill_key) * (D / 2) + lane * 16;
+    const uint8_t* scales = p.ks + (row0 + fill_key + lane) * (D / 16);
+    auto fill = [&](uint32_t slot_at) {
+      const int left = last - fill_key;
+      if (left >= 32) {
 #pragma unroll
-      for (int r = 0; r < kChunks; ++r) {
-        const bool take = key0 + (r * 32 + lane) / kChunks < L;
-        cp_async_or_zero<16>(st + (uint32_t)(r * 512 + lane * 16),
-                             take ? codes + r * 512 : (const uint8_t*)p.k, take);
+        for (int r = 0; r < kChunks; ++r)
+          cp_async<16>(lane_dst + slot_at + (uint32_t)(r * 512), codes + r * 512);
+        cp_async<D / 16>(lane_dst_s + slot_at, scales);
+      } else if (left > 0) {
+#pragma unroll
+        for (int r = 0; r < kChunks; ++r) {
+          const bool take = (r * 32 + lane) / kChunks < left;
+          cp_async_or_zero<16>(lane_dst + slot_at + (uint32_t)(r * 512),
+                               take ? codes + r * 512 : (const uint8_t*)p.k, take);
+        }
+        cp_async_or_zero<D / 16>(lane_dst_s + slot_at, lane < left ? scales : p.ks, lane < left);
       }
-      const bool take = key0 + lane < L;
-      cp_async_or_zero<D / 16>(st + (uint32_t)(Sm::kCodes + lane * (D / 16)),
-                               take ? scales : p.ks, take);
+      cp_async_commit();
+      fill_key += kWtKeys;
+      codes += kWtKeys * (D / 2);
+      scales += kWtKeys * (D / 16);
     };
     if constexpr (kKv4) {
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < kWtStages - 1; ++i) {
-        const int k = first + warp * 32 + i * kWtKeys;
-        if (k < last) fill(k, i);
-        cp_async_commit();
-      }
+      for (int i = 0; i < kWtStages - 1; ++i) fill((uint32_t)(i * Sm::kStage));
     }
 
     // the accepted rows of q as operand fragments, their scales, normalisers and
@@ -196,7 +205,7 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
         if (lane < D / 4) sm.qf[i >> 3][s][4 * (i & 7) + cc] = make_uint2(h0, h1);
         if (lane == 0) {
           sm.rowf[i] = p.scale_log2 * up;
-          sm.rowl[i] = l[x] == neg_inf() ? -l[x] : l[x];  // a row that saw nothing weighs nothing
+          sm.rowl[i] = l[x] == neg_inf() ? l[x] : -l[x];  // a row that saw nothing weighs nothing
           sm.rowt[i] = r < R ? P + r / Gq : -1;
         }
       }
@@ -204,50 +213,26 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
     if (groups == 1) stage(0);
     __syncthreads();
 
-    int slot = 0;
-    for (int at = first; at < last; at += kWtKeys) {
+    uint32_t slot_at = 0;  // the stage that holds this iteration's keys
+    const float* in_p = in + first + warp * 32 + 8 * c + g;   // the key this lane writes
+    float* out_p = out + first + warp * 32 + 8 * c + g;
+    for (int at = first; at < last; at += kWtKeys, in_p += kWtKeys, out_p += kWtKeys) {
       const int key0 = at + warp * 32;
       const bool live = key0 < L && groups > 0;
-      const int key = key0 + 8 * c + g;  // the one this lane writes
-      const float before = in && key < P ? in[key] : 0.f;
-      // the 32 keys' operand fragments: [8 keys][k step][a0 / a1, a2 / a3]
-      uint32_t kb[4][kSteps][2];
+      const int key = key0 + 8 * c + g;
+      const float before = in && key < P ? *in_p : 0.f;
+      // operand fragments: [8 keys][k step][a0 / a1, a2 / a3]
+      uint32_t kb[kKv4 ? 2 : 4][kSteps][2];
+      const unsigned char *st_keys = nullptr, *st_scales = nullptr;
       if constexpr (kKv4) {
         cp_async_wait<kWtStages - 2>();
         __syncwarp();
-        const int next = key0 + (kWtStages - 1) * kWtKeys;
-        if (next < last) fill(next, slot == 0 ? kWtStages - 1 : slot - 1);
-        cp_async_commit();
-        const unsigned char* st = sm.ring + (warp * kWtStages + slot) * Sm::kStage;
-        slot = slot == kWtStages - 1 ? 0 : slot + 1;
-        if (live) {
-          constexpr int kW = D / 32;
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const unsigned char* kr = st + (8 * t + g) * (D / 2) + 4 * kW * c;
-            const unsigned char* sr = st + Sm::kCodes + (8 * t + g) * (D / 16);
-            uint32_t w[kW], s2;
-            if constexpr (D == 128) {
-              const uint4 v = *reinterpret_cast<const uint4*>(kr);
-              w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-              s2 = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sr + 2 * c));
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(kr);
-              w[0] = v.x; w[1] = v.y;
-              s2 = e4m3x2_to_half2(sr[c]);
-            }
-#pragma unroll
-            for (int x = 0; x < kW; ++x) {
-              uint32_t h[4];
-              e2m1x8_to_half2(w[x], h);
-              const uint32_t s1 = (D == 128 && x >= 2) ? dup_hi(s2) : dup_lo(s2);
-              kb[t][2 * x][0] = hmul2(h[0], s1);
-              kb[t][2 * x][1] = hmul2(h[1], s1);
-              kb[t][2 * x + 1][0] = hmul2(h[2], s1);
-              kb[t][2 * x + 1][1] = hmul2(h[3], s1);
-            }
-          }
-        }
+        constexpr uint32_t kEnd = (kWtStages - 1) * Sm::kStage;
+        fill(slot_at == 0 ? kEnd : slot_at - Sm::kStage);
+        const unsigned char* st = sm.ring + warp * kWtStages * Sm::kStage + slot_at;
+        slot_at = slot_at == kEnd ? 0 : slot_at + Sm::kStage;
+        st_keys = st + g * (D / 2) + 4 * (D / 32) * c;
+        st_scales = st + Sm::kCodes + g * (D / 16);
       } else if (live) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -273,50 +258,85 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
         }
         const int tiles = (min(R - grp * kWtRows, kWtRows) + 7) / 8;
         if (live) {
-          // kTiles row tiles from nt on
-          auto tiles_of = [&](auto count, int nt) {
-            constexpr int kTiles = decltype(count)::value;
-            float s[kTiles][2][4] = {};
 #pragma unroll
-            for (int x = 0; x < kSteps; ++x)
+          for (int u = 0; u < 2; ++u) {  // sixteen keys at a time
+            if constexpr (kKv4) {
+              constexpr int kW = D / 32;
 #pragma unroll
-              for (int y = 0; y < kTiles; ++y) {
-                const uint2 q = sm.qf[nt + y][x][lane];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  if constexpr (kKv4)
-                    mma16816_f16(s[y][u], kb[2 * u][x][0], kb[2 * u + 1][x][0], kb[2 * u][x][1],
-                                 kb[2 * u + 1][x][1], q.x, q.y);
-                  else
-                    mma16816_bf16(s[y][u], kb[2 * u][x][0], kb[2 * u + 1][x][0], kb[2 * u][x][1],
-                                  kb[2 * u + 1][x][1], q.x, q.y);
+              for (int t = 0; t < 2; ++t) {
+                const unsigned char* kr = st_keys + (16 * u + 8 * t) * (D / 2);
+                const unsigned char* sr = st_scales + (16 * u + 8 * t) * (D / 16);
+                uint32_t w[kW], s2;
+                if constexpr (D == 128) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(kr);
+                  w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+                  s2 = e4m3x2_to_half2(*reinterpret_cast<const uint16_t*>(sr + 2 * c));
+                } else {
+                  const uint2 v = *reinterpret_cast<const uint2*>(kr);
+                  w[0] = v.x; w[1] = v.y;
+                  s2 = e4m3x2_to_half2(sr[c]);
                 }
-              }
 #pragma unroll
-            for (int y = 0; y < kTiles; ++y) {
-              const int i = (nt + y) * 8 + 2 * c;  // this lane's rows i, i + 1
-              const float2 f = *reinterpret_cast<const float2*>(&sm.rowf[i]);
-              const float2 l = *reinterpret_cast<const float2*>(&sm.rowl[i]);
-              const int2 lim = *reinterpret_cast<const int2*>(&sm.rowt[i]);
-              const bool whole = key0 + 31 <= P && (nt + y) * 8 + 8 <= R - grp * kWtRows;
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const float2 e = ffma2(
-                    make_float2(s[y][t >> 1][2 * (t & 1)], s[y][t >> 1][2 * (t & 1) + 1]), f,
-                    make_float2(-l.x, -l.y));
-                float2 w = make_float2(ex2(e.x), ex2(e.y));
-                if (!whole) {
-                  const int k = key0 + 8 * t + g;
-                  if (k > lim.x) w.x = 0.f;
-                  if (k > lim.y) w.y = 0.f;
+                for (int x = 0; x < kW; ++x) {
+                  uint32_t h[4];
+                  e2m1x8_to_half2(w[x], h);
+                  const uint32_t s1 = (D == 128 && x >= 2) ? dup_hi(s2) : dup_lo(s2);
+                  kb[t][2 * x][0] = hmul2(h[0], s1);
+                  kb[t][2 * x][1] = hmul2(h[1], s1);
+                  kb[t][2 * x + 1][0] = hmul2(h[2], s1);
+                  kb[t][2 * x + 1][1] = hmul2(h[3], s1);
                 }
-                col[t] = fadd2(col[t], w);
               }
             }
-          };
-          int nt = 0;  // pairs of tiles: four independent chains of products
-          for (; nt + 1 < tiles; nt += 2) tiles_of(std::integral_constant<int, 2>(), nt);
-          if (nt < tiles) tiles_of(std::integral_constant<int, 1>(), nt);
+            const uint32_t(&ka)[kSteps][2] = kb[kKv4 ? 0 : 2 * u];
+            const uint32_t(&kc)[kSteps][2] = kb[kKv4 ? 1 : 2 * u + 1];
+            // kTiles row tiles from nt on; even and odd k steps apart, so that
+            // two tiles are four independent chains of products
+            auto tiles_of = [&](auto count, int nt) {
+              constexpr int kTiles = decltype(count)::value;
+              float s[kTiles][2][4];
+#pragma unroll
+              for (int x = 0; x < kSteps; ++x)
+#pragma unroll
+                for (int y = 0; y < kTiles; ++y) {
+                  const uint2 q = sm.qf[nt + y][x][lane];
+                  float(&d)[4] = s[y][x & 1];
+                  if (kKv4 && x < 2)
+                    mma16816_f16_first(d, ka[x][0], kc[x][0], ka[x][1], kc[x][1], q.x, q.y);
+                  else if (kKv4)
+                    mma16816_f16(d, ka[x][0], kc[x][0], ka[x][1], kc[x][1], q.x, q.y);
+                  else if (x < 2)
+                    mma16816_bf16_first(d, ka[x][0], kc[x][0], ka[x][1], kc[x][1], q.x, q.y);
+                  else
+                    mma16816_bf16(d, ka[x][0], kc[x][0], ka[x][1], kc[x][1], q.x, q.y);
+                }
+#pragma unroll
+              for (int y = 0; y < kTiles; ++y) {
+                const int i = (nt + y) * 8 + 2 * c;  // this lane's rows i, i + 1
+                const float2 f = *reinterpret_cast<const float2*>(&sm.rowf[i]);
+                const float2 l = *reinterpret_cast<const float2*>(&sm.rowl[i]);
+                const bool whole = key0 + 31 <= P && (nt + y) * 8 + 8 <= R - grp * kWtRows;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  const float2 e =
+                      ffma2(fadd2(make_float2(s[y][0][2 * t], s[y][0][2 * t + 1]),
+                                  make_float2(s[y][1][2 * t], s[y][1][2 * t + 1])),
+                            f, l);
+                  float2 w = make_float2(ex2(e.x), ex2(e.y));
+                  if (!whole) {
+                    const int2 lim = *reinterpret_cast<const int2*>(&sm.rowt[i]);
+                    const int k = key0 + 16 * u + 8 * t + g;
+                    if (k > lim.x) w.x = 0.f;
+                    if (k > lim.y) w.y = 0.f;
+                  }
+                  col[2 * u + t] = fadd2(col[2 * u + t], w);
+                }
+              }
+            };
+            int nt = 0;
+            for (; nt + 1 < tiles; nt += 2) tiles_of(std::integral_constant<int, 2>(), nt);
+            if (nt < tiles) tiles_of(std::integral_constant<int, 1>(), nt);
+          }
         }
       }
       if (key0 < L) {
@@ -328,7 +348,7 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
           v += __shfl_xor_sync(0xffffffffu, v, 2);
           if (c == t) mine = v;
         }
-        if (key < L) out[key] = before + mine;
+        if (key < L) *out_p = before + mine;
       }
     }
     if constexpr (kKv4) cp_async_wait<0>();
