@@ -428,6 +428,19 @@ int spec_tree_attention(const void* q, const void* k_cache,
                         void* stream);
 
 /*
+ * spec_tree_attention with the rows' base-2 log normalisers: lse [B, N, Hq]
+ * float32 (out) = log2 sum_s 2^(log2(e) scale q . k_s) over the row's visible
+ * keys (-inf if there are none), as spec_kv_weights takes them.  out is what
+ * spec_tree_attention writes, bit for bit.  Errors as there, and SPEC_ERR_ARG
+ * for an lse that is NULL (B > 0) or not 4-byte aligned.
+ */
+int spec_tree_attention_lse(const void* q, const void* k_cache,
+                            const void* v_cache, const int32_t* prefix_len,
+                            const uint64_t* mask_bits, int B, int N, int Hq,
+                            int Hkv, int D, int S, float scale, void* out,
+                            float* lse, void* stream);
+
+/*
  * 4-bit KV cache.  A position of one key/value head holds D codes (e2m1, two
  * per byte, the even head dim in the low half byte) and D / 16 block scales
  * (e4m3, one per 16 consecutive head dims); the value a code c stands for is

@@ -115,6 +115,8 @@ _SIGNATURES = {
                                ctypes.POINTER(SpecAcceptStats), _P]),
     "spec_tree_attention": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                  ctypes.c_float, _P, _P]),
+    "spec_tree_attention_lse": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                                     _I, _F, _P, _P, _P]),
     "spec_kv4_append": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P, _P,
                              _P, _P, _P]),
     "spec_kv4_read": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _P,

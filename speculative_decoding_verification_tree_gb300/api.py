@@ -381,6 +381,31 @@ def spec_tree_attention(q, k_cache, v_cache, prefix_len, mask_bits, *,
     return out
 
 
+def spec_tree_attention_lse(q, k_cache, v_cache, prefix_len, mask_bits, *,
+                            scale=None, out=None, lse=None, stream=None):
+    """spec_tree_attention that also returns the rows' base-2 log normalisers:
+    (out [B, N, Hq, D] bf16, lse [B, N, Hq] float32)."""
+    B, N, Hq, D = shape = q.shape
+    _, Hkv, S, _ = k_cache.shape
+    dev = _index(q)
+    kv = (B, Hkv, S, D)
+    args = (_arg(q, torch.bfloat16, shape, dev, "q"),
+            _arg(k_cache, torch.bfloat16, kv, dev, "k_cache"),
+            _arg(v_cache, torch.bfloat16, kv, dev, "v_cache"),
+            _arg(prefix_len, torch.int32, (B,), dev, "prefix_len"),
+            _arg(mask_bits, torch.int64, (B, N), dev, "mask_bits"))
+    if out is None:
+        out = _alloc(shape, torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _alloc((B, N, Hq), torch.float32, dev, stream)
+    if scale is None:
+        scale = D ** -0.5
+    _enqueue("spec_tree_attention_lse", dev, stream, *args, B, N, Hq, Hkv, D,
+             S, scale, _arg(out, torch.bfloat16, shape, dev, "out"),
+             _arg(lse, torch.float32, (B, N, Hq), dev, "lse"))
+    return out, lse
+
+
 class KV4Cache(NamedTuple):
     """A 4-bit cache: codes [B, Hkv, S, D/2] and scales [B, Hkv, S, D/16]
     (uint8) of the keys and of the values."""

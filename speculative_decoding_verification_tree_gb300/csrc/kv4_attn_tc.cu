@@ -6,8 +6,8 @@
 // to fp16, everything else float32).  A CTA takes up to 256 query rows of one
 // (sequence, key/value head) as two 128-row tiles, and 64-key blocks of the
 // cache, or a share of them (splits, when there are fewer units than SMs):
-//   dequantisers (4 warps): the codes of block j + 2 on their way from HBM in
-//     registers while block j's become fp16 rows in a ring of swizzled
+//   dequantisers (4 warps): the codes of the next blocks on their way from HBM
+//     in registers while block j's become fp16 rows in a ring of swizzled
 //     shared-memory stages (K and V as stored: a 64-dim row per 128 bytes);
 //   S issuers, P V issuers (one thread per tile each): S_t = Q_t K^T with Q_t
 //     read from TMEM, O_t += P_t V with P_t from shared memory;
@@ -30,6 +30,7 @@ constexpr int kMT = 128;        // query rows per tile
 constexpr int kTiles = 2;
 constexpr int kRowsCta = kTiles * kMT;
 constexpr int kTcStages = 4;
+constexpr int kAhead = 3;       // blocks that a dequantiser thread has in registers
 constexpr int kPTile = kMT * kKB * 2;
 constexpr int kSoftWarps = 4 * kTiles;
 constexpr int kSoftThreads = kSoftWarps * 32;
@@ -76,6 +77,25 @@ __device__ __forceinline__ void await(TcSmem& sm, uint64_t* bar, uint32_t parity
   if (mbar_try_wait(bar, parity)) return;
   if (*(volatile uint32_t*)&sm.dead) return;
   if (!mbar_wait_bounded(bar, parity)) *(volatile uint32_t*)&sm.dead = 1;
+}
+
+// Loads that stay where they are written (ahead of the waits they overlap).
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld4(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld2(const uint8_t* p) {
+  unsigned short v;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
 }
 
 // One thread's part of a block on its way from HBM: D/2 head dims of one key.
@@ -227,17 +247,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
       const int64_t o = (int64_t)j * kKB;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        r.k[i] = have ? __ldcs(reinterpret_cast<const uint4*>(kc + o * (D / 2)) + i)
+        r.k[i] = have ? ld16(kc + o * (D / 2) + 16 * i)
                       : make_uint4(0, 0, 0, 0);
-        r.v[i] = have ? __ldcs(reinterpret_cast<const uint4*>(vc + o * (D / 2)) + i)
+        r.v[i] = have ? ld16(vc + o * (D / 2) + 16 * i)
                       : make_uint4(0, 0, 0, 0);
       }
       if constexpr (D == 128) {
-        r.ks = have ? __ldcs(reinterpret_cast<const uint32_t*>(ks + o * 8)) : 0u;
-        r.vs = have ? __ldcs(reinterpret_cast<const uint32_t*>(vs + o * 8)) : 0u;
+        r.ks = have ? ld4(ks + o * 8) : 0u;
+        r.vs = have ? ld4(vs + o * 8) : 0u;
       } else {
-        r.ks = have ? __ldcs(reinterpret_cast<const unsigned short*>(ks + o * 4)) : 0u;
-        r.vs = have ? __ldcs(reinterpret_cast<const unsigned short*>(vs + o * 4)) : 0u;
+        r.ks = have ? ld2(ks + o * 4) : 0u;
+        r.vs = have ? ld2(vs + o * 4) : 0u;
       }
     };
     // this thread's 16-byte chunks within a tile (D 128: the whole row of
@@ -278,15 +298,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
       fence_async_smem();
       mbar_arrive(&sm.kvfull[s]);
     };
-    Raw<D> r0, r1;
-    load(r0, 0);
-    load(r1, 1);
-    for (int j = 0; j < n; j += 2) {
-      put(r0, j);
-      load(r0, j + 2);
-      if (j + 1 < n) put(r1, j + 1);
-      load(r1, j + 3);
-    }
+    // kAhead blocks on their way: HBM's latency is longer than a block's time
+    Raw<D> r[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(r[i], i);
+    for (int j = 0; j < n; j += kAhead)
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (j + i < n) put(r[i], j + i);
+        load(r[i], j + i + kAhead);
+      }
     __syncwarp();
     asm volatile("bar.arrive 3, %0;" ::"n"(kSoftThreads + 128) : "memory");
   } else {

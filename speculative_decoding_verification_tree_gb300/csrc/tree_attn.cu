@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     tree_attn_tc(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const uint16_t* __restrict__ q, const int32_t* __restrict__ prefix_len,
                  const uint64_t* __restrict__ mask_bits, int N, int Hq, int Hkv, int S,
-                 float scale_log2, uint16_t* __restrict__ out) {
+                 float scale_log2, uint16_t* __restrict__ out, float* __restrict__ lse) {
   extern __shared__ __align__(1024) unsigned char araw[];
   const uint32_t raw = smem_u32(araw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -444,6 +444,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
         await(sm, &sm.pdone[t][(nblk - 1) & 1], (uint32_t)(((nblk - 1) >> 1) & 1));
       fence_after();
       const float inv = 1.f / l;
+      // the row's base-2 log normaliser (-inf where it saw nothing)
+      if (lse && valid) lse[qoff / kAD] = mref + log2f(l);
       uint4* dst = reinterpret_cast<uint4*>(out + qoff);
 #pragma unroll 1
       for (int c = 0; c < kAD / 32; ++c) {
@@ -506,10 +508,10 @@ bool cache_map(CUtensorMap* map, const void* base, int64_t rows) {
 
 using namespace sv;
 
-extern "C" int spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
-                                   const int32_t* prefix_len, const uint64_t* mask_bits, int B,
-                                   int N, int Hq, int Hkv, int D, int S, float scale, void* out,
-                                   void* stream) {
+static int tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* prefix_len, const uint64_t* mask_bits, int B, int N,
+                          int Hq, int Hkv, int D, int S, float scale, void* out, float* lse,
+                          void* stream) {
   // B and Hkv index grid dimensions z and y (at most 65535 each)
   if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hkv > 65535 ||
       Hq % Hkv != 0 || S < N)
@@ -537,7 +539,24 @@ extern "C" int spec_tree_attention(const void* q, const void* k_cache, const voi
   prof_begin(SPEC_PROF_ATTN, st);
   tree_attn_tc<<<grid, kAThreads, kASmemBytes, st>>>(
       mk, mv, (const uint16_t*)q, prefix_len, mask_bits, N, Hq, Hkv, S, scale * kLog2e,
-      (uint16_t*)out);
+      (uint16_t*)out, lse);
   prof_end(SPEC_PROF_ATTN, st);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+extern "C" int spec_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* prefix_len, const uint64_t* mask_bits, int B,
+                                   int N, int Hq, int Hkv, int D, int S, float scale, void* out,
+                                   void* stream) {
+  return tree_attention(q, k_cache, v_cache, prefix_len, mask_bits, B, N, Hq, Hkv, D, S, scale,
+                        out, nullptr, stream);
+}
+
+extern "C" int spec_tree_attention_lse(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* prefix_len, const uint64_t* mask_bits, int B,
+                                       int N, int Hq, int Hkv, int D, int S, float scale,
+                                       void* out, float* lse, void* stream) {
+  if (B > 0 && (!lse || (uintptr_t)lse % 4 != 0)) return SPEC_ERR_ARG;
+  return tree_attention(q, k_cache, v_cache, prefix_len, mask_bits, B, N, Hq, Hkv, D, S, scale,
+                        out, lse, stream);
 }

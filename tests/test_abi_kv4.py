@@ -85,6 +85,19 @@ def test_attention_argument_errors(lib):
     assert call(B=0, q=None, ws=None, nbytes=0) == lib.SPEC_OK
 
 
+def test_attention_lse_argument_errors(lib):
+    def call(B=2, N=8, D=128, q=FAKE, lse=FAKE, scale=0.1):
+        return lib.raw("spec_tree_attention_lse", q, FAKE, FAKE, FAKE, FAKE, B,
+                       N, 8, 2, D, 64, scale, FAKE, lse, None)
+    assert call(lse=None) == lib.SPEC_ERR_ARG
+    assert call(lse=ODD2) == lib.SPEC_ERR_ARG
+    assert call(q=None) == lib.SPEC_ERR_ARG
+    assert call(scale=0.0) == lib.SPEC_ERR_ARG
+    assert call(N=65) == lib.SPEC_ERR_SHAPE
+    assert call(D=64) == lib.SPEC_ERR_UNSUPPORTED
+    assert call(B=0, q=None, lse=None) == lib.SPEC_OK
+
+
 def test_weights_argument_errors(lib):
     def call(q=FAKE, k=FAKE, ks=FAKE, lse=FAKE, pre=FAKE, n=FAKE, nodes=FAKE,
              B=2, N=8, Hq=8, Hkv=2, D=128, S=64, scale=0.1, ku=1.0, w=FAKE,
@@ -212,7 +225,11 @@ def test_wrappers_match_their_signatures(monkeypatch):
     assert w.shape == (B, Hkv, S)
     kept, n = api.spec_kv_evict(w, i, cache, budget=5, recent=2)
     assert kept.shape == (B, Hkv, 5) and n.shape == (B,)
+    bits = torch.zeros(B, N, dtype=torch.int64)
+    bf = torch.zeros(B, Hkv, S, D, dtype=torch.bfloat16)
+    out, lse = api.spec_tree_attention_lse(q, bf, bf, i, bits)
+    assert out.shape == q.shape and lse.shape == (B, N, Hq)
     assert calls == ["spec_kv4_append", "spec_kv4_read",
                      "spec_tree_attention_kv4_workspace_bytes",
                      "spec_tree_attention_kv4", "spec_kv_weights",
-                     "spec_kv_evict"]
+                     "spec_kv_evict", "spec_tree_attention_lse"]

@@ -329,3 +329,43 @@ def test_eviction_replays_in_a_graph():
         assert kept[b, h, :len(want)].tolist() == want
         for t, o in zip(cache, moved):
             assert torch.equal(o[b, h, :len(want)], t[b, h, want])
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,prefix", [
+    (1, 4, 4, [0, 5]), (7, 8, 2, [1, 63]), (60, 16, 4, [130, 0]),
+    (33, 6, 3, [127, 129])])
+def test_bf16_attention_returns_its_normalisers(N, Hq, Hkv, prefix):
+    """spec_tree_attention_lse: out bit for bit spec_tree_attention's; lse the
+    oracle's within 2^-14 of the score magnitudes (float32 sums of 128
+    products at 2^-24 each, doubled) and 2^-18 for the sum and the logarithm;
+    then the weights of a bf16 cache sum to one per accepted row and head
+    (within the same bounds, 2^-12 relative here)."""
+    B, D = len(prefix), 128
+    S = max(prefix) + N + 9
+    rng = np.random.default_rng(N)
+    g = _gen(N)
+    q = torch.randn(B, N, Hq, D, generator=g, device="cuda").bfloat16()
+    k = torch.randn(B, Hkv, S, D, generator=g, device="cuda").bfloat16()
+    v = torch.randn(B, Hkv, S, D, generator=g, device="cuda").bfloat16()
+    parent = random_parent(rng, B, N)
+    parent[0] = np.arange(-1, N - 1)     # a chain in sequence 0
+    _, words = tree_mask(parent)
+    pre = _i32(prefix)
+    a = api()
+    base = a.spec_tree_attention(q, k, v, pre, _words(words), scale=0.09)
+    out, lse = a.spec_tree_attention_lse(q, k, v, pre, _words(words),
+                                         scale=0.09)
+    torch.cuda.synchronize()
+    assert torch.equal(out, base)
+    _, ref = kv4.attention(np64(q), np64(k), np64(v), prefix, words, 0.09)
+    mag = 0.09 * np.abs(np64(q)).sum(-1) * np.abs(np64(k)).max()
+    err = np.abs(lse.double().cpu().numpy() - ref)
+    assert (err <= 2.0 ** -14 * mag + 2.0 ** -18 * (1 + np.abs(ref))).all()
+    # sequence 0's chain is accepted whole, the others' nothing
+    lens = _i32([N] + [0] * (B - 1))
+    w = a.spec_kv_weights(q, k, lse, pre, lens, scale=0.09)
+    torch.cuda.synchronize()
+    total = w[0].double().sum(-1).cpu().numpy()
+    want = N * (Hq // Hkv)
+    assert np.allclose(total, want, rtol=2.0 ** -12)
+    assert (w[1:] == 0).all()
