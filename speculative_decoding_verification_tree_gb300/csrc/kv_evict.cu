@@ -147,13 +147,13 @@ __global__ void __launch_bounds__(kSelThreads)
 // weights_out may be weights: every weight is in a register before any is
 // written.
 template <int kPer>
-__global__ void __launch_bounds__(kPickThreads)
+__global__ void __launch_bounds__(kPickThreads, kPer <= 16 ? 2 : 1)
     evict_pick(const float* weights, const int32_t* __restrict__ length, int Hkv, int S,
                int budget, int recent, int64_t S_out, float* weights_out,
                int32_t* __restrict__ kept, int32_t* __restrict__ new_len) {
   launch_dependents();
   __shared__ int hist[2][256];          // this CTA's, by pass parity (read by the cluster)
-  __shared__ int copies[256][kCopies];
+  __shared__ __align__(16) int copies[256][kCopies];
   __shared__ int total[256];
   __shared__ int2 count_s;              // kept for sure, equal to the threshold (cluster)
   __shared__ int2 wcount[kPickWarps];
@@ -190,7 +190,30 @@ __global__ void __launch_bounds__(kPickThreads)
   // the top digits of the need-th largest key
   uint32_t prefix = 0;
   int want = need;  // how many of the keys that share the prefix are kept
-  for (int pass = 0; pass < 4 && need > 0; ++pass) {
+  const bool counted = C == 1 && steps == 1;
+  if (counted && need > 0) {
+    // one weight a thread: count the heavier ones instead (the need-th largest
+    // key is the one with fewer than `need` above it and not fewer at or above)
+    uint32_t* keys = reinterpret_cast<uint32_t*>(&copies[0][0]);
+    const int i = lo;
+    keys[i] = i < m ? order_key(v[0]) : 0u;  // 0 is below every key
+    __syncthreads();
+    const uint32_t mine = keys[i];
+    int above = 0, at_least = 0;
+    for (int j = 0; j < (m + 3) / 4; ++j) {
+      const uint4 q = reinterpret_cast<const uint4*>(keys)[j];
+      above += (q.x > mine) + (q.y > mine) + (q.z > mine) + (q.w > mine);
+      at_least += (q.x >= mine) + (q.y >= mine) + (q.z >= mine) + (q.w >= mine);
+    }
+    if (i < m && above < need && need <= at_least) {  // every holder of that key writes the same
+      prefix_s = mine;
+      want_s = need - above;
+    }
+    __syncthreads();
+    prefix = prefix_s;
+    want = want_s;
+  }
+  for (int pass = 0; pass < 4 && need > 0 && !counted; ++pass) {
     const int shift = 24 - 8 * pass;
     for (int i = threadIdx.x; i < 256 * kCopies; i += kPickThreads) (&copies[0][0])[i] = 0;
     __syncthreads();
