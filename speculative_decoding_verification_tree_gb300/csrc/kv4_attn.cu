@@ -819,10 +819,10 @@ size_t part_bytes(int B, int Hkv, int R, int D, int S) {
   return (size_t)2 * rows_warps<NT>(B, Hkv, R, S) * rows * (D + 2) * sizeof(float);
 }
 size_t attn_ws(int B, int Hkv, int R, int D, int S) {
+  if (R > kRowsMax) return kv4_tc_ws(B, Hkv, R, D, S);
   if (R <= 8) return part_bytes<1>(B, Hkv, R, D, S);
   if (R <= 16) return part_bytes<2>(B, Hkv, R, D, S);
-  if (R <= kRowsMax) return part_bytes<4>(B, Hkv, R, D, S);
-  return kv4_tc_ws(B, Hkv, R, D, S);
+  return part_bytes<4>(B, Hkv, R, D, S);
 }
 
 template <int D, int NT>
@@ -885,8 +885,9 @@ cudaError_t launch_rows(const Kv4Attn& a, void* ws, cudaStream_t st) {
 using namespace sv;
 
 // More than kRowsMax query rows per key/value head go to the tensor-core kernel
-// (kv4_attn_tc.cu).  Measured (32 sequences of 2 to 4 K keys, D 128): 32 rows
-// 78.5 us here, 92.8 us there; 36 rows 124 / 93 us.
+// (kv4_attn_tc.cu).  Measured (D 128): 32 sequences of 2 to 4 K keys, 16 rows
+// 48 us here and 78 there, 32 rows 76 / 73 us; 8 sequences of 32 K keys, 32 rows
+// 141 / 175 us.
 extern "C" size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D,
                                                           int S) {
   if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N ||

@@ -4,19 +4,24 @@
 // The mathematics and the numbers are kv4_attn.cu's (cache values exact in
 // fp16, rows of q scaled by powers of two, weights lifted by 2^7 and rounded
 // to fp16, everything else float32).  A CTA takes up to 256 query rows of one
-// (sequence, key/value head) as two 128-row tiles, and 64-key blocks of the
-// cache, or a share of them (splits, when there are fewer units than SMs):
+// (sequence, key/value head) as two 128-row tiles, or up to 128 as one, and
+// 64-key blocks of the cache, or a share of them (splits, when there are
+// fewer units than SMs):
 //   dequantisers (4 warps): the codes of the next blocks on their way from HBM
 //     in registers while block j's become fp16 rows in a ring of swizzled
 //     shared-memory stages (K and V as stored: a 64-dim row per 128 bytes);
-//   S issuers, P V issuers (one thread per tile each): S_t = Q_t K^T with Q_t
-//     read from TMEM, O_t += P_t V with P_t from shared memory;
-//   softmax (4 warps per tile, a thread per row): a running base-2 softmax
-//     against a reference maximum that moves only when a row's maximum grows
-//     by more than 2^8 (then O_t is rescaled in TMEM); two P buffers per tile.
-// TMEM (512 columns): Q_t at columns 64 t, S_t at 128 + 64 t, O_t at 256 +
-// 128 t.  Every mbarrier wait is bounded; a CTA that gives up stops waiting and
-// still frees its TMEM after waiting, bounded, for its own products.
+//   S issuers (two threads), P V issuers (one thread per tile): S = Q K^T with
+//     Q read from TMEM, O += P V with P from shared memory;
+//   softmax (8 warps, a thread per row): a running base-2 softmax against a
+//     reference maximum that moves only when a row's maximum grows by more
+//     than 2^8 (then O is rescaled in TMEM); two P buffers per tile.
+// With two tiles each has four softmax warps and one S buffer.  With one, two
+// groups of four warps take its blocks in turn, each with an S buffer of its
+// own, so that one group exponentiates while the other's scores are made; the
+// rows' references pass between the groups block by block.
+// TMEM (512 columns): Q_t at columns 64 t, S buffers at 128 and 192, O_t at 256
+// + 128 t.  Every mbarrier wait is bounded; a CTA that gives up stops waiting
+// and still frees its TMEM after waiting, bounded, for its own products.
 #include "kernels.h"
 #include "kv4.cuh"
 #include "kv4_attn.h"
@@ -27,12 +32,11 @@ namespace {
 
 constexpr int kKB = 64;         // keys per block
 constexpr int kMT = 128;        // query rows per tile
-constexpr int kTiles = 2;
-constexpr int kRowsCta = kTiles * kMT;
-constexpr int kTcStages = 4;
-constexpr int kAhead = 3;       // blocks that a dequantiser thread has in registers
+constexpr int kTcStages = 4;    // even: with one tile an S issuer takes every other block and must
+                                // meet every phase of its stages
+static_assert(kTcStages % 2 == 0, "see above");
 constexpr int kPTile = kMT * kKB * 2;
-constexpr int kSoftWarps = 4 * kTiles;
+constexpr int kSoftWarps = 8;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kDeqWarp = kSoftWarps;     // 4 warps
 constexpr int kCtlWarp = kSoftWarps + 4; // 4 warps
@@ -44,28 +48,40 @@ constexpr float kLift = 7.f;
 struct TcParams {
   Kv4Attn a;
   int gx, splits;   // row CTAs per (sequence, head); shares of its blocks
-  float* part;      // [unit][split][256][D], when splits > 1
-  float2* part_ml;  // [unit][split][256]
+  float* part;      // [unit][split][CTA's rows][D], when splits > 1
+  float2* part_ml;  // [unit][split][CTA's rows]
 };
 
+template <int kTiles>
 struct __align__(8) TcSmem {
   uint64_t kvfull[kTcStages], kvempty[kTcStages];
-  uint64_t sfull[kTiles], sfree[kTiles], pfull[kTiles][2], pdone[kTiles][2];
-  uint64_t qready, drain[kTiles][2];
+  uint64_t sfull[2], sfree[2];         // per S buffer
+  uint64_t pfull[2][2], pdone[2][2];   // per tile and P buffer
+  uint64_t turn[4][2];                 // one tile: per quadrant and group
+  uint64_t qready, drain[2][2];
   unsigned long long vnan[8];
+  static constexpr int kShared = kTiles == 1 ? kMT : 1;  // rows whose state groups share
+  float mref[kShared], rowf[kShared], lsum[2][kShared];
   uint32_t tmem_base;
   uint32_t dead;
   int seq;
 };
 
-template <int D>
+template <int D, int kTiles>
 struct TcCfg {
+  static constexpr int kNG = 2 / kTiles;            // softmax groups per tile
+  static constexpr int kRowsCta = kTiles * kMT;
   static constexpr int kHalf = kKB * 64 * 2;        // 64 keys x 64 dims
   static constexpr int kKVTile = kKB * D * 2;
   static constexpr int kStage = 2 * kKVTile;
   static constexpr int kOffP = kTcStages * kStage;
   static constexpr int kOffBar = kOffP + kTiles * 2 * kPTile;
-  static constexpr int kSmem = kOffBar + (int)sizeof(TcSmem) + 1024;
+  static constexpr int kSmem = kOffBar + (int)sizeof(TcSmem<kTiles>) + 1024;
+  // with the 1 KB the system keeps, within the 196 KB step of the L1 split:
+  // the next step leaves the loads 28 KB of L1 (two tiles: 117 us for 107)
+  static_assert(kSmem + 1024 <= 196 * 1024, "the L1 split");
+  // blocks that a dequantiser thread has in registers
+  static constexpr int kAhead = kTiles == 1 ? 4 : 3;
   // f16 operands, float32 D; S: M 128, N 64, both K-major; P V: N D, B MN-major
   static constexpr uint32_t kIdescS =
       (1u << 4) | ((uint32_t)(kKB >> 3) << 17) | ((uint32_t)(kMT >> 4) << 24);
@@ -73,7 +89,8 @@ struct TcCfg {
       (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kMT >> 4) << 24);
 };
 
-__device__ __forceinline__ void await(TcSmem& sm, uint64_t* bar, uint32_t parity) {
+template <class Sm>
+__device__ __forceinline__ void await(Sm& sm, uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return;
   if (*(volatile uint32_t*)&sm.dead) return;
   if (!mbar_wait_bounded(bar, parity)) *(volatile uint32_t*)&sm.dead = 1;
@@ -105,15 +122,17 @@ struct Raw {
   uint32_t ks, vs;
 };
 
-template <int D>
+template <int D, int kTiles>
 __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
-  using Cfg = TcCfg<D>;
+  using Cfg = TcCfg<D, kTiles>;
+  constexpr int kNG = Cfg::kNG, kRowsCta = Cfg::kRowsCta, kAhead = Cfg::kAhead;
   const Kv4Attn& p = prm.a;
   extern __shared__ __align__(1024) unsigned char araw[];
   const uint32_t raw = smem_u32(araw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   unsigned char* bp = araw + (base - raw);
-  TcSmem& sm = *reinterpret_cast<TcSmem*>(bp + Cfg::kOffBar);
+  using Sm = TcSmem<kTiles>;
+  Sm& sm = *reinterpret_cast<Sm*>(bp + Cfg::kOffBar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.Hq / p.Hkv, R = p.R, S = p.S, N = p.N;
   const int per_seq = prm.gx * prm.splits * p.Hkv;  // CTAs per sequence
@@ -157,9 +176,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
       mbar_init(&sm.kvfull[s], 128);
       mbar_init(&sm.kvempty[s], ntile);  // released by every tile's issuer
     }
-    for (int t = 0; t < kTiles; ++t) {
+    for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.sfull[t], 1);
       mbar_init(&sm.sfree[t], kMT);
+      for (int w = 0; w < 4; ++w) mbar_init(&sm.turn[w][t], 32);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.pfull[t][i], kMT);
         mbar_init(&sm.pdone[t][i], 1);
@@ -185,31 +205,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
 
   if (warp >= kCtlWarp) {
     const int t = (warp - kCtlWarp) & 1;
-    if (lane == 0 && t < ntile) {
+    if (lane == 0) {
       if (warp < kCtlWarp + 2) {
-        // ---------------------------------------------- tile t's S issuer
-        await(sm, &sm.qready, 0);
-        fence_after();
-        const uint32_t tq = tmem + (uint32_t)(64 * t);
-        const uint32_t ds = tmem + 128u + (uint32_t)(64 * t);
-        const uint64_t dk0 = desc_kmajor(base);
-        for (int j = 0; j < n; ++j) {
-          const int s = j % kTcStages;
-          await(sm, &sm.kvfull[s], (uint32_t)(j / kTcStages) & 1u);
-          if (j >= 1) await(sm, &sm.sfree[t], (uint32_t)((j - 1) & 1));
+        // ------------------------------------------------------ S issuers
+        // Two tiles: tile t's S of every block.  One: blocks t, t + 2, ...
+        // (buffer t).  k counts the buffer's uses.
+        if (kNG == 2 || t < ntile) {
+          await(sm, &sm.qready, 0);
           fence_after();
-          const uint64_t dk = dk0 + (uint64_t)((s * Cfg::kStage) >> 4);
+          const uint32_t tq = tmem + (uint32_t)(kNG == 2 ? 0 : 64 * t);
+          const uint32_t ds = tmem + 128u + (uint32_t)(64 * t);
+          const uint64_t dk0 = desc_kmajor(base);
+          int k = 0;
+          for (int j = kNG == 2 ? t : 0; j < n; j += kNG, ++k) {
+            const int s = j % kTcStages;
+            await(sm, &sm.kvfull[s], (uint32_t)(j / kTcStages) & 1u);
+            if (k >= 1) await(sm, &sm.sfree[t], (uint32_t)((k - 1) & 1));
+            fence_after();
+            const uint64_t dk = dk0 + (uint64_t)((s * Cfg::kStage) >> 4);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t koff = (uint32_t)((k >> 2) * Cfg::kHalf + (k & 3) * 32);
-            mma_f16_ts(ds, tq + (uint32_t)(8 * k), dk + (koff >> 4), Cfg::kIdescS,
-                       k > 0 ? 1u : 0u);
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t koff = (uint32_t)((i >> 2) * Cfg::kHalf + (i & 3) * 32);
+              mma_f16_ts(ds, tq + (uint32_t)(8 * i), dk + (koff >> 4), Cfg::kIdescS,
+                         i > 0 ? 1u : 0u);
+            }
+            mma_commit(&sm.sfull[t]);
           }
-          mma_commit(&sm.sfull[t]);
+          mma_commit(&sm.drain[t][0]);
+          mbar_wait_bounded(&sm.drain[t][0], 0);
         }
-        mma_commit(&sm.drain[t][0]);
-        mbar_wait_bounded(&sm.drain[t][0], 0);
-      } else {
+      } else if (t < ntile) {
         // -------------------------------------------- tile t's P V issuer
         const uint64_t dv0 = desc_mnmajor(base + Cfg::kKVTile, Cfg::kHalf);
         const uint64_t dp0 = desc_kmajor(base + Cfg::kOffP + (uint32_t)(2 * t * kPTile));
@@ -312,7 +337,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
     asm volatile("bar.arrive 3, %0;" ::"n"(kSoftThreads + 128) : "memory");
   } else {
     // ------------------------------------------------------------ softmax
-    const int t = warp >> 2;                  // tile
+    const int t = kTiles == 2 ? warp >> 2 : 0;   // tile
+    const int grp = kTiles == 2 ? 0 : warp >> 2;  // takes blocks grp, grp + kNG, ...
+    const int sb = kTiles == 2 ? t : grp;        // S buffer
     const int qd = warp & 3;                  // TMEM lane quadrant of this warp
     const int r = qd * 32 + lane;
     const int gr = row0 + t * kMT + r;
@@ -324,8 +351,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
                               : 0ull;
     const int64_t orow = ((int64_t)b * N + node) * p.Hq + hq;
     const uint32_t lanes = (uint32_t)(qd * 32) << 16;
-    float f;  // scores to base-2 exponents
-    {  // this row of q as fp16 into Q_t's TMEM lane
+    float f = 0.f;  // scores to base-2 exponents
+    if (grp == 0) {  // this row of q as fp16 into Q_t's TMEM lane
       const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * D);
       uint32_t w[D / 2];
       uint32_t top = 0;  // largest magnitude: bf16 magnitudes order like their bits
@@ -357,15 +384,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
       tst_wait();
       fence_before();
       f = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+      if (kNG == 2) {
+        sm.rowf[r] = f;
+        sm.mref[r] = neg_inf();
+      }
       mbar_arrive(&sm.qready);
     }
-    float m = neg_inf(), l = 0.f;
+    if constexpr (kNG == 2) {
+      named_sync(1, kMT * kNG);
+      f = sm.rowf[r];
+    }
+    float m = neg_inf(), l = 0.f;  // the reference that this thread's sum is against
     if (t < ntile) {
-      const uint32_t tS = tmem + lanes + 128u + (uint32_t)(64 * t);
+      const uint32_t tS = tmem + lanes + 128u + (uint32_t)(64 * sb);
       const uint32_t tO = tmem + lanes + 256u + (uint32_t)(128 * t);
       unsigned char* pt0 = bp + Cfg::kOffP + 2 * t * kPTile;
-      for (int j = 0; j < n; ++j) {
-        await(sm, &sm.sfull[t], (uint32_t)(j & 1));
+      for (int j = grp; j < n; j += kNG) {
+        await(sm, &sm.sfull[sb], (uint32_t)((j / kNG) & 1));
         __syncwarp();
         fence_after();
         float s[64];
@@ -381,7 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
           }
         }
         fence_before();
-        mbar_arrive(&sm.sfree[t]);  // the S issuer may write S_t of the next block
+        mbar_arrive(&sm.sfree[sb]);  // the S issuer may write the buffer's next block
         const int key0 = (j0 + j) * kKB;
         if (!valid || key0 + kKB > P) {
           const int npre = min(max(P - key0, 0), 64);
@@ -404,10 +439,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) bm4[c] = fmaxf(bm4[c], s[60 + c]);
         const float bm = fmaxf(fmax3f(bm4[0], bm4[1], bm4[2]), bm4[3]) * f;
-        const bool move = bm > m + 8.f;
-        const float mnew = move ? bm : m;
-        const float corr = (move && m != neg_inf()) ? ex2(m - mnew) : 1.f;
-        l *= corr;
+        float now = m;  // the row's reference after the block before
+        if constexpr (kNG == 2) {
+          if (j >= 1) {
+            await(sm, &sm.turn[qd][grp], (uint32_t)((grp ? (j >> 1) : (j >> 1) - 1) & 1));
+            now = *(volatile float*)&sm.mref[r];
+          }
+        }
+        const bool move = bm > now + 8.f;
+        const float mnew = move ? bm : now;
+        const float corr = (move && now != neg_inf()) ? ex2(now - mnew) : 1.f;
+        if constexpr (kNG == 2) {
+          if (move) *(volatile float*)&sm.mref[r] = mnew;
+          if (j + 1 < n) mbar_arrive(&sm.turn[qd][grp ^ 1]);
+          if (mnew != m) l *= ex2(m - mnew);  // m = -inf: l is 0
+        } else {
+          l *= corr;
+        }
         m = mnew;
         const float nm = m == neg_inf() ? kLift : kLift - m;
         uint32_t pk[32];
@@ -423,7 +471,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
         const float2 lsa = fadd2(ls4[0], ls4[1]);
         l += lsa.x + lsa.y;
         // P buffer j & 1 was read by the P V of block j - 2; a rescale of O_t
-        // needs the P V of block j - 1 done too
+        // needs the P V of block j - 1 done too (products complete in order, so
+        // after the first wait the second one's parity names block j - 1)
         const bool resc = j > 0 && __any_sync(0xffffffffu, corr != 1.f);
         if (j >= 2) await(sm, &sm.pdone[t][j & 1], (uint32_t)(((j - 2) >> 1) & 1));
         if (resc) await(sm, &sm.pdone[t][(j - 1) & 1], (uint32_t)(((j - 1) >> 1) & 1));
@@ -453,22 +502,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
       await(sm, &sm.drain[t][1], 0);
       fence_after();
     }
-    named_sync(3, kSoftThreads + 128);  // every note of a NaN block
+    named_sync(3, kSoftThreads + 128);  // every note of a NaN block, every row's last reference
     if (t < ntile) {
       const uint32_t tO = tmem + lanes + 256u + (uint32_t)(128 * t);
+      if constexpr (kNG == 2) {
+        const float last = *(volatile float*)&sm.mref[r];
+        if (last != m) l *= ex2(m - last);
+        m = last;
+        sm.lsum[grp][r] = l;
+        named_sync(1, kMT * kNG);
+        l = sm.lsum[0][r] + sm.lsum[1][r];
+      }
       float inv = 1.f;
       float* part = nullptr;
       if (prm.splits == 1) {
         inv = l == 0.f ? 0.f : p.v_unit / l;
-        if (valid && p.lse) p.lse[orow] = l == 0.f ? neg_inf() : m + log2f(l) - kLift;
+        if (valid && p.lse && grp == 0) p.lse[orow] = l == 0.f ? neg_inf() : m + log2f(l) - kLift;
       } else {
         const int64_t unit = ((int64_t)b * p.Hkv + kvh) * prm.gx + tile;
         const int64_t prow = (unit * prm.splits + split) * kRowsCta + t * kMT + r;
         part = prm.part + prow * D;
-        if (valid) prm.part_ml[prow] = make_float2(m, l);
+        if (valid && grp == 0) prm.part_ml[prow] = make_float2(m, l);
       }
+      // each group writes its share of the row
 #pragma unroll 1
-      for (int c = 0; c < D / 16; ++c) {
+      for (int c = grp * (D / 16 / kNG); c < (grp + 1) * (D / 16 / kNG); ++c) {
         uint32_t o[16];
         __syncwarp();
         if (n > 0) {
@@ -514,7 +572,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
 
 // Joins the splits: one warp per query row.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_tc_combine(const TcParams prm) {
+__global__ void __launch_bounds__(256) kv4_tc_combine(const TcParams prm, int kRowsCta) {
   const Kv4Attn& p = prm.a;
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -565,8 +623,10 @@ int tc_splits(int64_t units, int S) {
   return best;
 }
 
-template <int D>
+template <int D, int kTiles>
 cudaError_t launch_tc(const Kv4Attn& a, void* ws, cudaStream_t st) {
+  using Cfg = TcCfg<D, kTiles>;
+  constexpr int kRowsCta = Cfg::kRowsCta;
   TcParams prm;
   prm.a = a;
   prm.gx = (a.R + kRowsCta - 1) / kRowsCta;
@@ -575,15 +635,15 @@ cudaError_t launch_tc(const Kv4Attn& a, void* ws, cudaStream_t st) {
   prm.part = (float*)ws;
   prm.part_ml = (float2*)(prm.part + (size_t)units * prm.splits * kRowsCta * D);
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem((const void*)kv4_tc<D>, TcCfg<D>::kSmem, done);
+  cudaError_t e = allow_smem((const void*)kv4_tc<D, kTiles>, Cfg::kSmem, done);
   if (e != cudaSuccess) return e;
   prof_begin(SPEC_PROF_ATTN, st);
-  kv4_tc<D><<<(unsigned)(units * prm.splits), kTcThreads, TcCfg<D>::kSmem, st>>>(prm);
+  kv4_tc<D, kTiles><<<(unsigned)(units * prm.splits), kTcThreads, Cfg::kSmem, st>>>(prm);
   prof_end(SPEC_PROF_ATTN, st);
   e = cudaGetLastError();
   if (e != cudaSuccess || prm.splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)units, (unsigned)((min(a.R, kRowsCta) + 7) / 8));
+  cfg.gridDim = dim3((unsigned)units, (unsigned)(((a.R < kRowsCta ? a.R : kRowsCta) + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -591,19 +651,21 @@ cudaError_t launch_tc(const Kv4Attn& a, void* ws, cudaStream_t st) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_tc_combine<D>, prm);
+  return cudaLaunchKernelEx(&cfg, kv4_tc_combine<D>, prm, kRowsCta);
 }
 
 }  // namespace
 
 size_t kv4_tc_ws(int B, int Hkv, int R, int D, int S) {
-  const int64_t units = (int64_t)B * Hkv * ((R + kRowsCta - 1) / kRowsCta);
+  const int rows = R <= kMT ? kMT : 2 * kMT;
+  const int64_t units = (int64_t)B * Hkv * ((R + rows - 1) / rows);
   const int splits = tc_splits(units, S);
-  return splits == 1 ? 0 : (size_t)units * splits * kRowsCta * (D + 2) * sizeof(float);
+  return splits == 1 ? 0 : (size_t)units * splits * rows * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv4_tc(const Kv4Attn& a, int D, void* ws, cudaStream_t st) {
-  return D == 128 ? launch_tc<128>(a, ws, st) : launch_tc<64>(a, ws, st);
+  if (a.R <= kMT) return D == 128 ? launch_tc<128, 1>(a, ws, st) : launch_tc<64, 1>(a, ws, st);
+  return D == 128 ? launch_tc<128, 2>(a, ws, st) : launch_tc<64, 2>(a, ws, st);
 }
 
 }  // namespace sv
