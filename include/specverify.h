@@ -70,6 +70,7 @@ extern "C" {
 #define SPEC_MAX_TOP_K 128        /* tokens a truncating transform keeps   */
 #define SPEC_MAX_CHILDREN 64      /* children of one tree node             */
 #define SPEC_MAX_TREE_NODES 1024  /* N (tree) and K (chain)                */
+#define SPEC_MAX_POSITIONS (1 << 30) /* S of the 4-bit attention, the weights and the eviction */
 #define SPEC_EAGLE2_MAX_TOPK 32   /* children per expanded EAGLE-2 node    */
 #define SPEC_EAGLE2_MAX_WIDTH 2048 /* nodes kept per EAGLE-2 layer          */
 #define SPEC_EAGLE2_MAX_CANDIDATES 4096 /* EAGLE-2 candidates per sequence */
@@ -488,8 +489,9 @@ int spec_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales,
  * Workspace: spec_tree_attention_kv4_workspace_bytes(B, N, Hq, Hkv, D, S) bytes,
  * 256-byte aligned, uninitialised (0: none is needed, or the sizes are
  * invalid).
- * Errors: SPEC_ERR_SHAPE unless 1 <= N <= 64, Hq % Hkv == 0, S >= N and
- * B <= 65535, or when B * Hkv * ceil(N Hq / Hkv / 16) reaches 2^31;
+ * Errors: SPEC_ERR_SHAPE unless 1 <= N <= 64, Hq % Hkv == 0, N <= S <=
+ * SPEC_MAX_POSITIONS, B <= 65535 and N Hq / Hkv <= 2^30, or when
+ * B * Hkv * ceil(N Hq / Hkv / 16) reaches 2^31;
  * SPEC_ERR_UNSUPPORTED unless D is 64 or 128; SPEC_ERR_ARG for scale <= 0 or
  * not finite, a bad unit, a NULL pointer (B > 0), q, out or codes not 16-byte
  * aligned, scales or mask_bits not 8-byte aligned, prefix_len or lse not
@@ -530,7 +532,7 @@ int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
  * zeros), out [B, Hkv, S] float32; they may be the same array.
  * Each position's sum has a fixed order (no atomics).
  * Errors: as spec_tree_attention_kv4 (q and k 16-byte, k_scales 8-byte, the
- * rest 4-byte aligned), Hkv <= 65535.
+ * rest 4-byte aligned).
  */
 int spec_kv_weights(const void* q, const void* k, const uint8_t* k_scales,
                     const float* lse, const int32_t* prefix_len,
@@ -555,11 +557,12 @@ int spec_kv_weights(const void* q, const void* k, const uint8_t* k_scales,
  * kept [B, Hkv, budget] int32 (out): the kept positions, ascending, -1 padded.
  * new_len [B] int32 (out) = min(length, budget).
  * Rows behind the new length keep what they held.
- * Errors: SPEC_ERR_SHAPE for negative sizes, Hkv < 1, budget outside
- * [1, S_out], recent outside [0, budget], n_planes outside
+ * Errors: SPEC_ERR_SHAPE for negative sizes, Hkv < 1, S or S_out above
+ * SPEC_MAX_POSITIONS, budget outside [1, S_out], recent outside [0, budget], n_planes outside
  * [0, SPEC_EVICT_MAX_PLANES], row_bytes outside [1, 65536]; SPEC_ERR_ARG for
- * a NULL pointer (B > 0), a float or int array not 4-byte aligned, or an array
- * given in place with S_out != S.  B == 0 does nothing.
+ * a NULL pointer (B > 0), a float or int array not 4-byte aligned, an array
+ * given in place with S_out != S, or new_len == length (every head reads the
+ * lengths).  B == 0 does nothing.
  */
 #define SPEC_EVICT_MAX_PLANES 8
 int spec_kv_evict(const float* weights, const int32_t* length, int B, int Hkv,

@@ -31,6 +31,7 @@ SPEC_MAX_TOP_K = 128
 SPEC_MAX_CHILDREN = 64
 SPEC_MAX_TREE_NODES = 1024
 SPEC_EAGLE2_MAX_TOPK = 32
+SPEC_MAX_POSITIONS = 1 << 30
 SPEC_NOALLOC_MAX_ROWS = 8192
 SPEC_NOALLOC_MAX_PARTS = 65536
 

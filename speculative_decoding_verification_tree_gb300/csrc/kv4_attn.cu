@@ -891,10 +891,10 @@ using namespace sv;
 extern "C" size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D,
                                                           int S) {
   if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N ||
-      (D != 64 && D != 128))
+      S > SPEC_MAX_POSITIONS || (D != 64 && D != 128))
     return 0;
   const int64_t R = (int64_t)N * (Hq / Hkv);
-  if (B == 0 || (int64_t)B * Hkv * ((R + 15) / 16) > 2147483647) return 0;
+  if (B == 0 || R > (1 << 30) || (int64_t)B * Hkv * ((R + 15) / 16) > 2147483647) return 0;
   return (attn_ws(B, Hkv, (int)R, D, S) + 255) / 256 * 256;
 }
 
@@ -905,7 +905,8 @@ extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
                                        int D, int S, float scale, float k_unit, float v_unit,
                                        void* out, float* lse, void* workspace, size_t ws_bytes,
                                        void* stream) {
-  if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N)
+  if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N ||
+      S > SPEC_MAX_POSITIONS)
     return SPEC_ERR_SHAPE;
   if (D != 64 && D != 128) return SPEC_ERR_UNSUPPORTED;
   if (!(scale > 0.f) || !(scale < 3.4e38f) || !kv4_unit_ok(k_unit) || !kv4_unit_ok(v_unit))
@@ -919,7 +920,8 @@ extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
     return SPEC_ERR_ARG;
   const int64_t R = (int64_t)N * (Hq / Hkv);
   const int64_t tiles = (R + 15) / 16;
-  if ((int64_t)B * Hkv * tiles > 2147483647 || (double)B * Hkv * S > 4.0e15) return SPEC_ERR_SHAPE;
+  if (R > (1 << 30) || (int64_t)B * Hkv * tiles > 2147483647 || (double)B * Hkv * S > 4.0e15)
+    return SPEC_ERR_SHAPE;
   const size_t need = attn_ws(B, Hkv, (int)R, D, S);
   if (need > 0 && (!workspace || (uintptr_t)workspace % 256 != 0 || ws_bytes < need))
     return SPEC_ERR_WORKSPACE;

@@ -530,10 +530,14 @@ extern "C" int spec_kv_evict(const float* weights, const int32_t* length, int B,
                              int budget, int recent, int n_planes, const void* const* planes,
                              void* const* planes_out, const int* row_bytes, int S_out,
                              float* weights_out, int32_t* kept, int32_t* new_len, void* stream) {
-  if (B < 0 || Hkv < 1 || S < 0 || S_out < 0 || budget < 1 || budget > S_out || recent < 0 ||
+  if (B < 0 || Hkv < 1 || S < 0 || S_out < 0 || S > SPEC_MAX_POSITIONS ||
+      S_out > SPEC_MAX_POSITIONS || budget < 1 || budget > S_out || recent < 0 ||
       recent > budget || n_planes < 0 || n_planes > SPEC_EVICT_MAX_PLANES)
     return SPEC_ERR_SHAPE;
-  if ((double)B * Hkv > 2147483647.0) return SPEC_ERR_SHAPE;
+  // (sequence, head) pairs and the gather's chunks are grid dimensions
+  if ((double)B * Hkv * kMaxCluster > 2147483647.0 ||
+      (double)B * Hkv * budget > 2147483647.0 * 512)
+    return SPEC_ERR_SHAPE;
   if (n_planes > 0 && (!planes || !planes_out || !row_bytes)) return SPEC_ERR_ARG;
   for (int i = 0; i < n_planes; ++i)
     if (row_bytes[i] < 1 || row_bytes[i] > 65536) return SPEC_ERR_SHAPE;
@@ -548,12 +552,12 @@ extern "C" int spec_kv_evict(const float* weights, const int32_t* length, int B,
     if (!planes[i] || !planes_out[i]) return SPEC_ERR_ARG;
     if (planes[i] == planes_out[i] && S_out != S) return SPEC_ERR_ARG;
   }
-  if (weights_out == weights && S_out != S) return SPEC_ERR_ARG;
+  if ((weights_out == weights && S_out != S) || new_len == length) return SPEC_ERR_ARG;
   const int64_t pairs = (int64_t)B * Hkv;
   cudaStream_t st = (cudaStream_t)stream;
   const int C = pick_cluster(pairs, S);
   cudaError_t e;
-  if (C > 0 && pairs * C <= 2147483647) {
+  if (C > 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * C));
     cfg.blockDim = dim3(kPickThreads);

@@ -382,8 +382,9 @@ extern "C" int spec_kv_weights(const void* q, const void* k, const uint8_t* k_sc
                                const int32_t* path_len, const int32_t* path_nodes, int B, int N,
                                int Hq, int Hkv, int D, int S, float scale, float k_unit,
                                const float* weights, float* out, void* stream) {
-  if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hkv > 65535 ||
-      Hq % Hkv != 0 || S < N)
+  if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N ||
+      S > SPEC_MAX_POSITIONS || (int64_t)N * (Hq / Hkv) > (1 << 30) ||
+      (double)B * Hkv * S > 4.0e15)
     return SPEC_ERR_SHAPE;
   if (D != 64 && D != 128) return SPEC_ERR_UNSUPPORTED;
   if (!(scale > 0.f) || !(scale < 3.4e38f) || !kv4_unit_ok(k_unit)) return SPEC_ERR_ARG;

@@ -68,7 +68,8 @@ def test_attention_argument_errors(lib):
                        B, N, Hq, Hkv, D, S, scale, ku, vu, out, lse, ws,
                        nbytes, None)
     for kw in (dict(B=-1), dict(B=65536), dict(N=0), dict(N=65), dict(Hq=7),
-               dict(Hkv=0), dict(S=7), dict(B=65535, Hq=1 << 30, Hkv=1 << 30)):
+               dict(Hkv=0), dict(S=7), dict(S=(1 << 30) + 1),
+               dict(Hq=1 << 30, Hkv=1), dict(B=65535, Hq=1 << 30, Hkv=1 << 30)):
         assert call(**kw) == lib.SPEC_ERR_SHAPE, kw
     assert call(D=32) == lib.SPEC_ERR_UNSUPPORTED
     for kw in (dict(scale=0.0), dict(scale=float("nan")),
@@ -104,8 +105,8 @@ def test_weights_argument_errors(lib):
              out=FAKE):
         return lib.raw("spec_kv_weights", q, k, ks, lse, pre, n, nodes, B, N,
                        Hq, Hkv, D, S, scale, ku, w, out, None)
-    for kw in (dict(B=-1), dict(B=65536), dict(Hq=65536, Hkv=65536),
-               dict(N=0), dict(N=65), dict(Hq=7), dict(S=7)):
+    for kw in (dict(B=-1), dict(B=65536), dict(Hq=1 << 30, Hkv=1),
+               dict(S=(1 << 30) + 1), dict(N=0), dict(N=65), dict(Hq=7), dict(S=7)):
         assert call(**kw) == lib.SPEC_ERR_SHAPE, kw
     assert call(D=80) == lib.SPEC_ERR_UNSUPPORTED
     for kw in (dict(scale=-1.0), dict(ku=1.5), dict(ks=None, ku=2.0),
@@ -133,9 +134,11 @@ def test_evict_argument_errors(lib):
                dict(budget=0), dict(budget=33), dict(recent=-1),
                dict(recent=17), dict(n_planes=-1), dict(n_planes=9),
                dict(rows=(0,)), dict(rows=(65537,)),
-               dict(B=65536, Hkv=65536)):
+               dict(B=65536, Hkv=65536), dict(S=(1 << 30) + 1),
+               dict(S_out=(1 << 30) + 1)):
         assert call(**kw) == lib.SPEC_ERR_SHAPE, kw
-    for kw in (dict(w=None), dict(n=None), dict(kept=None), dict(new=None),
+    for kw in (dict(n=ODD4, new=ODD4),                 # lengths in place
+               dict(w=None), dict(n=None), dict(kept=None), dict(new=None),
                dict(planes=(None,)), dict(outs=(None,)), dict(arrays=False),
                dict(w=ODD2), dict(n=ODD2), dict(kept=ODD2), dict(new=ODD2),
                dict(wo=ODD2), dict(wo=FAKE),           # in place, S_out != S

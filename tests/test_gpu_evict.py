@@ -369,3 +369,63 @@ def test_bf16_attention_returns_its_normalisers(N, Hq, Hkv, prefix):
     want = N * (Hq // Hkv)
     assert np.allclose(total, want, rtol=2.0 ** -12)
     assert (w[1:] == 0).all()
+
+
+def test_calls_on_two_streams_at_once():
+    """Every operator with a stream of its own, two sets in flight at the same
+    time, equal to the same calls one after the other."""
+    a = api()
+    N, Hq, Hkv, D, S = 3, 8, 2, 128, 5000
+
+    def step(seed, stream):
+        g = _gen(seed)
+        mk = lambda n, h: torch.randn(1, n, h, D, generator=g, device="cuda"
+                                      ).bfloat16()
+        k, v, q = mk(S - 10, Hkv), mk(S - 10, Hkv), mk(N, Hq)
+        pre = _i32([S - 10 - N])
+        words = _words([[1, 3, 5]])
+        cache = a.kv4_cache(1, Hkv, S, D)
+        small = a.kv4_cache(1, Hkv, 512, D)
+        zero, lens = _i32([0]), _i32([2])
+        torch.cuda.synchronize()
+        for _ in range(3):
+            a.spec_kv4_append(k, v, zero, cache, stream=stream)
+            out, lse = a.spec_tree_attention_kv4(q, cache, pre, words, lse=True,
+                                                 stream=stream)
+            w = a.spec_kv_weights(q, cache, lse, pre, lens, stream=stream)
+            kept, n = a.spec_kv_evict(w, pre, cache, budget=512, recent=100,
+                                      planes_out=small, stream=stream)
+            rk, rv = a.spec_kv4_read(small, zero, 512, stream=stream)
+        return out, lse, w, kept, n, rk, rv
+
+    s = [torch.cuda.Stream() for _ in range(2)]
+    both = [step(i, s[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        alone = step(i, s[i])
+        torch.cuda.synchronize()
+        for x, y in zip(both[i], alone):
+            assert torch.equal(x, y)
+
+
+def test_views_and_host_tensors_are_refused():
+    a = api()
+    cache = a.kv4_cache(1, 2, 64, 128)
+    k = torch.zeros(1, 4, 2, 128, dtype=torch.bfloat16, device="cuda")
+    z = _i32([0])
+    with pytest.raises(ValueError, match="contiguous"):
+        a.spec_kv4_append(k.transpose(1, 2).contiguous().transpose(1, 2), k, z,
+                          cache)
+    with pytest.raises(ValueError):
+        a.spec_kv4_append(k, k, z.cpu(), cache)
+    w = torch.zeros(1, 2, 64, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        a.spec_kv_evict(w.transpose(1, 2).contiguous().transpose(1, 2), z,
+                        cache, budget=4, recent=0)
+    from speculative_decoding_verification_tree_gb300 import SpecError
+    with pytest.raises(SpecError):
+        a.spec_kv_evict(w, z, cache, budget=65, recent=0)   # more than S
+    with pytest.raises(SpecError):
+        a.spec_kv_evict(w, z, cache, budget=4, recent=0, new_len=z)
+    with pytest.raises(SpecError):
+        a.spec_kv4_append(k, k, z, cache, k_unit=0.3)

@@ -223,6 +223,8 @@ def test_append_special_values_and_positions_outside():
     (64, 2, 2, [200, 191]),         # full mask words
     (33, 6, 3, [127, 129]),
     (27, 14, 2, [95, 300]),         # 189 rows, seven per head
+    (64, 16, 2, [190, 40]),         # 512 rows: two CTAs a head
+    (5, 8, 1, [64, 255]),           # forty rows
 ])
 def test_tree_attention_kv4_matches_oracle(N, Hq, Hkv, prefix, D):
     B = len(prefix)
@@ -244,6 +246,8 @@ def test_tree_attention_kv4_matches_oracle(N, Hq, Hkv, prefix, D):
     (1, 4, 2, 300, 0, 90),        # more sequences than threads
     (1, 4, 1, 1, 20000, 20000),   # one long sequence over many pieces
     (20, 8, 2, 3, 1500, 5000),    # tree rows over long ragged prefixes
+    (60, 4, 1, 2, 2000, 6000),    # 240 rows, shares of a long prefix joined
+    (6, 4, 1, 1, 30000, 30000),   # 24 rows over many pieces
 ])
 def test_ragged_batches_and_split_sequences(N, Hq, Hkv, B, lo, hi):
     rng = np.random.default_rng(B + hi)
@@ -275,19 +279,25 @@ def test_large_and_small_query_rows_and_units():
     check_attention(out, lse, q, vals, [P], words, 0.5)
 
 
-def test_growing_scores_rescale():
+@pytest.mark.parametrize("N", [1, 2, 4, 10, 40])   # 8 to 320 rows
+@pytest.mark.parametrize("D", [64, 128])
+def test_growing_scores_rescale(N, D):
     # keys ordered so that the running maximum grows again and again
-    B, N, Hq, Hkv, D, P = 1, 1, 8, 1, 64, 3000
+    B, Hq, Hkv, P = 1, 8, 1, 1500
     cache, vals = make_cache(4, B, Hkv, P + N, D)
-    order = np.argsort(vals[0][0, 0].sum(-1))
+    order = np.concatenate([np.argsort(vals[0][0, 0, :P].sum(-1)),
+                            np.arange(P, P + N)])
     cache = api().KV4Cache(*[t[:, :, torch.from_numpy(order).cuda()].contiguous()
                              for t in cache])
     vals = tuple(x[:, :, order] for x in vals)
-    q = torch.ones(B, N, Hq, D, device="cuda").bfloat16()
+    q = torch.ones(B, N, Hq, D, device="cuda")
+    q *= torch.linspace(0.25, 1.5, N * Hq, device="cuda").reshape(1, N, Hq, 1)
+    q = q.bfloat16()
+    words = [[(1 << (i + 1)) - 1 for i in range(N)]]
     out, lse = api().spec_tree_attention_kv4(
-        q, cache, _i32([P]), _words([[1]]), scale=3.0, v_unit=0.125, lse=True)
+        q, cache, _i32([P]), _words(words), scale=2.0, v_unit=0.125, lse=True)
     torch.cuda.synchronize()
-    check_attention(out, lse, q, vals, [P], [[1]], 3.0)
+    check_attention(out, lse, q, vals, [P], words, 2.0)
 
 
 def test_rows_that_see_nothing_and_clamped_prefix():
@@ -308,7 +318,8 @@ def test_rows_that_see_nothing_and_clamped_prefix():
     assert torch.equal(again, out)
 
 
-@pytest.mark.parametrize("N,Hq,Hkv", [(6, 2, 2), (40, 8, 2)])
+@pytest.mark.parametrize("N,Hq,Hkv", [(6, 2, 2), (12, 4, 1), (20, 8, 2),
+                                      (40, 8, 2)])
 def test_nan_of_a_drafted_position_stays_on_its_branch(N, Hq, Hkv):
     D, P = 128, 70
     parent = np.array([[-1] + [max(0, (j - 1) // 2) for j in range(1, N)]])
