@@ -48,11 +48,10 @@ namespace sv {
 namespace {
 
 constexpr int kKeys = 32;       // keys per stage
-constexpr int kMinBlocks = 2;   // a warp's smallest piece
+constexpr int kMinBlocks = 6;   // a warp's smallest piece (a join reads every piece's output)
 constexpr float kLift = 7.f;    // log2 of the factor that lifts P
 constexpr int kSms = 152;
 constexpr int kRowsMax = 32;    // query rows up to which these kernels are used
-constexpr int kJoinWarps = 8;   // warps of a kv4_combine CTA
 constexpr int kJoinUnroll = 10; // 32-part groups read at once
 
 struct RowsParams : Kv4Attn {
@@ -672,7 +671,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
 // rows of a unit, kJoinWarps / per_cta warps a row.  The units are all of
 // them, or, when there are more units than piece borders, those that hold a
 // border, each found from the first border inside it.
-template <int D, int RT>
+template <int D, int RT, int kJoinWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     kv4_combine(const RowsParams p, bool by_border, int per_cta) {
   constexpr int kThreads = kJoinWarps * 32;
@@ -872,11 +871,18 @@ cudaError_t launch_rows(const Kv4Attn& a, void* ws, cudaStream_t st) {
   const bool by_border = units > p.warps - 1;
   const int64_t joins = by_border ? p.warps - 1 : units;
   const int per_cta = joins * p.rows <= 2 * kSms ? 1 : p.rows;
+  // a row of a long unit has many parts: sixteen warps read them; elsewhere
+  // eight warps share the rows (one sequence of 128 K keys 43 -> 41 us, 64 of
+  // 32 K 381 us against 390 with sixteen)
   cfg.gridDim = dim3((unsigned)joins, (unsigned)((p.rows + per_cta - 1) / per_cta));
-  cfg.blockDim = dim3(kJoinWarps * 32);
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_combine<D, RT>, p, by_border, per_cta);
+  if (per_cta == 1) {
+    cfg.blockDim = dim3(16 * 32);
+    return cudaLaunchKernelEx(&cfg, kv4_combine<D, RT, 16>, p, by_border, per_cta);
+  }
+  cfg.blockDim = dim3(8 * 32);
+  return cudaLaunchKernelEx(&cfg, kv4_combine<D, RT, 8>, p, by_border, per_cta);
 }
 
 }  // namespace

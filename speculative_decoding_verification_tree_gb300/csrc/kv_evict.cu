@@ -28,6 +28,7 @@ constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kPickMost = 32;     // weights a thread holds
 constexpr int kCopies = 8;        // histogram copies
 constexpr int kMaxCluster = 16;
+constexpr int kCountMost = 192;   // weights up to which counting beats the radix passes
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;
 constexpr int kSweepUnroll = 4;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kPickThreads, kPer <= 16 ? 2 : 1)
   // the top digits of the need-th largest key
   uint32_t prefix = 0;
   int want = need;  // how many of the keys that share the prefix are kept
-  const bool counted = C == 1 && steps == 1;
+  const bool counted = C == 1 && steps == 1 && m <= kCountMost;
   if (counted && need > 0) {
     // one weight a thread: count the heavier ones instead (the need-th largest
     // key is the one with fewer than `need` above it and not fewer at or above)
@@ -200,7 +201,8 @@ __global__ void __launch_bounds__(kPickThreads, kPer <= 16 ? 2 : 1)
     __syncthreads();
     const uint32_t mine = keys[i];
     int above = 0, at_least = 0;
-    for (int j = 0; j < (m + 3) / 4; ++j) {
+    const int quads = i - lane < m ? (m + 3) / 4 : 0;  // a warp without positions counts nothing
+    for (int j = 0; j < quads; ++j) {
       const uint4 q = reinterpret_cast<const uint4*>(keys)[j];
       above += (q.x > mine) + (q.y > mine) + (q.z > mine) + (q.w > mine);
       at_least += (q.x >= mine) + (q.y >= mine) + (q.z >= mine) + (q.w >= mine);
