@@ -14,10 +14,13 @@
 // before the conversion, which puts equal ones back on the border and moves
 // none across it.
 //
-// One thread takes one block at a time: 32 bytes in, 9 out.  Pure streaming,
-// bound by HBM.  A CTA's rows are consecutive positions of a head (the next
-// head's after the last), so that the codes and scales it writes are contiguous
-// while each row it reads is a whole 128- or 256-byte line.
+// One thread takes two blocks, 32 bytes in and 9 out each, all loads first.  A
+// CTA's rows are consecutive positions of a head (the next head's after the
+// last), so that the codes and scales it writes are contiguous while each row
+// it reads is a whole 128- or 256-byte line.  Streaming: the bound is HBM, with
+// instruction issue close behind (82% of its slots, cold caches).  4 x 8192
+// positions of 8 heads, D 128 (172 MB): 33 us, 5.2 TB/s, written and 33 us read
+// back.  The same rounding in packed arithmetic took the same time.
 #include "kernels.h"
 #include "kv4.cuh"
 

@@ -36,6 +36,13 @@
 // line, cut into equal pieces, one per warp, whatever the sequences' lengths; a
 // unit cut by a piece border leaves partial (m, l, O) in the workspace, and
 // kv4_combine joins them.  Warps never wait for one another.
+// Short work, where the join's launch and traffic would cost more than idle
+// warps, takes kv4_unit instead: a cluster of CTAs per unit, its warps' results
+// joined through distributed shared memory (unit_cluster has the rule).
+// Bounds and times (D 128, 32 / 8 heads, single tokens): 64 sequences of 32 K
+// keys, 2.39 GB of cache, 381 us = 6.3 TB/s, HBM; 32 of 2 to 4 K keys, 114 MB, 32
+// us = 3.6 TB/s, issue (55%) and the load latency of a unit's first and last
+// blocks; one sequence of 1 K keys 6.4 us, launch and one block's latency.
 #include <cuda_runtime.h>
 #include <stddef.h>
 
@@ -793,10 +800,10 @@ int rows_warps(int B, int Hkv, int R, int S) {
 // CTAs per cluster of kv4_unit, or 0 for pieces of the line.  Units leave
 // some of the resident CTAs idle, or the last wave part empty, for as many
 // 32-key blocks a warp as the longest unit may have; pieces cost the join's
-// launch and partial outputs.  Measured (32 / 8 heads, D 128): units 10.9 us,
-// pieces 15.1 us at one sequence of 1 K keys, 15.0 / 19.1 at 8 K, 27.3 / 25.2
-// at 32 K, 81 / 48 at 128 K; 32 sequences of up to 4 K 35.6 / 39.6, 64 of them
-// 62.1 / 61.1, 64 of 32 K 442 / 388.
+// launch and partial outputs.  Measured (32 / 8 heads, D 128): units 6.4 us,
+// pieces 15.9 us at one sequence of 1 K keys, 9.6 / 17.0 at 8 K, 22.2 / 21.6
+// at 32 K, 75.8 / 40.6 at 128 K; 32 sequences of up to 4 K 31.7 / 34.3, 64 of
+// them 57.4 / 55.5, 64 of 32 K 438 / 381.
 template <int NT>
 int unit_cluster(int64_t units, int S) {
   constexpr int64_t slots = kSms * RowsCfg<NT>::kCtas;
@@ -892,8 +899,8 @@ using namespace sv;
 
 // More than kRowsMax query rows per key/value head go to the tensor-core kernel
 // (kv4_attn_tc.cu).  Measured (D 128): 32 sequences of 2 to 4 K keys, 16 rows
-// 48 us here and 78 there, 32 rows 76 / 73 us; 8 sequences of 32 K keys, 32 rows
-// 141 / 175 us.
+// 48 us here and 73 there, 20 rows 72 / 73, 32 rows 75 / 72 us; 8 sequences of
+// 32 K keys, 32 rows 141 / 165 us; one of 1 K keys 15 / 14 us.
 extern "C" size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D,
                                                           int S) {
   if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N ||

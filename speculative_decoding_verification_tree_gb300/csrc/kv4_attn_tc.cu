@@ -19,6 +19,11 @@
 // groups of four warps take its blocks in turn, each with an S buffer of its
 // own, so that one group exponentiates while the other's scores are made; the
 // rows' references pass between the groups block by block.
+// Bound: the softmax warps and the single S buffer of a tile.  32 sequences of 2
+// to 4 K keys, 240 rows (60 nodes, 4 heads a group), D 128: 107 us = 920 TFLOP/s,
+// 1.2 TB/s; per 64-key block of a tile about 1930 cycles, of which the products
+// take 1250 of the tensor pipe for both tiles.  One tile: 64 rows 73 us, 128 rows
+// 73 us (as half of a two-tile CTA 87 and 79 us).
 // TMEM (512 columns): Q_t at columns 64 t, S buffers at 128 and 192, O_t at 256
 // + 128 t.  Every mbarrier wait is bounded; a CTA that gives up stops waiting
 // and still frees its TMEM after waiting, bounded, for its own products.
@@ -607,7 +612,9 @@ __global__ void __launch_bounds__(256) kv4_tc_combine(const TcParams prm, int kR
 
 // Shares of a unit's blocks: the number that fills the SMs best, counted in
 // blocks of the longest unit (a CTA's start costs about three, the join's launch
-// and traffic about eight).
+// and traffic about eight).  Measured with this rule and unsplit: 240 rows, one
+// sequence of 128 K keys 127 us / 1896 us, of 1 K keys 25.3 / 25.2; five ragged
+// ones of up to 5 K keys, 2 heads, D 64 18.7 / 77.4.
 int tc_splits(int64_t units, int S) {
   const int64_t blocks = (S + kKB - 1) / kKB;
   int best = 1;

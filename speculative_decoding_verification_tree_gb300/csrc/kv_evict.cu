@@ -15,6 +15,11 @@
 // head)'s rows and walks it in chunks, each read whole before it is written.
 // That is safe because kept[j] >= j, so a chunk's writes reach no position
 // that a later chunk still has to read.
+// Bounds and times: 32 sequences of 2 to 4 K positions, 8 heads, 4-bit rows of D
+// 128, half kept (159 MB): 41 us, of which the pick about 13 (latency of its four
+// passes) and the gather 28 (HBM, and the sectors of 64-byte rows); one sequence
+// of 128 K positions, 8 heads, bf16 rows, 16 K kept (139 MB): 44 us, pick and
+// gather about half each.
 #include "kernels.h"
 #include "common.cuh"
 
@@ -28,7 +33,9 @@ constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kPickMost = 32;     // weights a thread holds
 constexpr int kCopies = 8;        // histogram copies
 constexpr int kMaxCluster = 16;
-constexpr int kCountMost = 192;   // weights up to which counting beats the radix passes
+// weights up to which every weight's rank is counted instead (256 pairs of 170
+// positions: 8.9 us counted, 10.4 with the radix passes; slower above about 200)
+constexpr int kCountMost = 192;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;
 constexpr int kSweepUnroll = 4;
@@ -514,7 +521,8 @@ cudaError_t launch_moves(const MovePlanes& out, int n_out, const MovePlanes& in,
 
 // CTAs per cluster of evict_pick for caches of S positions, or 0 (evict_select):
 // enough registers for the weights, and more CTAs, of at least 2048 weights
-// each, when there are few (sequence, head) pairs.
+// each, when there are few (sequence, head) pairs (8 pairs of 32 K weights 17.6
+// us, 26.7 in the fewest CTAs; of 4 K 11.9 / 11.8).
 int pick_cluster(int64_t pairs, int S) {
   int C = 1;
   while ((int64_t)C * kPickThreads * kPickMost < S && C < kMaxCluster) C *= 2;
@@ -570,6 +578,8 @@ extern "C" int spec_kv_evict(const float* weights, const int32_t* length, int B,
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    // the fewest registers that hold the weights: more CTAs per SM (256 pairs of 4 K
+    // weights 41.0 us, 44.7 with the largest form; of 1 K 13.7 / 18.0)
     const int64_t per = (S + (int64_t)C * kPickThreads - 1) / ((int64_t)C * kPickThreads);
     if (C > 8) {  // more than the portable cluster size
       e = cudaFuncSetAttribute(evict_pick<kPickMost>, cudaFuncAttributeNonPortableClusterSizeAllowed,
