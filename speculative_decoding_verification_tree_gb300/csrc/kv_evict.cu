@@ -4,22 +4,29 @@
 //
 // Weights are mapped to unsigned keys that order like them (NaN as -inf, -0 as
 // +0).  evict_pick, one cluster of CTAs per (sequence, head), reads each weight
-// once into a register: a radix select over four 8-bit digits (histograms with
-// a copy per lane residue, summed over the cluster) finds the smallest kept
-// key and how many positions holding it are kept (the lowest ones); then each
-// warp writes the kept positions, and their weights, of its run of the line, in
-// order.  Caches too long for a cluster's registers take evict_select, one CTA
-// that reads the weights from memory in every pass.
+// once into shared memory; a thread owns up to 32 consecutive positions, with a
+// bit each for kept and undecided.  A radix select over at most four 8-bit
+// digits (histograms with a copy per lane residue, summed over the cluster)
+// finds the smallest kept key and how many positions holding it are kept (the
+// lowest ones); a pass looks at undecided positions only, and there is none
+// after the digit whose holders are all kept.  Counts of kept positions, summed
+// over lanes, warps and cluster, give each its place; a list in shared memory
+// makes the stores of positions and weights contiguous.  Caches too long for a
+// cluster's shared memory take evict_select, one CTA that reads the weights from
+// memory in every pass.
 // The gather: a plane is moved by one thread per word of a kept row when it
 // goes to another buffer; in place, a CTA takes a column slice of a (sequence,
 // head)'s rows and walks it in chunks, each read whole before it is written.
 // That is safe because kept[j] >= j, so a chunk's writes reach no position
 // that a later chunk still has to read.
-// Bounds and times: 32 sequences of 2 to 4 K positions, 8 heads, 4-bit rows of D
-// 128, half kept (159 MB): 41 us, of which the pick about 13 (latency of its four
-// passes) and the gather 28 (HBM, and the sectors of 64-byte rows); one sequence
-// of 128 K positions, 8 heads, bf16 rows, 16 K kept (139 MB): 44 us, pick and
-// gather about half each.
+// Bounds and times (pick: latency of its barriers, cluster exchanges and passes;
+// gather: HBM): 32 sequences of 2 to 4 K positions, 8 heads, 4-bit rows of D 128,
+// half kept (159 MB): 39 us, 12 of them the pick; the gather also pays for the
+// other halves of 128-byte lines.  One sequence of 128 K positions, 8 heads, bf16
+// rows, 16 K kept (139 MB): 38.5 us, about 14 of them the pick; the pick of 208
+// pairs of 45 K weights: 48 us.  (Weights in registers, with whole scans in every
+// pass, took 41, 44 and 95: instruction fetch of the unrolled code, one CTA per
+// SM.)
 #include "kernels.h"
 #include "common.cuh"
 
@@ -30,22 +37,30 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kPickMost = 32;     // weights a thread holds
-constexpr int kCopies = 8;        // histogram copies
+constexpr int kPickMost = 32;     // weights of a thread, at most: a bit each
+constexpr int kCopies = 4;        // histogram copies
 constexpr int kMaxCluster = 16;
-// weights up to which every weight's rank is counted instead (256 pairs of 170
-// positions: 8.9 us counted, 10.4 with the radix passes; slower above about 200)
-constexpr int kCountMost = 192;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;
 constexpr int kSweepUnroll = 4;
 constexpr int kMaxPlanes = 9;  // SPEC_EVICT_MAX_PLANES and the weights
 
+// Orders like w, NaN as -inf and -0 as +0 (the sum and the maximum see to that).
 __device__ __forceinline__ uint32_t order_key(float w) {
-  uint32_t u = __float_as_uint(w);
-  if ((u & 0x7fffffffu) > 0x7f800000u) u = 0xff800000u;
-  if (u == 0x80000000u) u = 0u;
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(fmaxf(w + 0.f, neg_inf()));
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ void copy4(float* to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from)
+               : "memory");
+}
+// The lowest n bits, n clamped to [0, 32].
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+__device__ __forceinline__ void copy4_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(kSelThreads)
@@ -152,21 +167,22 @@ __global__ void __launch_bounds__(kSelThreads)
 }
 
 // The kept positions of one (sequence, head) and their weights.
-// weights_out may be weights: every weight is in a register before any is
+// weights_out may be weights: every weight is in shared memory before any is
 // written.
-template <int kPer>
-__global__ void __launch_bounds__(kPickThreads, kPer <= 16 ? 2 : 1)
+__global__ void __launch_bounds__(kPickThreads, 3)
     evict_pick(const float* weights, const int32_t* __restrict__ length, int Hkv, int S,
                int budget, int recent, int64_t S_out, float* weights_out,
                int32_t* __restrict__ kept, int32_t* __restrict__ new_len) {
   launch_dependents();
+  extern __shared__ float held[];       // this CTA's weights, then its kept offsets
   __shared__ int hist[2][256];          // this CTA's, by pass parity (read by the cluster)
   __shared__ __align__(16) int copies[256][kCopies];
   __shared__ int total[256];
-  __shared__ int2 count_s;              // kept for sure, equal to the threshold (cluster)
-  __shared__ int2 wcount[kPickWarps];
+  // kept for sure | equal to the threshold << 16: of the CTA (read by the cluster), of warps
+  __shared__ uint32_t count_s, wcount[kPickWarps];
   __shared__ uint32_t prefix_s;
   __shared__ int want_s;
+  __shared__ bool all_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
   const int64_t pair = blockIdx.x / C;
@@ -186,53 +202,48 @@ __global__ void __launch_bounds__(kPickThreads, kPer <= 16 ? 2 : 1)
   }
   const int m = len - recent;         // positions the weights decide about
   const int need = budget - recent;   // of which this many stay
-  // this warp's run: positions lo + 32 k + lane, k < steps
-  const int steps = (len + C * kPickThreads - 1) / (C * kPickThreads);  // <= kPer
-  const int lo = ((rank * kPickWarps + warp) * steps) * 32 + lane;
-  float v[kPer];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k)
-    v[k] = k < steps && lo + 32 * k < len ? w[lo + 32 * k] : 0.f;
+  // a thread's run: positions first .. first + steps - 1, laid out an odd number
+  // of words apart, so that the lanes' words lie in different banks
+  const int steps = (len + C * kPickThreads - 1) / (C * kPickThreads);  // <= kPickMost
+  const int stride = steps | 1;
+  const int cta0 = rank * kPickThreads * steps;
+  const int first = cta0 + threadIdx.x * steps;
+  const float* v = held + threadIdx.x * stride;
+  {
+    int run = warp * 32 + lane / steps, k = lane % steps;  // of the warp's element e
+    const int dr = 32 / steps, dk = 32 % steps;
+    const int e0 = cta0 + warp * 32 * steps;
+    for (int e = lane; e < 32 * steps; e += 32) {
+      if (e0 + e < len) copy4(held + run * stride + k, w + e0 + e);
+      run += dr;
+      k += dk;
+      if (k >= steps) k -= steps, ++run;
+    }
+  }
+  copy4_wait();
+  __syncwarp();  // a warp holds its lanes' runs
+  // bit k: position first + k is kept, or undecided
+  uint32_t open = low_bits(min(m - first, steps));
+  uint32_t sure = low_bits(min(len - first, steps)) & ~open;
 
   // radix select, most significant digit first: after digit d, `prefix` holds
   // the top digits of the need-th largest key
-  uint32_t prefix = 0;
+  uint32_t prefix = 0, mask = 0;  // mask: its digits so far
   int want = need;  // how many of the keys that share the prefix are kept
-  const bool counted = C == 1 && steps == 1 && m <= kCountMost;
-  if (counted && need > 0) {
-    // one weight a thread: count the heavier ones instead (the need-th largest
-    // key is the one with fewer than `need` above it and not fewer at or above)
-    uint32_t* keys = reinterpret_cast<uint32_t*>(&copies[0][0]);
-    const int i = lo;
-    keys[i] = i < m ? order_key(v[0]) : 0u;  // 0 is below every key
-    __syncthreads();
-    const uint32_t mine = keys[i];
-    int above = 0, at_least = 0;
-    const int quads = i - lane < m ? (m + 3) / 4 : 0;  // a warp without positions counts nothing
-    for (int j = 0; j < quads; ++j) {
-      const uint4 q = reinterpret_cast<const uint4*>(keys)[j];
-      above += (q.x > mine) + (q.y > mine) + (q.z > mine) + (q.w > mine);
-      at_least += (q.x >= mine) + (q.y >= mine) + (q.z >= mine) + (q.w >= mine);
-    }
-    if (i < m && above < need && need <= at_least) {  // every holder of that key writes the same
-      prefix_s = mine;
-      want_s = need - above;
-    }
-    __syncthreads();
-    prefix = prefix_s;
-    want = want_s;
-  }
-  for (int pass = 0; pass < 4 && need > 0 && !counted; ++pass) {
+  // all holders of the prefix kept: no more digits are needed
+  bool all = need == 0;
+  for (int pass = 0; pass < 4 && !all; ++pass) {
     const int shift = 24 - 8 * pass;
     for (int i = threadIdx.x; i < 256 * kCopies; i += kPickThreads) (&copies[0][0])[i] = 0;
     __syncthreads();
-    const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      if (k >= steps) break;
-      const uint32_t key = order_key(v[k]);
-      if (lo + 32 * k < m && (key & mask) == prefix)
+    for (uint32_t c = open; c; c &= c - 1) {
+      const uint32_t key = order_key(v[__ffs(c) - 1]);
+      if ((key & mask) == prefix) {
         atomicAdd(&copies[(key >> shift) & 255u][lane % kCopies], 1);
+      } else {
+        open ^= c & -c;
+        if ((key & mask) > prefix) sure |= c & -c;
+      }
     }
     __syncthreads();
     if (threadIdx.x < 256) {
@@ -275,6 +286,7 @@ __global__ void __launch_bounds__(kPickThreads, kPer <= 16 ? 2 : 1)
           if (left > 0 && left <= cnt[i]) {
             prefix_s = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
             want_s = left;
+            all_s = left == cnt[i];
           }
           left -= cnt[i];
         }
@@ -283,63 +295,52 @@ __global__ void __launch_bounds__(kPickThreads, kPer <= 16 ? 2 : 1)
     __syncthreads();
     prefix = prefix_s;
     want = want_s;
+    all = all_s;
+    mask |= 255u << shift;
   }
-  if (need == 0) prefix = 0xffffffffu;  // above every key: nothing but the recent ones
-  // `want` of the positions whose key equals `prefix` are kept, lowest first
-  int sure = 0, eq = 0;
+  if (need == 0) prefix = mask = 0xffffffffu;  // above every key: only the recent ones
+  // `want` of the positions whose key has the prefix are kept, lowest first
+  for (uint32_t c = open; c; c &= c - 1) {
+    const uint32_t key = order_key(v[__ffs(c) - 1]) & mask;
+    if (key != prefix) {
+      open ^= c & -c;
+      if (key > prefix) sure |= c & -c;
+    }
+  }
+  const uint32_t mine = __popc(sure) | __popc(open) << 16;  // a CTA's counts fit 16 bits each
+  uint32_t upto = mine;  // of the warp's lanes up to this one
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (k >= steps) break;
-    const int i = lo + 32 * k;
-    const uint32_t key = order_key(v[k]);
-    sure += i < len && (i >= m || key > prefix) ? 1 : 0;
-    eq += i < m && key == prefix ? 1 : 0;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
   }
-  sure = __reduce_add_sync(0xffffffffu, sure);
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  if (lane == 0) wcount[warp] = make_int2(sure, eq);
+  if (lane == 31) wcount[warp] = upto;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int2 t = make_int2(0, 0);
-    for (int x = 0; x < kPickWarps; ++x) {
-      t.x += wcount[x].x;
-      t.y += wcount[x].y;
-    }
-    count_s = t;
-  }
-  if (C > 1)
+  const uint32_t of_warp = lane < kPickWarps ? wcount[lane] : 0u;
+  const uint32_t of_cta = __reduce_add_sync(0xffffffffu, of_warp);
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0u) + upto - mine;
+  int at = 0, taken = 0;  // sure ones and equal ones of the CTAs before this one
+  if (C > 1) {
+    if (threadIdx.x == 0) count_s = of_cta;
     cluster_sync();
-  else
-    __syncthreads();
-  int at = 0, taken = 0;  // sure ones and equal ones before this warp's run
-  for (int r = 0; r < rank; ++r) {
-    const uint32_t a = mapa(smem_u32(&count_s), (uint32_t)r);
-    at += (int)ld_dsmem_u32(a);
-    taken += (int)ld_dsmem_u32(a + 4);
+    const uint32_t c = lane < rank ? ld_dsmem_u32(mapa(smem_u32(&count_s), (uint32_t)lane)) : 0u;
+    at = __reduce_add_sync(0xffffffffu, (int)(c & 0xffffu));
+    taken = __reduce_add_sync(0xffffffffu, (int)(c >> 16));
   }
-  for (int x = 0; x < warp; ++x) {
-    at += wcount[x].x;
-    taken += wcount[x].y;
-  }
-  taken = min(taken, want);
-  at += taken;
-  const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (k >= steps) break;
-    const int i = lo + 32 * k;
-    const uint32_t key = order_key(v[k]);
-    const uint32_t eqm = __ballot_sync(0xffffffffu, i < m && key == prefix);
-    const bool on = i < len && (i >= m || key > prefix ||
-                                (key == prefix && taken + __popc(eqm & below) < want));
-    const uint32_t onm = __ballot_sync(0xffffffffu, on);
-    if (on) {
-      const int j = at + __popc(onm & below);
-      kp[j] = i;
-      if (wo) wo[j] = v[k];
-    }
-    at += __popc(onm);
-    taken = min(want, taken + __popc(eqm));
+  // the CTA's kept offsets in order, then coalesced stores
+  at += min(taken, want);
+  const int kept_cta = (int)(of_cta & 0xffffu) + min(taken + (int)(of_cta >> 16), want) -
+                       min(taken, want);
+  uint16_t* list = reinterpret_cast<uint16_t*>(held + kPickThreads * stride);
+  int eq = taken + (int)(before >> 16);  // equal ones before this thread's
+  int j = (int)(before & 0xffffu) + min(eq, want) - min(taken, want);
+  for (uint32_t c = sure | open; c; c &= c - 1)
+    if ((sure & c & -c) || eq++ < want) list[j++] = threadIdx.x * steps + __ffs(c) - 1;
+  __syncthreads();
+  for (int t = threadIdx.x; t < kept_cta; t += kPickThreads) {
+    const int e = list[t];
+    kp[at + t] = cta0 + e;
+    if (wo) wo[at + t] = held[stride == steps ? e : e + e / steps];
   }
   if (C > 1) cluster_sync();  // no CTA leaves while another reads its counts
 }
@@ -520,14 +521,15 @@ cudaError_t launch_moves(const MovePlanes& out, int n_out, const MovePlanes& in,
 }
 
 // CTAs per cluster of evict_pick for caches of S positions, or 0 (evict_select):
-// enough registers for the weights, and more CTAs, of at least 2048 weights
-// each, when there are few (sequence, head) pairs (8 pairs of 32 K weights 17.6
-// us, 26.7 in the fewest CTAs; of 4 K 11.9 / 11.8).
+// enough to hold the weights, and more, of at least 2048 weights each (5120 with
+// 16, more than the portable size), when there are few (sequence, head) pairs.
+// Measured, 8 pairs, 16 K kept of 128 K: 38.5 us in 16 CTAs, 42.9 in 8; 96 K
+// 24.4 / 26.3, 64 K 22.9 / 22.6, 32 K 18.8 / 16.5 and 23.7 in 2.
 int pick_cluster(int64_t pairs, int S) {
   int C = 1;
   while ((int64_t)C * kPickThreads * kPickMost < S && C < kMaxCluster) C *= 2;
   if ((int64_t)C * kPickThreads * kPickMost < S) return 0;
-  while (C < 8 && pairs * C * 2 <= 152 && S / (2 * C) >= 2048) C *= 2;
+  while (C < kMaxCluster && pairs * C * 2 <= 152 && S / (2 * C) >= (C < 8 ? 2048 : 5120)) C *= 2;
   return C;
 }
 
@@ -578,17 +580,18 @@ extern "C" int spec_kv_evict(const float* weights, const int32_t* length, int B,
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    // the fewest registers that hold the weights: more CTAs per SM (256 pairs of 4 K
-    // weights 41.0 us, 44.7 with the largest form; of 1 K 13.7 / 18.0)
-    const int64_t per = (S + (int64_t)C * kPickThreads - 1) / ((int64_t)C * kPickThreads);
+    const int64_t steps = (S + (int64_t)C * kPickThreads - 1) / ((int64_t)C * kPickThreads);
+    constexpr int kBytes = kPickThreads * (int)(sizeof(float) + sizeof(uint16_t));  // of a step
+    static std::atomic<uint64_t> done{0};
+    e = allow_smem((const void*)evict_pick, kBytes * (kPickMost | 1), done);
+    if (e != cudaSuccess) return SPEC_ERR_CUDA;
     if (C > 8) {  // more than the portable cluster size
-      e = cudaFuncSetAttribute(evict_pick<kPickMost>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                               1);
+      e = cudaFuncSetAttribute(evict_pick, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return SPEC_ERR_CUDA;
     }
-    e = cudaLaunchKernelEx(&cfg, per <= 8 ? evict_pick<8> : (per <= 16 ? evict_pick<16> : evict_pick<kPickMost>),
-                           weights, length, Hkv,
-                           S, budget, recent, (int64_t)S_out, weights_out, kept, new_len);
+    cfg.dynamicSmemBytes = (size_t)(steps | 1) * kBytes;
+    e = cudaLaunchKernelEx(&cfg, evict_pick, weights, length, Hkv, S, budget, recent,
+                           (int64_t)S_out, weights_out, kept, new_len);
   } else {
     evict_select<<<(unsigned)pairs, kSelThreads, 0, st>>>(weights, length, Hkv, S, budget, recent,
                                                           kept, new_len);

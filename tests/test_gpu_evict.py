@@ -221,6 +221,30 @@ def test_evict_matches_oracle(B, Hkv, S, length, budget, recent, kind, in_place)
                                   equal_nan=True)
 
 
+@pytest.mark.parametrize("S", [512, 513, 1024, 1537, 16384, 16385, 90000])
+@pytest.mark.parametrize("bits", [7, 8, 15, 16, 23, 24, 31])
+def test_evict_where_the_key_is_decided_early(S, bits):
+    """The heavier group's keys differ from the others' first in the given bit
+    from the top, so a select by digits can stop, or must go on, after any of
+    them; runs of whole and broken lengths."""
+    rng = np.random.default_rng(S + bits)
+    heavy = rng.random(S) < 0.3
+    low = (1 << (31 - bits)) - 1
+    u = np.full(S, 0x3F200000 & ~((low << 1) | 1), np.uint32)
+    u |= rng.integers(0, low + 1, size=S).astype(np.uint32)
+    u[heavy] |= np.uint32(low + 1)
+    w = u.view(np.float32)[None, None]
+    a = api()
+    n = int(heavy.sum())
+    for budget in (n, n + 1, max(1, n - 1), max(1, n // 2)):
+        t = torch.from_numpy(w.copy()).cuda()
+        kept, _ = a.spec_kv_evict(t, _i32([S]), (), budget=budget, recent=0)
+        torch.cuda.synchronize()
+        want = evict.kept_positions(w[0, 0], S, budget, 0)
+        assert kept[0, 0].tolist() == want
+        assert np.array_equal(t[0, 0, :budget].cpu().numpy(), w[0, 0, want])
+
+
 def test_evict_without_planes_and_empty_batch():
     a = api()
     w = torch.tensor([[[3.0, 1.0, 2.0, 0.0]]], device="cuda")
