@@ -43,6 +43,7 @@ constexpr int kMaxCluster = 16;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;
 constexpr int kSweepUnroll = 4;
+constexpr int kSweepMost = 1024;  // threads
 constexpr int kMaxPlanes = 9;  // SPEC_EVICT_MAX_PLANES and the weights
 
 // Orders like w, NaN as -inf and -0 as +0 (the sum and the maximum see to that).
@@ -427,8 +428,8 @@ template <typename W>
 __device__ __forceinline__ void sweep_rows(const MovePlane& pl, const int32_t* __restrict__ kp,
                                            int budget, unsigned char* base0, int w0, int nw) {
   W* base = reinterpret_cast<W*>(base0) + w0;
-  // thread t takes word t % nw of rows t / nw, + 256 / nw, ... of a chunk
-  const int rows = kMoveThreads / nw;
+  // thread t takes word t % nw of rows t / nw, + threads / nw, ... of a chunk
+  const int rows = (int)blockDim.x / nw;
   const int tr = threadIdx.x / nw, tw = threadIdx.x % nw;
   W v[2][kSweepUnroll];
   bool move[2][kSweepUnroll];
@@ -462,7 +463,7 @@ __device__ __forceinline__ void sweep_rows(const MovePlane& pl, const int32_t* _
 }
 // In place: blockIdx.x = (sequence, head), blockIdx.y = plane, blockIdx.z = slice of
 // at most 32 bytes of the rows.
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kSweepMost)
     evict_sweep(const MovePlanes planes, const int32_t* __restrict__ kept, int budget, int64_t S) {
   grid_dependency_wait();
   const MovePlane pl = planes.p[blockIdx.y];
@@ -510,10 +511,17 @@ cudaError_t launch_moves(const MovePlanes& out, int n_out, const MovePlanes& in,
   }
   if (n_in > 0) {
     int most = 0;  // slices; rows have at most 65536 bytes
+    int64_t ctas = 0;
     for (int i = 0; i < n_in; ++i) {
       const int c = (in.p[i].width * in.p[i].words + 31) / 32;
       most = most > c ? most : c;
+      ctas += pairs * c;
     }
+    // few CTAs take longer chunks.  The call in place, 1024 / 512 / 256 threads: 128
+    // CTAs (8 pairs, 16 K bf16 rows kept) 62 / 68 / 95 us; 384 (64 pairs, 8 K 4-bit
+    // rows) 85 / 88 / 103; 512 (32 pairs, 4 K bf16 rows) 60 / 56 / 52; 1536 (256
+    // pairs, 2 K 4-bit rows) 58 / 46 / 44.
+    cfg.blockDim = dim3(ctas <= 152 ? kSweepMost : (ctas <= 400 ? kSweepMost / 2 : kMoveThreads));
     cfg.gridDim = dim3((unsigned)pairs, (unsigned)n_in, (unsigned)most);
     e = cudaLaunchKernelEx(&cfg, evict_sweep, in, kept, budget, (int64_t)S);
   }

@@ -221,6 +221,14 @@ def test_evict_matches_oracle(B, Hkv, S, length, budget, recent, kind, in_place)
                                   equal_nan=True)
 
 
+@pytest.mark.parametrize("B", [7, 20, 40])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_batches_match_oracle(B, in_place):
+    # few and many (sequence, head) pairs: chunks of 1024, 512, 256 threads
+    length = [(37 * b) % 1291 for b in range(B)]
+    test_evict_matches_oracle(B, 2, 1290, length, 700, 31, "plain", in_place)
+
+
 @pytest.mark.parametrize("S", [512, 513, 1024, 1537, 16384, 16385, 90000])
 @pytest.mark.parametrize("bits", [7, 8, 15, 16, 23, 24, 31])
 def test_evict_where_the_key_is_decided_early(S, bits):
