@@ -15,7 +15,7 @@
 // eleven bits for every key within 2^-21 of the reference.  Scores, sums
 // and outputs are float32.
 //
-// Kernel kv4_rows (8, 16 or 32 query rows a tile): warp-level m16n8k16 products
+// Kernel kv4_rows (8, 16, 24 or 32 query rows a tile): warp-level m16n8k16 products
 // with the cache as the 16-row operand, converted in registers, so that it
 // crosses shared memory once, as codes, and eight query rows waste nothing.
 // Each warp owns a ring of 32-key stages filled with cp.async and needs no
@@ -109,13 +109,17 @@ struct Stage {
 };
 
 // Warps per CTA, CTAs per SM and ring stages by the number of row tiles of
-// eight, whose outputs take 32 registers each (D 128).
+// eight, whose outputs take 32 registers each (D 128).  Products for rows that
+// are not there cost as much as others: 20 rows in three tiles 58 us, in four 72
+// (32 sequences of 2 to 4 K keys), 180 / 226 (16 of 32 K).  Three tiles with ten
+// warps, q in shared memory, 72.
 template <int NT>
 struct RowsCfg {
   static constexpr int kWarps = NT == 2 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kCtas = NT == 1 ? 2 : 1;  // per SM
-  static constexpr int kStages = NT == 4 ? 4 : 3;
+  static constexpr int kStages = NT >= 3 ? 4 : 3;
+  static constexpr bool kQShared = NT == 4;  // q's fragments in shared memory
   static constexpr int kPieces = kSms * kCtas * kWarps;
 };
 
@@ -124,7 +128,8 @@ struct RowsSmem {
   static constexpr int kWarps = RowsCfg<NT>::kWarps;
   static constexpr int kRing = kWarps * RowsCfg<NT>::kStages * Stage<D>::kBytes;
   unsigned char ring[kRing];
-  uint2 qf[NT == 4 ? kWarps : 1][NT == 4 ? D / 16 : 1][NT][32];  // q's operand fragments
+  static constexpr bool kQ = RowsCfg<NT>::kQShared;
+  uint2 qf[kQ ? kWarps : 1][kQ ? D / 16 : 1][NT][32];  // q's operand fragments
   unsigned long long vnan[kWarps][D / kKv4Block];  // drafted keys whose V block is NaN
   int64_t before[RowsCfg<NT>::kThreads + 1];
   int64_t tmp[kWarps];
@@ -206,7 +211,7 @@ __device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>&
   constexpr int kSteps = D / 16;      // k steps of S
   constexpr int kMT = D / 16;         // m tiles of O^T
   constexpr int kW = D / 32;          // code words a lane loads per key of K
-  constexpr bool kQReg = NT < 4;      // q's fragments stay in registers
+  constexpr bool kQReg = !RowsCfg<NT>::kQShared;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int b = t.b, kvh = t.kvh, rt = t.rt, P = t.P, L = P + p.N;
@@ -828,6 +833,7 @@ size_t attn_ws(int B, int Hkv, int R, int D, int S) {
   if (R > kRowsMax) return kv4_tc_ws(B, Hkv, R, D, S);
   if (R <= 8) return part_bytes<1>(B, Hkv, R, D, S);
   if (R <= 16) return part_bytes<2>(B, Hkv, R, D, S);
+  if (R <= 24) return part_bytes<3>(B, Hkv, R, D, S);
   return part_bytes<4>(B, Hkv, R, D, S);
 }
 
@@ -899,7 +905,7 @@ using namespace sv;
 
 // More than kRowsMax query rows per key/value head go to the tensor-core kernel
 // (kv4_attn_tc.cu).  Measured (D 128): 32 sequences of 2 to 4 K keys, 16 rows
-// 48 us here and 73 there, 20 rows 72 / 73, 32 rows 75 / 72 us; 8 sequences of
+// 48 us here and 73 there, 20 rows 58 / 73, 32 rows 75 / 72 us; 8 sequences of
 // 32 K keys, 32 rows 141 / 165 us; one of 1 K keys 15 / 14 us.
 extern "C" size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D,
                                                           int S) {
@@ -963,10 +969,12 @@ extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
   else if (D == 128)
     e = R <= 8 ? launch_rows<128, 1>(p, workspace, st)
                : (R <= 16 ? launch_rows<128, 2>(p, workspace, st)
-                          : launch_rows<128, 4>(p, workspace, st));
+                          : (R <= 24 ? launch_rows<128, 3>(p, workspace, st)
+                                     : launch_rows<128, 4>(p, workspace, st)));
   else
     e = R <= 8 ? launch_rows<64, 1>(p, workspace, st)
                : (R <= 16 ? launch_rows<64, 2>(p, workspace, st)
-                          : launch_rows<64, 4>(p, workspace, st));
+                          : (R <= 24 ? launch_rows<64, 3>(p, workspace, st)
+                                     : launch_rows<64, 4>(p, workspace, st)));
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -262,6 +262,22 @@ def test_ragged_batches_and_split_sequences(N, Hq, Hkv, B, lo, hi):
     check_attention(out, lse, q, vals, prefix, words, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("prefix", [[400, 33], [20001]])   # one CTA cluster; pieces
+@pytest.mark.parametrize("N,Hq", [(1, 17), (1, 23), (3, 8), (5, 5), (31, 1),
+                                  (4, 8), (3, 11), (2, 12)])
+def test_rows_at_the_borders_of_row_tiles(N, Hq, prefix, D):
+    rng = np.random.default_rng(N * Hq + D)
+    B, S = len(prefix), max(prefix) + N + 1
+    cache, vals = make_cache(N * Hq, B, 1, S, D)
+    q = torch.randn(B, N, Hq, D, generator=_gen(Hq), device="cuda").bfloat16()
+    _, words = tree_mask(random_parent(rng, B, N))
+    out, lse = api().spec_tree_attention_kv4(
+        q, cache, _i32(prefix), _words(words), v_unit=0.125, lse=True)
+    torch.cuda.synchronize()
+    check_attention(out, lse, q, vals, prefix, words, D ** -0.5)
+
+
 def test_large_and_small_query_rows_and_units():
     # rows of very different magnitude, among them zeros; unit 2^-20 keys
     B, N, Hq, Hkv, D, P = 1, 3, 4, 2, 128, 150
