@@ -80,6 +80,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// m 2^e, m in [1, 2], kept normal: a factor of 0 or infinity would make NaN of a
+// masked score (-inf) or of a score of 0.  Where it is clamped the scores are
+// either below 2^-100 (a row scaled to [1, 2) times a cache's codes and scales is
+// below 2^20) or far outside float32.
+__device__ __forceinline__ float row_factor(float m, int e) {
+  return m * __uint_as_float((uint32_t)(127 + max(-126, min(126, e))) << 23);
+}
 // both halves of the low / high half of h
 __device__ __forceinline__ uint32_t dup_lo(uint32_t h) { return __byte_perm(h, h, 0x1010); }
 __device__ __forceinline__ uint32_t dup_hi(uint32_t h) { return __byte_perm(h, h, 0x3232); }

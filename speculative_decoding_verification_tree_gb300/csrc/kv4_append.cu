@@ -21,6 +21,8 @@
 // instruction issue close behind (82% of its slots, cold caches).  4 x 8192
 // positions of 8 heads, D 128 (172 MB): 33 us, 5.2 TB/s, written and 33 us read
 // back.  The same rounding in packed arithmetic took the same time.
+#include <math.h>
+
 #include "kernels.h"
 #include "kv4.cuh"
 
@@ -198,6 +200,14 @@ bool kv4_unit_ok(float u) {
   } x;
   x.f = u;
   return (x.i & 0x7fffffu) == 0;
+}
+
+ScoreScale score_scale(float scale, float unit) {
+  int es, ep, eu;
+  const float ms = frexpf(scale, &es);           // [1/2, 1)
+  const float mp = frexpf(ms * kLog2e, &ep);     // rounded as scale * log2(e) is
+  frexpf(unit, &eu);                             // unit = 2^(eu - 1)
+  return {2.f * mp, es + ep - 1 + eu - 1};
 }
 
 }  // namespace sv

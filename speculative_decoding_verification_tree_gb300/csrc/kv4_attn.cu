@@ -264,7 +264,7 @@ __device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>&
       else
         sm.qf[warp][x][nt][lane] = h;  // read back by this lane alone
     }
-    const float fg = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+    const float fg = row_factor(p.scale.m, p.scale.e + e);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       f[nt][x] = __shfl_sync(0xffffffffu, fg, 4 * (2 * c + x));
@@ -958,7 +958,7 @@ extern "C" int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
   p.Hkv = Hkv;
   p.S = S;
   p.R = (int)R;
-  p.scale_log2 = scale * kLog2e * k_unit;
+  p.scale = score_scale(scale, k_unit);
   p.v_unit = v_unit;
   p.out = (uint16_t*)out;
   p.lse = lse;

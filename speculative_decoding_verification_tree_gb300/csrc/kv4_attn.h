@@ -11,7 +11,7 @@ struct Kv4Attn {
   const int32_t* prefix_len;
   const uint64_t* mask_bits;
   int B, N, Hq, Hkv, S, R;  // R: query rows per key/value head
-  float scale_log2;  // scale * log2(e) * k_unit
+  ScoreScale scale;  // scale log2(e) k_unit
   float v_unit;
   uint16_t* out;
   float* lse;  // or null

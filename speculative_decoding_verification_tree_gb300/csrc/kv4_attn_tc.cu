@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
       }
       tst_wait();
       fence_before();
-      f = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+      f = row_factor(p.scale.m, p.scale.e + e);
       if (kNG == 2) {
         sm.rowf[r] = f;
         sm.mref[r] = neg_inf();

@@ -25,6 +25,7 @@
 // in 29 us = 2.2 TB/s, the latency of conversion, product and exponential in one
 // warp's 32 keys (issue 47%; a third CTA per SM, or 4-bit keys loaded straight
 // into registers, measured slower).
+#include <cfloat>
 #include <type_traits>
 
 #include "kernels.h"
@@ -49,7 +50,8 @@ struct WeightParams {
   const float* lse;
   const int32_t *prefix_len, *path_len, *path_nodes;
   int B, N, Hq, Hkv, S;
-  float scale_log2;
+  ScoreScale scale;  // scale log2(e) k_unit (4-bit keys)
+  float factor;      // scale log2(e) (bf16 keys)
   const float* in;
   float* out;
 };
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
       for (int x = 0; x < kMine; ++x) {
         const int i = warp + kWtWarps * x, r = grp * kWtRows + i;
         if (i >= rows) break;
-        float up = 1.f;
+        int up = 0;  // the row was scaled by 2^-up
         uint32_t h0 = w[x].x, h1 = w[x].y;
         int s, cc;
         if constexpr (kKv4) {
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
           if (mx == 0.f || e == 128) e = 0;
           e = max(-126, min(126, e));
           const float dn = __uint_as_float((uint32_t)(127 - e) << 23);
-          up = __uint_as_float((uint32_t)(127 + e) << 23);
+          up = e;
           h0 = pack_half2(x0 * dn, x1 * dn);
           h1 = pack_half2(x2 * dn, x3 * dn);
           cc = lane / (D / 16);
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
         }
         if (lane < D / 4) sm.qf[i >> 3][s][4 * (i & 7) + cc] = make_uint2(h0, h1);
         if (lane == 0) {
-          sm.rowf[i] = p.scale_log2 * up;
+          sm.rowf[i] = kKv4 ? row_factor(p.scale.m, p.scale.e + up) : p.factor;
           sm.rowl[i] = l[x] == neg_inf() ? l[x] : -l[x];  // a row that saw nothing weighs nothing
           sm.rowt[i] = r < R ? P + r / Gq : -1;
         }
@@ -414,7 +416,8 @@ extern "C" int spec_kv_weights(const void* q, const void* k, const uint8_t* k_sc
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.S = S;
-  p.scale_log2 = scale * kLog2e * k_unit;
+  p.scale = score_scale(scale, k_unit);
+  p.factor = fminf(scale * kLog2e, FLT_MAX);
   p.in = weights;
   p.out = out;
   p.B = B;
