@@ -420,7 +420,8 @@ int spec_accept_stats(const int32_t* count, const int32_t* parent,
  * SPEC_ERR_SHAPE when B * Hkv * S reaches 2^31 cache rows; SPEC_ERR_CUDA if
  * the caches cannot be described to the copy engine.  B == 0 does nothing.
  * Runs on the tensor cores (tcgen05): one CTA per 256 query rows of one
- * (sequence, key/value head).
+ * (sequence, key/value head).  Its waits are bounded; rows of a CTA whose wait
+ * gave up (after about a second) are NaN, as there is no status word.
  */
 int spec_tree_attention(const void* q, const void* k_cache,
                         const void* v_cache, const int32_t* prefix_len,
@@ -485,7 +486,9 @@ int spec_kv4_read(const uint8_t* k_codes, const uint8_t* k_scales,
  *     log2 sum_s 2^(log2(e) scale q . k_s) over its visible keys.
  * A row that sees nothing (prefix 0 and no mask bit) gives zeros and lse =
  * -inf.  What cache positions behind prefix_len + N hold does not matter; a
- * NaN block of a drafted position reaches only the rows that see it.
+ * NaN block of a drafted position reaches only the rows that see it.  Rows of
+ * a CTA one of whose bounded waits gave up (after about a second) are NaN in
+ * out and lse, as there is no status word.
  * Workspace: spec_tree_attention_kv4_workspace_bytes(B, N, Hq, Hkv, D, S) bytes,
  * 256-byte aligned, uninitialised (0: none is needed, or the sizes are
  * invalid).

@@ -25,8 +25,9 @@
 // take 1250 of the tensor pipe for both tiles.  One tile: 64 rows 73 us, 128 rows
 // 73 us (as half of a two-tile CTA 87 and 79 us).
 // TMEM (512 columns): Q_t at columns 64 t, S buffers at 128 and 192, O_t at 256
-// + 128 t.  Every mbarrier wait is bounded; a CTA that gives up stops waiting
-// and still frees its TMEM after waiting, bounded, for its own products.
+// + 128 t.  Every mbarrier wait is bounded; a CTA that gives up stops waiting,
+// still frees its TMEM after waiting, bounded, for its own products, and returns
+// NaN rows and normalisers (there is no status word).
 #include "kernels.h"
 #include "kv4.cuh"
 #include "kv4_attn.h"
@@ -518,6 +519,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
         named_sync(1, kMT * kNG);
         l = sm.lsum[0][r] + sm.lsum[1][r];
       }
+      // whoever gave up wrote `dead` before the arrival that led here
+      bool gave_up = *(volatile uint32_t*)&sm.dead != 0;
+#ifdef SV_TEST_GAVE_UP  // a test's build: CTA 0 as if one of its waits had
+      gave_up |= blockIdx.x == 0;
+#endif
+      if (gave_up) l = __int_as_float(0x7fffffff);
       float inv = 1.f;
       float* part = nullptr;
       if (prm.splits == 1) {

@@ -40,10 +40,9 @@
 // 128 + 64 t, O_t at 256 + 128 t.  With Q in TMEM the tensor cores read only
 // K (2 KB per MMA instead of 6) from shared memory for S, and shared memory
 // holds the 5-stage ring and two P buffers per tile (224 KB).  Every
-// mbarrier wait is bounded (SPEC_STATUS_TIMEOUT is not reported by this
-// entry point, which has no status word; a CTA that gives up stops waiting
-// and still frees its TMEM after waiting, bounded, for its own MMAs and
-// copies).
+// mbarrier wait is bounded; a CTA that gives up stops waiting, still frees
+// its TMEM after waiting, bounded, for its own MMAs and copies, and returns
+// NaN rows and normalisers (there is no status word).
 #include <cfloat>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -444,6 +443,12 @@ __global__ void __launch_bounds__(kAThreads, 1)
       if (nblk > 0)
         await(sm, &sm.pdone[t][(nblk - 1) & 1], (uint32_t)(((nblk - 1) >> 1) & 1));
       fence_after();
+      // whoever gave up wrote `dead` before the arrival that led here
+      bool gave_up = *(volatile uint32_t*)&sm.dead != 0;
+#ifdef SV_TEST_GAVE_UP  // a test's build: CTA 0 as if one of its waits had
+      gave_up |= blockIdx.x + blockIdx.y + blockIdx.z == 0;
+#endif
+      if (gave_up) l = __int_as_float(0x7fffffff);
       const float inv = 1.f / l;
       // the row's base-2 log normaliser (-inf where it saw nothing)
       if (lse && valid) lse[qoff / kAD] = mref + log2f(l);
