@@ -555,7 +555,7 @@ int spec_kv_weights(const void* q, const void* k, const uint8_t* k_scales,
  * planes: n_planes host pointers to device arrays [B, Hkv, S, row_bytes[i]]
  *     (keys, values, codes, scales, ...); planes_out [B, Hkv, S_out,
  *     row_bytes[i]] receive the kept rows.  planes_out[i] == planes[i] (with
- *     S_out == S) moves in place; otherwise the two must not overlap.
+ *     S_out == S) moves in place.
  * weights_out [B, Hkv, S_out] (may be NULL, or equal weights if S_out == S).
  * kept [B, Hkv, budget] int32 (out): the kept positions, ascending, -1 padded.
  * new_len [B] int32 (out) = min(length, budget).
@@ -564,8 +564,10 @@ int spec_kv_weights(const void* q, const void* k, const uint8_t* k_scales,
  * SPEC_MAX_POSITIONS, budget outside [1, S_out], recent outside [0, budget], n_planes outside
  * [0, SPEC_EVICT_MAX_PLANES], row_bytes outside [1, 65536]; SPEC_ERR_ARG for
  * a NULL pointer (B > 0), a float or int array not 4-byte aligned, an array
- * given in place with S_out != S, or new_len == length (every head reads the
- * lengths).  B == 0 does nothing.
+ * given in place with S_out != S, or an output (planes_out, weights_out, kept,
+ * new_len) that overlaps another output or an input other than the one it
+ * replaces in place: the same plane twice in place, the weights among planes that
+ * move with them, new_len == length.  B == 0 does nothing.
  */
 #define SPEC_EVICT_MAX_PLANES 8
 int spec_kv_evict(const float* weights, const int32_t* length, int B, int Hkv,

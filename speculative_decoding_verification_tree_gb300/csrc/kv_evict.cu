@@ -541,6 +541,52 @@ int pick_cluster(int64_t pairs, int S) {
   return C;
 }
 
+// Whether the arrays of a call overlap where they must not: an output with
+// another output, or with an input other than the one it replaces in place.
+// (A buffer listed twice in place would be moved by two sets of CTAs at once.)
+// A buffer that is also an input elsewhere may be moved in place: the weights are
+// read, and other buffers written, before planes move; but weights that move in
+// place do so first.
+struct Range {
+  uintptr_t at;
+  uint64_t bytes;
+  bool meets(const Range& o) const {
+    return bytes > 0 && o.bytes > 0 && at < o.at + o.bytes && o.at < at + bytes;
+  }
+};
+bool evict_overlaps(const float* weights, const int32_t* length, int64_t B, int64_t pairs,
+                    int64_t S, int budget, int n_planes, const void* const* planes,
+                    void* const* planes_out, const int* row_bytes, int64_t S_out,
+                    const float* weights_out, const int32_t* kept, const int32_t* new_len) {
+  // planes, then the weights; an absent array is empty
+  Range in[kMaxPlanes], out[kMaxPlanes];
+  for (int i = 0; i < n_planes; ++i) {
+    in[i] = {(uintptr_t)planes[i], (uint64_t)(pairs * S) * row_bytes[i]};
+    out[i] = {(uintptr_t)planes_out[i], (uint64_t)(pairs * S_out) * row_bytes[i]};
+  }
+  in[n_planes] = {(uintptr_t)weights, (uint64_t)(pairs * S) * 4};
+  out[n_planes] = {(uintptr_t)weights_out, weights_out ? (uint64_t)(pairs * S_out) * 4 : 0};
+  const Range small[3] = {{(uintptr_t)kept, (uint64_t)(pairs * budget) * 4},
+                          {(uintptr_t)new_len, (uint64_t)B * 4},
+                          {(uintptr_t)length, (uint64_t)B * 4}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < i; ++j)
+      if (small[i].meets(small[j])) return true;
+  for (int i = 0; i <= n_planes; ++i) {
+    for (const Range& s : small)
+      if (out[i].meets(s)) return true;
+    // kept and new_len are written while planes and weights are read
+    if (in[i].meets(small[0]) || in[i].meets(small[1])) return true;
+    for (int j = 0; j <= n_planes; ++j) {
+      if (j < i && out[i].meets(out[j])) return true;
+      const bool itself =
+          in[j].at == out[i].at && (i == j || (i < n_planes && in[j].at == in[i].at));
+      if (!itself && out[i].meets(in[j])) return true;
+    }
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -572,8 +618,11 @@ extern "C" int spec_kv_evict(const float* weights, const int32_t* length, int B,
     if (!planes[i] || !planes_out[i]) return SPEC_ERR_ARG;
     if (planes[i] == planes_out[i] && S_out != S) return SPEC_ERR_ARG;
   }
-  if ((weights_out == weights && S_out != S) || new_len == length) return SPEC_ERR_ARG;
+  if (weights_out == weights && S_out != S) return SPEC_ERR_ARG;
   const int64_t pairs = (int64_t)B * Hkv;
+  if (evict_overlaps(weights, length, B, pairs, S, budget, n_planes, planes, planes_out, row_bytes,
+                     S_out, weights_out, kept, new_len))
+    return SPEC_ERR_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const int C = pick_cluster(pairs, S);
   cudaError_t e;

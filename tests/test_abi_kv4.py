@@ -147,6 +147,37 @@ def test_evict_argument_errors(lib):
     assert call(B=0, w=None, planes=(None,), outs=(None,)) == lib.SPEC_OK
 
 
+def test_evict_refuses_arrays_that_overlap(lib):
+    """2 x 2 pairs of 64 positions; every array apart but for the ones named.
+    All calls are refused before any device work."""
+    at = lambda i: FAKE.value + (i << 20)
+    W, N, K, V, KO, VO, WO, KEPT, NEW = map(at, range(9))
+
+    def call(planes=(K, V), outs=(K, V), rows=(64, 64), w=W, wo=W, n=N,
+             kept=KEPT, new=NEW, S=64, S_out=64):
+        k = len(planes)
+        return lib.raw("spec_kv_evict", w, n, 2, 2, S, 16, 4, k,
+                       (ctypes.c_void_p * k)(*planes),
+                       (ctypes.c_void_p * k)(*outs), (ctypes.c_int * k)(*rows),
+                       S_out, wo, kept, new, None)
+    size = 2 * 2 * 64 * 64
+    for kw in (dict(planes=(K, K), outs=(K, K)),          # twice in place
+               dict(planes=(K, V), outs=(KO, KO)),        # one output for two
+               dict(planes=(K, V), outs=(V, K)),          # exchanged
+               dict(planes=(K, V), outs=(KO, K)),         # over another's input
+               dict(outs=(K + 64, VO)),                   # shifted by a row
+               dict(outs=(KO, KO + size - 4)),            # their last word
+               dict(planes=(K, W), outs=(K, W), rows=(64, 4)),   # moved twice
+               dict(planes=(K, W), outs=(K, VO), rows=(64, 4)),  # moves first
+               dict(planes=(K, V), outs=(W, V), wo=None),
+               dict(wo=K, outs=(KO, VO)), dict(wo=KO, outs=(KO, VO)),
+               dict(wo=W + 4), dict(new=N), dict(new=N + 4), dict(kept=N),
+               dict(kept=W), dict(kept=K + size - 4), dict(kept=WO, wo=WO),
+               dict(new=W), dict(new=V), dict(new=KEPT), dict(wo=N, outs=(KO, VO)),
+               dict(outs=(N, VO))):
+        assert call(**kw) == lib.SPEC_ERR_ARG, kw
+
+
 def test_wrappers_reject_malformed_tensors():
     bf, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
     B, N, Hq, Hkv, D, S = 2, 3, 4, 2, 128, 16

@@ -461,3 +461,25 @@ def test_views_and_host_tensors_are_refused():
         a.spec_kv_evict(w, z, cache, budget=4, recent=0, new_len=z)
     with pytest.raises(SpecError):
         a.spec_kv4_append(k, k, z, cache, k_unit=0.3)
+
+
+def test_evict_takes_a_buffer_in_place_and_as_another_input():
+    """A plane moved in place and copied by the same call, and the weights
+    moved as a plane of their own, below and above what a cluster holds."""
+    a = api()
+    for S in (900, 262145):
+        g = _gen(S)
+        w = torch.rand(1, 2, S, generator=g, device="cuda")
+        k = torch.randint(0, 256, (1, 2, S, 8), generator=g, device="cuda",
+                          dtype=torch.uint8)
+        w0, k0 = w.clone(), k.clone()
+        copy = torch.zeros(1, 2, S, 8, dtype=torch.uint8, device="cuda")
+        kept, n = a.spec_kv_evict(w, _i32([S]), (k, k, w), budget=300,
+                                  recent=20, planes_out=(k, copy, w))
+        torch.cuda.synchronize()
+        assert n.tolist() == [300]
+        for h in range(2):
+            want = evict.kept_positions(w0[0, h].cpu().numpy(), S, 300, 20)
+            assert kept[0, h].tolist() == want
+            for got, src in ((w, w0), (k, k0), (copy, k0)):
+                assert torch.equal(got[0, h, :300], src[0, h, want])
