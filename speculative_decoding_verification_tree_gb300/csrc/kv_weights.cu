@@ -212,8 +212,10 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
         if (lane < D / 4) sm.qf[i >> 3][s][4 * (i & 7) + cc] = make_uint2(h0, h1);
         if (lane == 0) {
           sm.rowf[i] = kKv4 ? row_factor(p.scale.m, p.scale.e + up) : p.factor;
-          sm.rowl[i] = l[x] == neg_inf() ? l[x] : -l[x];  // a row that saw nothing weighs nothing
-          sm.rowt[i] = r < R ? P + r / Gq : -1;
+          // a row that saw nothing weighs nothing, whatever the keys hold
+          const bool blind = l[x] == neg_inf();
+          sm.rowl[i] = blind ? l[x] : -l[x];
+          sm.rowt[i] = r < R && !blind ? P + r / Gq : -1;
         }
       }
     };
@@ -322,7 +324,8 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
                 const int i = (nt + y) * 8 + 2 * c;  // this lane's rows i, i + 1
                 const float2 f = *reinterpret_cast<const float2*>(&sm.rowf[i]);
                 const float2 l = *reinterpret_cast<const float2*>(&sm.rowl[i]);
-                const bool whole = key0 + 31 <= P && (nt + y) * 8 + 8 <= R - grp * kWtRows;
+                const bool whole = key0 + 31 <= P && (nt + y) * 8 + 8 <= R - grp * kWtRows &&
+                                   fminf(l.x, l.y) != neg_inf();
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                   const float2 e =

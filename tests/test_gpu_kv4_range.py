@@ -72,3 +72,39 @@ def test_factor_of_a_zero_row_over_a_bf16_cache():
     assert torch.allclose(lse[0, :, 0].cpu(), torch.tensor(
         [math.log2(P + t + 1) for t in range(N)]), rtol=0, atol=2.0 ** -15)
     assert np.allclose(w[0, 0, :P].cpu().numpy(), want, rtol=2.0 ** -14)
+
+
+@pytest.mark.parametrize("kind", ["kv4", "bf16"])
+def test_rows_that_saw_nothing_add_nothing_to_nan_keys(kind):
+    """lse = -inf: nothing is added, also where a key is NaN or a score
+    overflows; the other rows' weights reach every position they see."""
+    B, N, Hq, D, P = 1, 9, 2, 128, 700
+    g = _gen(5)
+    q = torch.randn(B, N, Hq, D, generator=g, device="cuda").bfloat16()
+    k = torch.randn(B, 1, P + N, D, generator=g, device="cuda").bfloat16()
+    if kind == "kv4":
+        cache = api().kv4_cache(B, 1, P + N, D)
+        kk = k.transpose(1, 2).contiguous()
+        api().spec_kv4_append(kk, kk, _i32([0]), cache)
+        k = cache[:2]
+    lse = torch.full((B, N, Hq), 9.0, device="cuda")
+    w0 = torch.rand(B, 1, P + N, generator=g, device="cuda")
+    lse[0, 1:] = float("-inf")
+    args = (_i32([P]), _i32([N]))
+    one = api().spec_kv_weights(q, k, lse, _i32([P]), _i32([1]), weights=w0)
+    got = api().spec_kv_weights(q, k, lse, *args, weights=w0)
+    torch.cuda.synchronize()
+    assert torch.equal(got[:, :, :P + 1], one[:, :, :P + 1])
+    assert (got[:, :, P + 1:] == 0).all()
+    # now no row sees anything, and keys are NaN
+    lse[:] = float("-inf")
+    if kind == "kv4":
+        cache.k_scale[0, 0, 5::7] = 0x7F
+    else:
+        k[0, 0, 5::7] = float("nan")
+    got = api().spec_kv_weights(q, k, lse, *args, weights=w0)
+    huge = api().spec_kv_weights(q, k, lse, *args, scale=3e38, weights=w0)
+    torch.cuda.synchronize()
+    for x in (got, huge):
+        assert torch.equal(x[:, :, :P], w0[:, :, :P])
+        assert (x[:, :, P:] == 0).all()
