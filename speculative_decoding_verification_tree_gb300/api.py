@@ -77,6 +77,11 @@ def _on(dev):
     return contextlib.nullcontext()  # host-side tests with CPU tensors
 
 
+def _default_device(device):
+    """`device` as given (0 is a device), else the current CUDA device."""
+    return torch.cuda.current_device() if device is None else device
+
+
 def params(temperature=1.0, top_k=0, top_p=1.0, draft_kind="logits", seed=0,
            offset=0, draft_lse=None, flags=0) -> SpecParams:
     if draft_lse is not None:
@@ -97,7 +102,7 @@ def workspace(op, B, n, V, device=None):
     if nbytes == 0:
         raise ValueError("invalid sizes for the workspace")
     return torch.empty(nbytes, dtype=torch.uint8,
-                       device=device or torch.cuda.current_device())
+                       device=_default_device(device))
 
 
 def spec_verify_chain(target, draft, draft_tokens, *, temperature=1.0,
@@ -309,7 +314,7 @@ def spec_kv_commit(kv, prefix_len, path_len, path_nodes=None, *, layout,
 
 def accept_stats_records(n, nbins=20, device=None):
     """Zeroed records for spec_accept_stats (a dict of device tensors)."""
-    dev = device or torch.cuda.current_device()
+    dev = _default_device(device)
     z = lambda k, dt=torch.int64: torch.zeros(k, dtype=dt, device=dev)
     return {"len_hist": z(n + 1), "node_tested": z(n), "node_accepted": z(n),
             "depth_tested": z(n), "depth_accepted": z(n),
@@ -417,7 +422,7 @@ class KV4Cache(NamedTuple):
 
 def kv4_cache(B, Hkv, S, D=128, device=None) -> KV4Cache:
     """A zeroed 4-bit cache."""
-    dev = device or torch.cuda.current_device()
+    dev = _default_device(device)
     z = lambda w: torch.zeros(B, Hkv, S, w, dtype=torch.uint8, device=dev)
     return KV4Cache(z(D // 2), z(D // 16), z(D // 2), z(D // 16))
 

@@ -203,3 +203,23 @@ def test_wrappers_reject_tensors_on_another_device(captured):
                            other(B, dtype=torch.int32), None,
                            layout=(1, 1, 0, 0, 0, 16), row_bytes=16, N=N)
     assert captured == []  # nothing reached the library
+
+
+def test_allocators_take_device_zero(monkeypatch):
+    """device=0 is a device, not "no device", whatever device is current."""
+    seen = []
+    real = torch.zeros
+
+    def make(*a, device=None, **kw):
+        seen.append(device)
+        return real(1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch, "zeros", make)
+    monkeypatch.setattr(torch, "empty", make)
+    monkeypatch.setattr(_lib, "call", lambda *a: 256)
+    for device, want in ((0, 0), (None, 1), ("cpu", "cpu")):
+        seen.clear()
+        api.kv4_cache(1, 2, 3, device=device)
+        api.workspace(_lib.SPEC_OP_CHAIN, 1, 2, 3, device)
+        api.accept_stats_records(4, device=device)
+        assert seen and all(d == want for d in seen), (device, seen)
