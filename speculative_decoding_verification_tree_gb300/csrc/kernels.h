@@ -190,12 +190,11 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
 // A 4-bit cache's unit: a power of two in [2^-64, 2^64].
 bool kv4_unit_ok(float u);
 
-// scale log2(e) unit = m 2^e, m in [1, 2): the product alone, and its product
-// with a query row's power of two, leave float32's range for units and scales
-// that are accepted (row_factor in kv4.cuh puts them together).
+// scale log2(e) unit = half * m, with half a power of two that takes half of its
+// exponent: the product itself leaves float32's range for units and scales that
+// are accepted (row_factor in kv4.cuh puts a row's factor together).
 struct ScoreScale {
-  float m;
-  int e;
+  float half, m;
 };
 ScoreScale score_scale(float scale, float unit);
 

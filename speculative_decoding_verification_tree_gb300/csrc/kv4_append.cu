@@ -207,7 +207,8 @@ ScoreScale score_scale(float scale, float unit) {
   const float ms = frexpf(scale, &es);           // [1/2, 1)
   const float mp = frexpf(ms * kLog2e, &ep);     // rounded as scale * log2(e) is
   frexpf(unit, &eu);                             // unit = 2^(eu - 1)
-  return {2.f * mp, es + ep - 1 + eu - 1};
+  const int e = es + ep + eu - 2;
+  return {ldexpf(1.f, e / 2), ldexpf(2.f * mp, e - e / 2)};
 }
 
 }  // namespace sv

@@ -264,7 +264,7 @@ __device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>&
       else
         sm.qf[warp][x][nt][lane] = h;  // read back by this lane alone
     }
-    const float fg = row_factor(p.scale.m, p.scale.e + e);
+    const float fg = row_factor(p.scale, e);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       f[nt][x] = __shfl_sync(0xffffffffu, fg, 4 * (2 * c + x));

@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv4_tc(const TcParams prm) {
       }
       tst_wait();
       fence_before();
-      f = row_factor(p.scale.m, p.scale.e + e);
+      f = row_factor(p.scale, e);
       if (kNG == 2) {
         sm.rowf[r] = f;
         sm.mref[r] = neg_inf();

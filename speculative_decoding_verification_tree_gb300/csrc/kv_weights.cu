@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kWtThreads, kWtCtas) kv_weights(const WeightPa
         }
         if (lane < D / 4) sm.qf[i >> 3][s][4 * (i & 7) + cc] = make_uint2(h0, h1);
         if (lane == 0) {
-          sm.rowf[i] = kKv4 ? row_factor(p.scale.m, p.scale.e + up) : p.factor;
+          sm.rowf[i] = kKv4 ? row_factor(p.scale, up) : p.factor;
           // a row that saw nothing weighs nothing, whatever the keys hold
           const bool blind = l[x] == neg_inf();
           sm.rowl[i] = blind ? l[x] : -l[x];
