@@ -15,7 +15,7 @@
 // eleven bits for every key within 2^-21 of the reference.  Scores, sums
 // and outputs are float32.
 //
-// Kernel kv4_rows (8, 16, 24 or 32 query rows a tile): warp-level m16n8k16 products
+// Kernel kv4_rows (room for 8, 16, 24 or 32 query rows): warp-level m16n8k16 products
 // with the cache as the 16-row operand, converted in registers, so that it
 // crosses shared memory once, as codes, and eight query rows waste nothing.
 // Each warp owns a ring of 32-key stages filled with cp.async and needs no
@@ -32,8 +32,7 @@
 // Product row n of eight keys is key 4 (n & 1) + n / 2, and the stage's rows are
 // permuted (and their 16-byte chunks exchanged) so that neither read has bank
 // conflicts.
-// Work: the 32-key blocks of all (sequence, head, row tile) units form one
-// line, cut into equal pieces, one per warp, whatever the sequences' lengths; a
+// Work: the 32-key blocks of all (sequence, head) units form one line, cut into equal pieces, one per warp, whatever the sequences' lengths; a
 // unit cut by a piece border leaves partial (m, l, O) in the workspace, and
 // kv4_combine joins them.  Warps never wait for one another.
 // Short work, where the join's launch and traffic would cost more than idle
@@ -62,10 +61,8 @@ constexpr int kRowsMax = 32;    // query rows up to which these kernels are used
 constexpr int kJoinUnroll = 10; // 32-part groups read at once
 
 struct RowsParams : Kv4Attn {
-  int nrt;           // row tiles per (sequence, head)
-  float* part;       // [2 * warps][rows][D]: O of a unit's piece
-  float2* part_ml;   // [2 * warps][rows]: its reference and sum
-  int rows;          // rows of a part: min(R, rows per tile)
+  float* part;       // [2 * warps][R][D]: O of a unit's piece
+  float2* part_ml;   // [2 * warps][R]: its reference and sum
   int warps;         // pieces of the line
 };
 
@@ -77,13 +74,11 @@ __device__ __forceinline__ int seq_blocks(const RowsParams& p, int b) {
   return (clamped_prefix(p, b) + p.N + kKeys - 1) / kKeys;
 }
 
-// The line of blocks: sequences in order, each with `units` runs (heads x row
-// tiles) of seq_blocks.
+// The line of blocks: sequences in order, each with a run of seq_blocks per head.
 struct LineBlocks {
   const RowsParams& p;
-  int units;
   __device__ __forceinline__ int64_t operator()(int b) const {
-    return (int64_t)seq_blocks(p, b) * units;
+    return (int64_t)seq_blocks(p, b) * p.Hkv;
   }
 };
 __device__ __forceinline__ int64_t piece_blocks(int64_t total, int warps) {
@@ -176,12 +171,15 @@ struct LaneFill {
   }
 };
 
-// A lane's share of one row tile of one (sequence, head).
-template <int D, int NT>
-struct Tile {
-  int b, kvh, rt, P;
-  __device__ __forceinline__ int row(int nt, int x) const {  // of the lane's, or -1
-    return rt * 8 * NT + nt * 8 + 2 * (int)(threadIdx.x & 3) + x;
+// One (sequence, head).
+struct Unit {
+  int b, kvh, P;
+  // the lane's row x of row tile nt (opaque, so that what depends on it is
+  // computed where it is used and not held over the key loop)
+  __device__ __forceinline__ int row(int nt, int x) const {
+    int r = nt * 8 + 2 * (int)(threadIdx.x & 3) + x;
+    asm volatile("" : "+r"(r));
+    return r;
   }
   __device__ __forceinline__ uint64_t mask(const RowsParams& p, int nt, int x) const {
     const int r = row(nt, x);
@@ -192,7 +190,7 @@ struct Tile {
     return ((int64_t)b * p.N + r / Gq) * p.Hq + kvh * Gq + r % Gq;
   }
 };
-// Its reference, sum (over the lane's own keys) and output.  m tile j, rows g
+// A lane's references, sums (over its own keys) and outputs of a unit's rows.  m tile j, rows g
 // and g + 8 of the product are dims D/8 g + 2 j and + 2 j + 1, so the lane holds
 // D/8 contiguous dims of its rows: row x in o[j][nt][x] and o[j][nt][2 + x].
 template <int D, int NT>
@@ -203,10 +201,9 @@ struct Acc {
 // One warp over keys key0, key0 + step, ... (32 each) below kend.
 template <int D, int NT>
 __device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>& sm,
-                                           const Tile<D, NT>& t, int key0, int step, int kend,
+                                           const Unit& t, int key0, int step, int kend,
                                            Acc<D, NT>& a) {
   using G = Stage<D>;
-  constexpr int RT = 8 * NT;
   constexpr int kStages = RowsCfg<NT>::kStages;
   constexpr int kSteps = D / 16;      // k steps of S
   constexpr int kMT = D / 16;         // m tiles of O^T
@@ -214,7 +211,7 @@ __device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>&
   constexpr bool kQReg = !RowsCfg<NT>::kQShared;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int b = t.b, kvh = t.kvh, rt = t.rt, P = t.P, L = P + p.N;
+  const int b = t.b, kvh = t.kvh, P = t.P, L = P + p.N;
   const int Gq = p.Hq / p.Hkv;
   const uint32_t ring = smem_u32(sm.ring) + (uint32_t)(warp * kStages * G::kBytes);
   const unsigned char* ringp = sm.ring + warp * kStages * G::kBytes;
@@ -235,7 +232,8 @@ __device__ __forceinline__ void run_blocks(const RowsParams& p, RowsSmem<D, NT>&
   uint2 qr[kSteps][NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = rt * RT + nt * 8 + g;
+    int r = nt * 8 + g;
+    asm volatile("" : "+r"(r));  // as in Unit::row
     const bool valid = r < p.R;
     const int node = valid ? r / Gq : 0;
     const int hq = kvh * Gq + (valid ? r % Gq : 0);
@@ -507,8 +505,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
   launch_dependents();
 
-  const int units = p.Hkv * p.nrt;
-  const LineBlocks line = {p, units};
+  const LineBlocks line = {p};
   scan_line<kThreads>(p.B, line, sm.before, sm.tmp);
   const int64_t total = sm.before[kThreads];
   const int64_t piece = piece_blocks(total, p.warps);
@@ -523,11 +520,11 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   while (at < end) {
     const int P = clamped_prefix(p, b);
     const int nblk = (P + p.N + kKeys - 1) / kKeys;
-    const int unit = (int)((at - seq_start) / nblk);
-    const int64_t unit_start = seq_start + (int64_t)unit * nblk;
+    const int kvh = (int)((at - seq_start) / nblk);
+    const int64_t unit_start = seq_start + (int64_t)kvh * nblk;
     const int k0 = (int)(at - unit_start);
     const int k1 = (int)min((int64_t)nblk, end - unit_start);
-    const Tile<D, NT> t = {b, unit / p.nrt, unit % p.nrt, P};
+    const Unit t = {b, kvh, P};
     Acc<D, NT> a;
     run_blocks<D, NT>(p, sm, t, k0 * kKeys, kKeys, k1 * kKeys, a);
 
@@ -553,7 +550,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
           if (p.lse && g == 0)
             p.lse[orow] = sum == 0.f ? neg_inf() : a.m[nt][x] + log2f(sum) - kLift;
         } else {
-          const int64_t prow = ((int64_t)2 * wid + (first ? 0 : 1)) * p.rows + (r - t.rt * 8 * NT);
+          const int64_t prow = ((int64_t)2 * wid + (first ? 0 : 1)) * p.R + r;
           float4* dst = reinterpret_cast<float4*>(p.part + prow * D + (D / 8) * g);
 #pragma unroll
           for (int j = 0; j < kMT; j += 2)
@@ -564,8 +561,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
       }
     at = unit_start + k1;
     first = false;
-    if (unit + 1 == units && k1 == nblk) {  // the next block belongs to the next sequence
-      seq_start += (int64_t)units * nblk;
+    if (kvh + 1 == p.Hkv && k1 == nblk) {  // the next block belongs to the next sequence
+      seq_start += (int64_t)p.Hkv * nblk;
       ++b;
     }
   }
@@ -589,10 +586,8 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   const int g = lane >> 2, c = lane & 3;
   const int C = p.warps;
   const int rank = blockIdx.x % C;
-  int unit = blockIdx.x / C;
-  Tile<D, NT> t;
-  t.rt = unit % p.nrt;
-  unit /= p.nrt;
+  const int unit = blockIdx.x / C;
+  Unit t;
   t.kvh = unit % p.Hkv;
   t.b = unit / p.Hkv;
   t.P = clamped_prefix(p, t.b);
@@ -606,7 +601,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
   float2* ml = reinterpret_cast<float2*>(sm.ring + kMerge);  // [warp][row]
   float* own = reinterpret_cast<float*>(sm.ring + kOwn);     // [row][D]
   float2* own_ml = reinterpret_cast<float2*>(own + RT * D);
-  const int rows = min(RT, p.R - t.rt * RT);
+  const int rows = p.R;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -623,7 +618,7 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
     }
   __syncthreads();
   auto emit = [&](int row, int chunk, const float4& v, float M, float sum) {
-    const int64_t orow = t.out_row(p, t.rt * RT + row);
+    const int64_t orow = t.out_row(p, row);
     const float inv = sum == 0.f ? 0.f : p.v_unit / sum;
     *reinterpret_cast<uint2*>(p.out + orow * D + 4 * chunk) =
         make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
@@ -682,22 +677,23 @@ __global__ void __launch_bounds__(RowsCfg<NT>::kThreads, RowsCfg<NT>::kCtas)
 // Joins the parts of a unit that several warps worked on: a CTA takes `per_cta`
 // rows of a unit, kJoinWarps / per_cta warps a row.  The units are all of
 // them, or, when there are more units than piece borders, those that hold a
-// border, each found from the first border inside it.
-template <int D, int RT, int kJoinWarps>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+// border, each found from the first border inside it.  The loads it has in flight
+// take registers: left alone the compiler keeps 64 of them (8 sequences of 32 K
+// keys, 32 rows: 149 us for 141).
+template <int D, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinWarps == 8 ? 2 : 1)
     kv4_combine(const RowsParams p, bool by_border, int per_cta) {
   constexpr int kThreads = kJoinWarps * 32;
   __shared__ int64_t before[kThreads + 1], tmp[kJoinWarps];
   __shared__ float acc_s[kJoinWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int units = p.Hkv * p.nrt;
-  const LineBlocks line = {p, units};
+  const LineBlocks line = {p};
   scan_line<kThreads>(p.B, line, before, tmp);
   grid_dependency_wait();  // before any exit: this grid must not end first
   const int64_t total = before[kThreads];
   const int64_t piece = piece_blocks(total, p.warps);
-  Tile<D, RT / 8> t;
-  int unit, nblk;
+  Unit t;
+  int nblk;
   int64_t t0;  // the unit's first block
   if (by_border) {
     const int64_t pos = (int64_t)(blockIdx.x + 1) * piece;
@@ -705,31 +701,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     int64_t start;
     t.b = locate<kThreads>(p.B, line, before, pos, &start);
     nblk = seq_blocks(p, t.b);
-    unit = (int)((pos - start) / nblk);
-    t0 = start + (int64_t)unit * nblk;
+    t.kvh = (int)((pos - start) / nblk);
+    t0 = start + (int64_t)t.kvh * nblk;
     if (t0 == pos || t0 < pos - piece) return;  // not inside, or not the first one inside
   } else {
-    t.b = (int)(blockIdx.x / units);
-    unit = (int)(blockIdx.x % units);
+    t.b = (int)(blockIdx.x / p.Hkv);
+    t.kvh = (int)(blockIdx.x % p.Hkv);
     nblk = seq_blocks(p, t.b);
     const int per = (p.B + kThreads - 1) / kThreads;
-    t0 = before[t.b / per] + (int64_t)unit * nblk;
+    t0 = before[t.b / per] + (int64_t)t.kvh * nblk;
     for (int i = t.b / per * per; i < t.b; ++i) t0 += line(i);
   }
   const int c0 = (int)(t0 / piece), c1 = (int)((t0 + nblk - 1) / piece);
   if (c0 == c1) return;
-  t.kvh = unit / p.nrt;
-  t.rt = unit % p.nrt;
   const int n = c1 - c0 + 1;
   const int lead = t0 == (int64_t)c0 * piece ? 0 : 1;
   const int wpr = max(1, kJoinWarps / per_cta);  // more than one: one row per warp group
-  const int last = min((int)(blockIdx.y + 1) * per_cta, min(RT, p.R - t.rt * RT));
+  const int last = min((int)(blockIdx.y + 1) * per_cta, p.R);
   const int sub = warp % wpr;
   constexpr int kV = D / 32;  // floats per lane
   for (int row = blockIdx.y * per_cta + warp / wpr; row < last || wpr > 1;
        row += kJoinWarps / wpr) {
     auto part = [&](int i) -> int64_t {
-      return ((int64_t)2 * (c0 + i) + (i == 0 ? lead : 0)) * p.rows + row;
+      return ((int64_t)2 * (c0 + i) + (i == 0 ? lead : 0)) * p.R + row;
     };
     float M = neg_inf(), sum = 0.f;  // every warp for itself
     float acc[kV] = {};
@@ -783,7 +777,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
           for (int i = 0; i < kV; ++i) acc[i] += acc_s[warp + w][lane * kV + i];
     }
     if (sub == 0 && row < last) {
-      const int64_t orow = t.out_row(p, t.rt * RT + row);
+      const int64_t orow = t.out_row(p, row);
       const float inv = sum == 0.f ? 0.f : p.v_unit / sum;
       uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + orow * D + lane * kV);
 #pragma unroll
@@ -796,9 +790,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 
 // Pieces (warps) a call uses: no more than its blocks could fill.
 template <int NT>
-int rows_warps(int B, int Hkv, int R, int S) {
-  const int64_t nrt = (R + 8 * NT - 1) / (8 * NT);
-  const int64_t blocks = (int64_t)B * Hkv * nrt * ((S + kKeys - 1) / kKeys);
+int rows_warps(int B, int Hkv, int S) {
+  const int64_t blocks = (int64_t)B * Hkv * ((S + kKeys - 1) / kKeys);
   const int64_t want = (blocks + kMinBlocks - 1) / kMinBlocks;
   return (int)(want < RowsCfg<NT>::kPieces ? want : RowsCfg<NT>::kPieces);
 }
@@ -824,10 +817,8 @@ int unit_cluster(int64_t units, int S) {
 // Bytes of the pieces' partial results: 0 when clusters do without.
 template <int NT>
 size_t part_bytes(int B, int Hkv, int R, int D, int S) {
-  const int64_t units = (int64_t)B * Hkv * ((R + 8 * NT - 1) / (8 * NT));
-  if (unit_cluster<NT>(units, S) > 0) return 0;
-  const int rows = R < 8 * NT ? R : 8 * NT;
-  return (size_t)2 * rows_warps<NT>(B, Hkv, R, S) * rows * (D + 2) * sizeof(float);
+  if (unit_cluster<NT>((int64_t)B * Hkv, S) > 0) return 0;
+  return (size_t)2 * rows_warps<NT>(B, Hkv, S) * R * (D + 2) * sizeof(float);
 }
 size_t attn_ws(int B, int Hkv, int R, int D, int S) {
   if (R > kRowsMax) return kv4_tc_ws(B, Hkv, R, D, S);
@@ -841,21 +832,18 @@ template <int D, int NT>
 cudaError_t launch_rows(const Kv4Attn& a, void* ws, cudaStream_t st) {
   RowsParams p = {};
   (Kv4Attn&)p = a;
-  constexpr int RT = 8 * NT;
   using Cfg = RowsCfg<NT>;
   constexpr int smem = (int)sizeof(RowsSmem<D, NT>);
   static_assert((smem + 1024) * Cfg::kCtas <= 228 * 1024, "the pieces are resident at once");
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem((const void*)kv4_rows<D, NT>, smem, done);
   if (e != cudaSuccess) return e;
-  p.nrt = (p.R + RT - 1) / RT;
-  p.rows = p.R < RT ? p.R : RT;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = st;
   cudaLaunchAttribute attr;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const int64_t units = (int64_t)p.B * p.Hkv * p.nrt;
+  const int64_t units = (int64_t)p.B * p.Hkv;
   const int cluster = unit_cluster<NT>(units, p.S);
   if (cluster > 0) {
     static std::atomic<uint64_t> done_unit{0};
@@ -873,9 +861,9 @@ cudaError_t launch_rows(const Kv4Attn& a, void* ws, cudaStream_t st) {
     prof_end(SPEC_PROF_ATTN, st);
     return e;
   }
-  p.warps = rows_warps<NT>(p.B, p.Hkv, p.R, p.S);
+  p.warps = rows_warps<NT>(p.B, p.Hkv, p.S);
   p.part = (float*)ws;
-  p.part_ml = (float2*)(p.part + (size_t)2 * p.warps * p.rows * D);
+  p.part_ml = (float2*)(p.part + (size_t)2 * p.warps * p.R * D);
   prof_begin(SPEC_PROF_ATTN, st);
   kv4_rows<D, NT><<<(p.warps + Cfg::kWarps - 1) / Cfg::kWarps, Cfg::kThreads, smem, st>>>(p);
   prof_end(SPEC_PROF_ATTN, st);
@@ -883,19 +871,19 @@ cudaError_t launch_rows(const Kv4Attn& a, void* ws, cudaStream_t st) {
   if (e != cudaSuccess || p.warps == 1) return e;
   const bool by_border = units > p.warps - 1;
   const int64_t joins = by_border ? p.warps - 1 : units;
-  const int per_cta = joins * p.rows <= 2 * kSms ? 1 : p.rows;
+  const int per_cta = joins * p.R <= 2 * kSms ? 1 : p.R;
   // a row of a long unit has many parts: sixteen warps read them; elsewhere
   // eight warps share the rows (one sequence of 128 K keys 43 -> 41 us, 64 of
   // 32 K 381 us against 390 with sixteen)
-  cfg.gridDim = dim3((unsigned)joins, (unsigned)((p.rows + per_cta - 1) / per_cta));
+  cfg.gridDim = dim3((unsigned)joins, (unsigned)((p.R + per_cta - 1) / per_cta));
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   if (per_cta == 1) {
     cfg.blockDim = dim3(16 * 32);
-    return cudaLaunchKernelEx(&cfg, kv4_combine<D, RT, 16>, p, by_border, per_cta);
+    return cudaLaunchKernelEx(&cfg, kv4_combine<D, 16>, p, by_border, per_cta);
   }
   cfg.blockDim = dim3(8 * 32);
-  return cudaLaunchKernelEx(&cfg, kv4_combine<D, RT, 8>, p, by_border, per_cta);
+  return cudaLaunchKernelEx(&cfg, kv4_combine<D, 8>, p, by_border, per_cta);
 }
 
 }  // namespace
