@@ -526,6 +526,8 @@ int spec_tree_attention_kv4(const void* q, const uint8_t* k_codes,
  *
  * q [B, N, Hq, D] bf16 and lse [B, N, Hq] float32 as the attention call took
  * and returned them (a row with lse = -inf saw nothing and adds nothing).
+ * D is 64 or 128; spec_tree_attention_lse has D 128 alone, so for a bf16 cache
+ * of D 64 the normalisers are the caller's own.
  * path_nodes [B, N] int32, or NULL: the first path_len[b] rows (a chain, or
  * N = 1).  A path whose length is outside [0, N] or which names a node outside
  * [0, N) adds nothing (path_len then counts as 0).  prefix_len is clamped to
@@ -551,7 +553,8 @@ int spec_kv_weights(const void* q, const void* k, const uint8_t* k_scales,
  * counts as -inf).  The kept positions stay in order and move to 0, 1, ...
  * together with their weights.  A sequence no longer than the budget keeps
  * everything.
- * weights [B, Hkv, S] float32, length [B] int32 (clamped to [0, S]).
+ * weights [B, Hkv, S] float32, length [B] int32 (clamped to [0, S]: the -1 that
+ * spec_kv_commit gives for an invalid path counts as 0).
  * planes: n_planes host pointers to device arrays [B, Hkv, S, row_bytes[i]]
  *     (keys, values, codes, scales, ...); planes_out [B, Hkv, S_out,
  *     row_bytes[i]] receive the kept rows.  planes_out[i] == planes[i] (with

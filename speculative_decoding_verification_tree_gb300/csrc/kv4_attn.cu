@@ -32,16 +32,20 @@
 // Product row n of eight keys is key 4 (n & 1) + n / 2, and the stage's rows are
 // permuted (and their 16-byte chunks exchanged) so that neither read has bank
 // conflicts.
-// Work: the 32-key blocks of all (sequence, head) units form one line, cut into equal pieces, one per warp, whatever the sequences' lengths; a
-// unit cut by a piece border leaves partial (m, l, O) in the workspace, and
-// kv4_combine joins them.  Warps never wait for one another.
+// Work: the 32-key blocks of all (sequence, head) units form one line, cut into
+// equal pieces, one per warp, whatever the sequences' lengths; a unit cut by a
+// piece border leaves partial (m, l, O) in the workspace, and kv4_combine joins
+// them.  Warps never wait for one another.
 // Short work, where the join's launch and traffic would cost more than idle
 // warps, takes kv4_unit instead: a cluster of CTAs per unit, its warps' results
 // joined through distributed shared memory (unit_cluster has the rule).
-// Bounds and times (D 128, 32 / 8 heads, single tokens): 64 sequences of 32 K
-// keys, 2.39 GB of cache, 381 us = 6.3 TB/s, HBM; 32 of 2 to 4 K keys, 114 MB, 32
-// us = 3.6 TB/s, issue (55%) and the load latency of a unit's first and last
-// blocks; one sequence of 1 K keys 6.4 us, launch and one block's latency.
+// Bounds and times (D 128, 32 / 8 heads, single tokens, caches cold): 64 sequences
+// of 32 K keys, 2.39 GB of cache, 379 us = 6.3 TB/s, HBM; 32 of 2 to 4 K keys, 114
+// MB, 32.7 us = 3.5 TB/s, uneven work (256 CTAs, one per sequence and head, on 304
+// places, lengths apart by two: 27 us at the copy rate), then issue (55%) and the
+// load latency of a unit's first and last blocks; one sequence of 128 K keys 40.5
+// us, the join of 2341 pieces; one of 1 K keys 6.4 us, launch and one block's
+// latency.
 #include <cuda_runtime.h>
 #include <stddef.h>
 
@@ -106,8 +110,9 @@ struct Stage {
 // Warps per CTA, CTAs per SM and ring stages by the number of row tiles of
 // eight, whose outputs take 32 registers each (D 128).  Products for rows that
 // are not there cost as much as others: 20 rows in three tiles 58 us, in four 72
-// (32 sequences of 2 to 4 K keys), 180 / 226 (16 of 32 K).  Three tiles with ten
-// warps, q in shared memory, 72.
+// (32 sequences of 2 to 4 K keys), 182 / 226 (16 of 32 K).  Three tiles with ten
+// warps, q in shared memory, 72.  At D 128 kv4_rows spills with two tiles (92 bytes
+// stored, 152 loaded a thread, at 168 registers) and with four (56 / 64 at 255).
 template <int NT>
 struct RowsCfg {
   static constexpr int kWarps = NT == 2 ? 12 : 8;
@@ -795,13 +800,15 @@ int rows_warps(int B, int Hkv, int S) {
   const int64_t want = (blocks + kMinBlocks - 1) / kMinBlocks;
   return (int)(want < RowsCfg<NT>::kPieces ? want : RowsCfg<NT>::kPieces);
 }
-// CTAs per cluster of kv4_unit, or 0 for pieces of the line.  Units leave
+// CTAs per cluster of kv4_unit, or 0 for pieces of the line, by the cache's
+// capacity S (the host does not know the lengths).  Units leave
 // some of the resident CTAs idle, or the last wave part empty, for as many
 // 32-key blocks a warp as the longest unit may have; pieces cost the join's
 // launch and partial outputs.  Measured (32 / 8 heads, D 128): units 6.4 us,
 // pieces 15.9 us at one sequence of 1 K keys, 9.6 / 17.0 at 8 K, 22.2 / 21.6
 // at 32 K, 75.8 / 40.6 at 128 K; 32 sequences of up to 4 K 31.7 / 34.3, 64 of
-// them 57.4 / 55.5, 64 of 32 K 438 / 381.
+// them 57.4 / 55.5 (where the rule stays with units), 64 of 32 K 438 / 381.  One
+// sequence of 1 K keys in a cache of 32 K or 128 K positions: pieces, 15.7 us.
 template <int NT>
 int unit_cluster(int64_t units, int S) {
   constexpr int64_t slots = kSms * RowsCfg<NT>::kCtas;
@@ -893,8 +900,9 @@ using namespace sv;
 
 // More than kRowsMax query rows per key/value head go to the tensor-core kernel
 // (kv4_attn_tc.cu).  Measured (D 128): 32 sequences of 2 to 4 K keys, 16 rows
-// 48 us here and 73 there, 20 rows 58 / 73, 32 rows 75 / 72 us; 8 sequences of
-// 32 K keys, 32 rows 141 / 165 us; one of 1 K keys 15 / 14 us.
+// 48 us here and 73 there, 20 rows 58 / 73, 32 rows 75 / 72 us; one of 1 K keys,
+// 32 rows 15 / 14 us; 8 sequences of 32 K keys, 32 rows 141 / 165 us, for which
+// 32 rows stay here.
 extern "C" size_t spec_tree_attention_kv4_workspace_bytes(int B, int N, int Hq, int Hkv, int D,
                                                           int S) {
   if (B < 0 || B > 65535 || N < 1 || N > 64 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || S < N ||

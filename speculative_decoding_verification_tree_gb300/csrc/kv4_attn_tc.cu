@@ -20,7 +20,7 @@
 // own, so that one group exponentiates while the other's scores are made; the
 // rows' references pass between the groups block by block.
 // Bound: the softmax warps and the single S buffer of a tile.  32 sequences of 2
-// to 4 K keys, 240 rows (60 nodes, 4 heads a group), D 128: 107 us = 920 TFLOP/s,
+// to 4 K keys, 240 rows (60 nodes, 4 heads a group), D 128: 108 us = 913 TFLOP/s,
 // 1.2 TB/s; per 64-key block of a tile about 1930 cycles, of which the products
 // take 1250 of the tensor pipe for both tiles.  One tile: 64 rows 73 us, 128 rows
 // 73 us (as half of a two-tile CTA 87 and 79 us).
@@ -618,10 +618,13 @@ __global__ void __launch_bounds__(256) kv4_tc_combine(const TcParams prm, int kR
 }
 
 // Shares of a unit's blocks: the number that fills the SMs best, counted in
-// blocks of the longest unit (a CTA's start costs about three, the join's launch
-// and traffic about eight).  Measured with this rule and unsplit: 240 rows, one
+// blocks of a unit as long as the cache's capacity S (a CTA's start costs about
+// three, the join's launch and traffic about eight; the host does not know the
+// lengths).  Measured with this rule and unsplit: 240 rows, one
 // sequence of 128 K keys 127 us / 1896 us, of 1 K keys 25.3 / 25.2; five ragged
-// ones of up to 5 K keys, 2 heads, D 64 18.7 / 77.4.
+// ones of up to 5 K keys, 2 heads, D 64 19.1 / 77.4.  Capacity far above the
+// lengths costs empty shares: 32 sequences of 2 to 4 K keys, 240 rows, 108 us at
+// S 4160 (unsplit), 352 us and 341 MB of partial results at S 131137 (ten shares).
 int tc_splits(int64_t units, int S) {
   const int64_t blocks = (S + kKB - 1) / kKB;
   int best = 1;

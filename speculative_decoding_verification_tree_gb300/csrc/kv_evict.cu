@@ -21,10 +21,11 @@
 // that a later chunk still has to read.
 // Bounds and times (pick: latency of its barriers, cluster exchanges and passes;
 // gather: HBM): 32 sequences of 2 to 4 K positions, 8 heads, 4-bit rows of D 128,
-// half kept (159 MB): 39 us, 12 of them the pick; the gather also pays for the
+// half kept (159 MB): 39 us, 13 of them the pick; the gather also pays for the
 // other halves of 128-byte lines.  One sequence of 128 K positions, 8 heads, bf16
-// rows, 16 K kept (139 MB): 38.5 us, about 14 of them the pick; the pick of 208
-// pairs of 45 K weights: 48 us.  (Weights in registers, with whole scans in every
+// rows, 16 K kept (139 MB): 41.5 us, half of them the pick, caches cold; in place
+// 62, 36 of them the sweep (33% of DRAM's rate: each CTA's chunks in order, two
+// barriers each); the pick of 208 pairs of 45 K weights: 48 us.  (Weights in registers, with whole scans in every
 // pass, took 41, 44 and 95: instruction fetch of the unrolled code, one CTA per
 // SM.)
 #include "kernels.h"
@@ -517,10 +518,13 @@ cudaError_t launch_moves(const MovePlanes& out, int n_out, const MovePlanes& in,
       most = most > c ? most : c;
       ctas += pairs * c;
     }
-    // few CTAs take longer chunks.  The call in place, 1024 / 512 / 256 threads: 128
-    // CTAs (8 pairs, 16 K bf16 rows kept) 62 / 68 / 95 us; 384 (64 pairs, 8 K 4-bit
-    // rows) 85 / 88 / 103; 512 (32 pairs, 4 K bf16 rows) 60 / 56 / 52; 1536 (256
-    // pairs, 2 K 4-bit rows) 58 / 46 / 44.
+    // few CTAs take longer chunks.  The call in place, 1024 / 512 / 256 threads, caches
+    // cold: 64 CTAs (4 pairs, 16 K bf16 rows kept) 47 / 60 / 86 us; 128 (8 pairs) 62 /
+    // 68 / 95; 256 (16 pairs, 8 K bf16 rows) 58 / 55 / 65; 384 (64 pairs, 8 K 4-bit
+    // rows) 65 / 56 / 65; 512 (32 pairs, 4 K bf16 rows) 49 / 47 / 42; 768 (128 pairs, 2
+    // K 4-bit rows) 32 / 27 / 25; 1536 (256 pairs) 57 / 47 / 46.  Not the best at 192
+    // (32 pairs, 8 K 4-bit rows: 33 / 38 / 51) and 384 of bf16 rows (24 pairs, 8 K
+    // rows: 74 / 77 / 63).
     cfg.blockDim = dim3(ctas <= 152 ? kSweepMost : (ctas <= 400 ? kSweepMost / 2 : kMoveThreads));
     cfg.gridDim = dim3((unsigned)pairs, (unsigned)n_in, (unsigned)most);
     e = cudaLaunchKernelEx(&cfg, evict_sweep, in, kept, budget, (int64_t)S);

@@ -20,11 +20,12 @@
 // its sum has a fixed order: no atomics.
 // Work: the 256-key blocks (32 keys a warp) of all (sequence, head) pairs form
 // one line, cut into equal pieces, one per resident CTA.
-// Bounds and times (32 sequences of 2 to 4 K keys, 32 / 8 heads, D 128): bf16, one
-// row a head, 208 MB in 36 us = 5.8 TB/s, HBM; 4-bit after a 60-node tree, 64 MB
-// in 29 us = 2.2 TB/s, the latency of conversion, product and exponential in one
-// warp's 32 keys (issue 47%; a third CTA per SM, or 4-bit keys loaded straight
-// into registers, measured slower).
+// Bounds and times (32 sequences of 2 to 4 K keys, 32 / 8 heads, D 128, caches
+// cold): bf16, one row a head, 208 MB in 37 us = 5.6 TB/s, HBM; 4-bit after a
+// 60-node tree, 64 MB in 34 us = 1.9 TB/s (30 us with keys and weights in L2), the
+// latency of conversion, product and exponential in one warp's 32 keys (issue
+// 47%; a third CTA per SM, or 4-bit keys loaded straight into registers, measured
+// slower).
 #include <cfloat>
 #include <type_traits>
 
