@@ -195,9 +195,9 @@ struct Unit {
     return ((int64_t)b * p.N + r / Gq) * p.Hq + kvh * Gq + r % Gq;
   }
 };
-// A lane's references, sums (over its own keys) and outputs of a unit's rows.  m tile j, rows g
-// and g + 8 of the product are dims D/8 g + 2 j and + 2 j + 1, so the lane holds
-// D/8 contiguous dims of its rows: row x in o[j][nt][x] and o[j][nt][2 + x].
+// A lane's references, sums (over its own keys) and outputs of a unit's rows.  m
+// tile j, rows g and g + 8 of the product are dims D/8 g + 2 j and + 2 j + 1, so the
+// lane holds D/8 contiguous dims of its rows: row x in o[j][nt][x] and o[j][nt][2 + x].
 template <int D, int NT>
 struct Acc {
   float m[NT][2], l[NT][2], o[D / 16][NT][4];

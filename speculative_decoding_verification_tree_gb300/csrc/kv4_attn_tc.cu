@@ -620,11 +620,11 @@ __global__ void __launch_bounds__(256) kv4_tc_combine(const TcParams prm, int kR
 // Shares of a unit's blocks: the number that fills the SMs best, counted in
 // blocks of a unit as long as the cache's capacity S (a CTA's start costs about
 // three, the join's launch and traffic about eight; the host does not know the
-// lengths).  Measured with this rule and unsplit: 240 rows, one
-// sequence of 128 K keys 127 us / 1896 us, of 1 K keys 25.3 / 25.2; five ragged
-// ones of up to 5 K keys, 2 heads, D 64 19.1 / 77.4.  Capacity far above the
-// lengths costs empty shares: 32 sequences of 2 to 4 K keys, 240 rows, 108 us at
-// S 4160 (unsplit), 352 us and 341 MB of partial results at S 131137 (ten shares).
+// lengths).  Measured with this rule and unsplit: 240 rows, one sequence of 128 K
+// keys 127 us / 1896 us, of 1 K keys 25.3 / 25.2; five ragged ones of up to 5 K
+// keys, 2 heads, D 64 19.1 / 77.4.  Capacity far above the lengths costs empty
+// shares: 32 sequences of 2 to 4 K keys, 240 rows, 108 us at S 4160 (unsplit), 352 us
+// and 341 MB of partial results at S 131137 (ten shares).
 int tc_splits(int64_t units, int S) {
   const int64_t blocks = (S + kKB - 1) / kKB;
   int best = 1;

@@ -25,9 +25,9 @@
 // other halves of 128-byte lines.  One sequence of 128 K positions, 8 heads, bf16
 // rows, 16 K kept (139 MB): 41.5 us, half of them the pick, caches cold; in place
 // 62, 36 of them the sweep (33% of DRAM's rate: each CTA's chunks in order, two
-// barriers each); the pick of 208 pairs of 45 K weights: 48 us.  (Weights in registers, with whole scans in every
-// pass, took 41, 44 and 95: instruction fetch of the unrolled code, one CTA per
-// SM.)
+// barriers each); the pick of 208 pairs of 45 K weights: 48 us.  (Weights in
+// registers, with whole scans in every pass, took 41, 44 and 95: instruction fetch
+// of the unrolled code, one CTA per SM.)
 #include "kernels.h"
 #include "common.cuh"
 

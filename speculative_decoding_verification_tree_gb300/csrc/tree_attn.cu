@@ -544,8 +544,8 @@ static int tree_attention(const void* q, const void* k_cache, const void* v_cach
   cudaStream_t st = (cudaStream_t)stream;
   prof_begin(SPEC_PROF_ATTN, st);
   tree_attn_tc<<<grid, kAThreads, kASmemBytes, st>>>(
-      mk, mv, (const uint16_t*)q, prefix_len, mask_bits, N, Hq, Hkv, S, fminf(scale * kLog2e, FLT_MAX),
-      (uint16_t*)out, lse);
+      mk, mv, (const uint16_t*)q, prefix_len, mask_bits, N, Hq, Hkv, S,
+      fminf(scale * kLog2e, FLT_MAX), (uint16_t*)out, lse);
   prof_end(SPEC_PROF_ATTN, st);
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
