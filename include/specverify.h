@@ -588,6 +588,70 @@ int spec_philox_uniforms(uint64_t seed, uint32_t offset, const int32_t* b,
                          const int32_t* idx, const int32_t* slot, int n,
                          float* out, void* stream);
 
+/*
+ * Log probabilities of given tokens under softmax(z / T), with each row's
+ * normaliser, entropy and most probable alternatives, in one pass over the
+ * logits: what a caller reports for the tokens a step emitted, or rates
+ * finished answers with.
+ *
+ * logits [R, V] dtype (SPEC_F32 / SPEC_BF16), row r at logits + r*ld elements
+ *     (ld >= V: a padded vocabulary's rows need not be copied).
+ * rows [M] int32, or NULL for rows 0 .. M-1 (M <= R): the logit row of each
+ *     output row, any row any number of times.  An entry outside [0, R) is an
+ *     absent row: log probabilities, normaliser and entropy 0, ids -1.
+ * tokens [M, n] int32: the given tokens, repeats allowed.  A token outside
+ *     [0, V), like the verifier's -1 padding, gets log probability 0.
+ * logprob [M, n] float32 (out): ln p(token).
+ * row_lse [M] float32 (out, may be NULL): base-2 log normaliser
+ *     log2 sum_v 2^(z_v log2(e) / T), as spec_lm_head writes it.
+ * entropy [M] float32 (out, may be NULL): -sum p ln p.
+ * top_ids [M, top] int32, top_logprob [M, top] float32 (out; NULL if top is 0):
+ *     the `top` most probable tokens, best first, equal logits by lower index
+ *     (0 and -0 are equal).
+ * Sums are float32; no atomics order a result, so equal calls give equal bits.
+ * A logit of -inf is a token of probability 0.  A row with NaN or +inf, or with
+ * nothing but -inf, has NaN log probabilities and entropy (alternatives are
+ * still ordered by logit; NaN is never one, and where numbers run out ids are
+ * -1 with NaN).
+ * Errors: SPEC_ERR_DTYPE; SPEC_ERR_SHAPE for sizes < 0, V outside [1,
+ * SPEC_MAX_VOCAB], ld < V, n > SPEC_MAX_CHILDREN, top > min(V,
+ * SPEC_MAX_TOP_K), M > R without rows, or M >= 2^28; SPEC_ERR_ARG for a
+ * temperature that is not finite and > 0, a missing array, or one not aligned
+ * to its elements.  M == 0 does nothing.
+ */
+int spec_token_logprobs(const void* logits, int dtype, int64_t ld, int R, int V,
+                        const int32_t* rows, int M, const int32_t* tokens,
+                        int n, int top, float temperature, float* logprob,
+                        float* row_lse, float* entropy, int32_t* top_ids,
+                        float* top_logprob, void* stream);
+
+/*
+ * Gradient of sum_j g_logprob ln p(token_j) + sum_j g_top ln p(top_id_j) +
+ * g_entropy H with respect to the logits, row by row:
+ *   dz_x = (1/T) (sum_j g_j 1[t_j = x] - p_x (sum_j g_j + g_H (ln p_x + H)))
+ * with t_j, g_j over the given tokens and the alternatives (which are taken as
+ * given tokens: their choice has no gradient), repeated ones adding up and
+ * tokens outside [0, V) left out.
+ * row_lse [M] and entropy [M]: what spec_token_logprobs returned for these rows
+ *     at this temperature (without `rows`).  entropy and g_entropy [M] may both
+ *     be NULL; tokens, g_logprob [M, n] or top_ids, g_top [M, top] may be NULL
+ *     if n or top is 0.
+ * grad [M, V] (out, dtype of the logits, row r at grad + r*ld_grad): computed in
+ *     float32, rounded once.  What lies between the rows is not written.  grad
+ *     may be the logits themselves (same pointer and stride); no other overlap.
+ * A logit of -inf has gradient 0 (plus its own g_j).
+ * Errors as spec_token_logprobs, SPEC_ERR_ARG for one of entropy / g_entropy
+ * alone or a grad that overlaps the logits otherwise; SPEC_ERR_SHAPE if
+ * M * ceil(V / (1024 x logits per 16 bytes)) reaches 2^31.
+ */
+int spec_token_logprobs_grad(const void* logits, int dtype, int64_t ld, int M,
+                             int V, const int32_t* tokens, int n,
+                             const int32_t* top_ids, int top, float temperature,
+                             const float* row_lse, const float* entropy,
+                             const float* g_logprob, const float* g_top,
+                             const float* g_entropy, void* grad,
+                             int64_t ld_grad, void* stream);
+
 /* Human-readable name of a return code. */
 const char* spec_error_string(int code);
 

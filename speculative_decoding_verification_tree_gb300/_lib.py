@@ -81,6 +81,7 @@ class SpecAcceptStats(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
@@ -131,6 +132,10 @@ _SIGNATURES = {
     "spec_kv_evict": (_I, [_P, _P, _I, _I, _I, _I, _I, _I,
                            ctypes.POINTER(_P), ctypes.POINTER(_P),
                            ctypes.POINTER(_I), _I, _P, _P, _P, _P]),
+    "spec_token_logprobs": (_I, [_P, _I, _L, _I, _I, _P, _I, _P, _I, _I, _F,
+                                 _P, _P, _P, _P, _P, _P]),
+    "spec_token_logprobs_grad": (_I, [_P, _I, _L, _I, _I, _P, _I, _P, _I, _F,
+                                      _P, _P, _P, _P, _P, _P, _L, _P]),
     "spec_profile_enable": (_I, [_I]),
     "spec_profile_read": (_I, [_I, ctypes.POINTER(ctypes.c_double),
                                ctypes.POINTER(ctypes.c_int)]),

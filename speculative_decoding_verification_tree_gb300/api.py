@@ -658,6 +658,125 @@ def spec_kv_evict(weights, length, planes, *, budget, recent, planes_out=None,
     return kept, new_len
 
 
+class TokenLogprobs(NamedTuple):
+    """Result of spec_token_logprobs; what was not asked for is None."""
+    logprob: torch.Tensor
+    lse: torch.Tensor
+    entropy: torch.Tensor | None
+    top_ids: torch.Tensor | None
+    top_logprob: torch.Tensor | None
+
+
+def _rows(t, dev, name):
+    """Address and row stride of a [..., V] tensor whose rows lie at one
+    stride (a padded vocabulary's view has one)."""
+    if t.dtype not in _DT:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"all tensors must be on cuda:{dev}; got one on "
+                         f"{t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-1]
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: a row must be contiguous")
+    ld, rows = None, 1
+    for size, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = step
+        elif step != ld * rows:
+            raise ValueError(f"{name}: rows must lie at one stride")
+        rows *= size
+    return t.data_ptr(), t.shape[-1] if ld is None else ld
+
+
+def _per_row(t, lead, what):
+    """Entries per row of a [...] or [..., n] tensor over rows `lead`."""
+    if t.shape == lead:
+        return 1
+    if t.dim() == len(lead) + 1 and t.shape[:-1] == lead:
+        return t.shape[-1]
+    raise ValueError(f"{what} must have shape {tuple(lead)} or "
+                     f"{tuple(lead)} + (n,), got {tuple(t.shape)}")
+
+
+def spec_token_logprobs(logits, tokens, *, temperature=1.0, top=0,
+                        entropy=False, rows=None, stream=None):
+    """Log probabilities of given tokens (see the C declaration).  logits
+    [..., V] float32 or bf16, the rows at one stride (a view of padded rows is
+    fine); tokens [...] or [..., n] int32, -1 for none; rows: an int32 tensor
+    naming the logit row (of all, flattened) of each output row, whose shape
+    then takes the place of the logits' leading one.  Returns TokenLogprobs:
+    logprob of the tokens' shape, lse [...] (base 2), entropy [...], top_ids
+    and top_logprob [..., top]."""
+    V = logits.shape[-1]
+    lead = logits.shape[:-1]
+    dev = _index(logits)
+    la, ld = _rows(logits, dev, "logits")
+    R = M = math.prod(lead)
+    ra = None
+    if rows is not None:
+        lead = rows.shape
+        ra, M = _arg(rows, torch.int32, lead, dev, "rows"), rows.numel()
+    n = _per_row(tokens, lead, "tokens")
+    ta = _arg(tokens, torch.int32, tokens.shape, dev, "tokens")
+    f32 = torch.float32
+    lp = _alloc(tokens.shape, f32, dev, stream)
+    lse = _alloc(lead, f32, dev, stream)
+    ent = _alloc(lead, f32, dev, stream) if entropy else None
+    ids = tl = None
+    if top:
+        ids = _alloc(lead + (top,), torch.int32, dev, stream)
+        tl = _alloc(lead + (top,), f32, dev, stream)
+    _enqueue("spec_token_logprobs", dev, stream, la, _DT[logits.dtype], ld, R,
+             V, ra, M, ta, n, top, temperature, lp.data_ptr(), lse.data_ptr(),
+             None if ent is None else ent.data_ptr(),
+             None if ids is None else ids.data_ptr(),
+             None if tl is None else tl.data_ptr())
+    return TokenLogprobs(lp, lse, ent, ids, tl)
+
+
+def spec_token_logprobs_grad(logits, tokens, lse, g_logprob, *,
+                             temperature=1.0, entropy=None, g_entropy=None,
+                             top_ids=None, g_top=None, out=None, stream=None):
+    """Gradient with respect to the logits of what spec_token_logprobs (without
+    `rows`) returned, given the gradients of its log probabilities, entropy and
+    alternatives' log probabilities (see the C declaration).  out: a [..., V]
+    tensor of the logits' dtype with rows at one stride, which may be `logits`
+    itself.  Returns out."""
+    V = logits.shape[-1]
+    lead = logits.shape[:-1]
+    dev = _index(logits)
+    la, ld = _rows(logits, dev, "logits")
+    f32 = torch.float32
+    n = _per_row(tokens, lead, "tokens")
+    ta = _arg(tokens, torch.int32, tokens.shape, dev, "tokens")
+    ga = _arg(g_logprob, f32, tokens.shape, dev, "g_logprob")
+    if (entropy is None) != (g_entropy is None):
+        raise ValueError("entropy and g_entropy go together")
+    if (top_ids is None) != (g_top is None):
+        raise ValueError("top_ids and g_top go together")
+    ea = ha = ia = xa = None
+    top = 0
+    if entropy is not None:
+        ea = _arg(entropy, f32, lead, dev, "entropy")
+        ha = _arg(g_entropy, f32, lead, dev, "g_entropy")
+    if top_ids is not None:
+        top = top_ids.shape[-1]
+        ia = _arg(top_ids, torch.int32, lead + (top,), dev, "top_ids")
+        xa = _arg(g_top, f32, lead + (top,), dev, "g_top")
+    if out is None:
+        out = _alloc(logits.shape, logits.dtype, dev, stream)
+    if out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the logits' shape and dtype")
+    oa, ldo = _rows(out, dev, "out")
+    _enqueue("spec_token_logprobs_grad", dev, stream, la, _DT[logits.dtype],
+             ld, math.prod(lead), V, ta, n, ia, top, temperature,
+             _arg(lse, f32, lead, dev, "lse"), ea, ga, xa, ha, oa, ldo)
+    return out
+
+
 def spec_get_status(ws, stream=None) -> int:
     v = ctypes.c_uint32(0)
     with _on(_device(ws, stream=stream)):
