@@ -589,6 +589,43 @@ int spec_philox_uniforms(uint64_t seed, uint32_t offset, const int32_t* b,
                          float* out, void* stream);
 
 /*
+ * Causal attention over whole prompts, packed one after another: the pass that
+ * makes the keys, values and hidden states which verification later reads.
+ * Prompt b is tokens seq_start[b] .. seq_start[b+1] - 1, and its token i gives
+ *
+ *   o[i,h] = sum_{j <= i} softmax_j(scale * q[i,h] . k[j,h/G]) v[j,h/G]
+ *
+ * over the prompt's own tokens (G = Hq / Hkv query heads per key/value head).
+ *
+ * Layout (device, bf16 stored as uint16): q [T, Hq, D], k and v [T, Hkv, D] with
+ *   the given strides between tokens in elements (multiples of 8, at least a
+ *   token's heads: slices of one projection's output need no copy); heads and
+ *   dims of a token are contiguous.  out [T, Hq, D] contiguous.  seq_start
+ *   [B+1] int32, ascending from 0 (or later) to at most T; values are clamped to
+ *   [0, T], a prompt that does not ascend is empty, and a token of two prompts
+ *   gets the result of either.
+ * lse [T, Hq] float32 (out, may be NULL): the rows' base-2 log normalisers, as
+ *   spec_tree_attention_lse writes them.
+ * Tokens outside every prompt are not written.  Empty prompts are fine.
+ * Softmax and accumulation in float32, weights rounded to bf16 for the second
+ * product, the output to bf16.  A token's NaN or infinite key or value reaches
+ * its own and later tokens of its prompt only.  Deterministic.
+ * Errors: SPEC_ERR_SHAPE for sizes < 0, Hq % Hkv != 0, G > 128, T >
+ * SPEC_MAX_POSITIONS or strides too small; SPEC_ERR_UNSUPPORTED unless D is 64
+ * or 128 and the strides are multiples of 8; SPEC_ERR_ARG for scale <= 0 or not
+ * finite, a NULL pointer (B, T > 0), q, k, v or out not 16-byte aligned,
+ * seq_start or lse not 4-byte aligned; SPEC_ERR_CUDA if the tensors cannot be
+ * described to the copy engine.  B == 0 or T == 0 does nothing.
+ * Runs on the tensor cores (tcgen05).  Its waits are bounded; rows of a CTA
+ * whose wait gave up (after about a second) are NaN, as there is no status word.
+ */
+int spec_prompt_attention(const void* q, int64_t q_token, const void* k,
+                          int64_t k_token, const void* v, int64_t v_token,
+                          const int32_t* seq_start, int B, int T, int Hq,
+                          int Hkv, int D, float scale, void* out, float* lse,
+                          void* stream);
+
+/*
  * Log probabilities of given tokens under softmax(z / T), with each row's
  * normaliser, entropy and most probable alternatives, in one pass over the
  * logits: what a caller reports for the tokens a step emitted, or rates

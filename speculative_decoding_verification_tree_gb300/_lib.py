@@ -132,6 +132,8 @@ _SIGNATURES = {
     "spec_kv_evict": (_I, [_P, _P, _I, _I, _I, _I, _I, _I,
                            ctypes.POINTER(_P), ctypes.POINTER(_P),
                            ctypes.POINTER(_I), _I, _P, _P, _P, _P]),
+    "spec_prompt_attention": (_I, [_P, _L, _P, _L, _P, _L, _P, _I, _I, _I, _I,
+                                   _I, _F, _P, _P, _P]),
     "spec_token_logprobs": (_I, [_P, _I, _L, _I, _I, _P, _I, _P, _I, _I, _F,
                                  _P, _P, _P, _P, _P, _P]),
     "spec_token_logprobs_grad": (_I, [_P, _I, _L, _I, _I, _P, _I, _P, _I, _F,

@@ -658,6 +658,52 @@ def spec_kv_evict(weights, length, planes, *, budget, recent, planes_out=None,
     return kept, new_len
 
 
+def _packed(t, H, T, D, dev, name):
+    """Address and token stride (elements) of a [T, H, D] bf16 tensor whose
+    tokens are contiguous and lie at one stride."""
+    if t.dtype is not torch.bfloat16 or tuple(t.shape) != (T, H, D):
+        _want(t, torch.bfloat16, (T, H, D), name)
+    if t.get_device() != dev:
+        raise ValueError(f"all tensors must be on cuda:{dev}; got one on "
+                         f"{t.device}")
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr(), st if T > 1 else H * D
+
+
+def spec_prompt_attention(q, k, v, seq_start, *, scale=None, lse=False,
+                          out=None, stream=None):
+    """Causal attention of packed prompts (see the C declaration): q [T, Hq, D],
+    k and v [T, Hkv, D] bf16, which may be slices of one [T, heads, D] tensor;
+    seq_start [B+1] int32; D 64 or 128.  lse: True, or a [T, Hq] float32
+    tensor, for the rows' base-2 log normalisers.  out (if given) keeps what it
+    holds for tokens outside every prompt.  Returns (out [T, Hq, D] bf16, lse
+    or None)."""
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    B = seq_start.shape[0] - 1
+    if B < 0:
+        raise ValueError("seq_start must hold B + 1 entries")
+    dev = _index(q)
+    args = (*_packed(q, Hq, T, D, dev, "q"), *_packed(k, Hkv, T, D, dev, "k"),
+            *_packed(v, Hkv, T, D, dev, "v"),
+            _arg(seq_start, torch.int32, (B + 1,), dev, "seq_start"))
+    if out is None:
+        out = _alloc((T, Hq, D), torch.bfloat16, dev, stream)
+    if lse is True:
+        lse = _alloc((T, Hq), torch.float32, dev, stream)
+    elif lse is False:
+        lse = None
+    if scale is None:
+        scale = D ** -0.5
+    _enqueue("spec_prompt_attention", dev, stream, *args, B, T, Hq, Hkv, D,
+             scale, _arg(out, torch.bfloat16, (T, Hq, D), dev, "out"),
+             None if lse is None else _arg(lse, torch.float32, (T, Hq), dev,
+                                           "lse"))
+    return out, lse
+
+
 class TokenLogprobs(NamedTuple):
     """Result of spec_token_logprobs; what was not asked for is None."""
     logprob: torch.Tensor
