@@ -71,6 +71,7 @@ extern "C" {
 #define SPEC_MAX_CHILDREN 64      /* children of one tree node             */
 #define SPEC_MAX_TREE_NODES 1024  /* N (tree) and K (chain)                */
 #define SPEC_MAX_POSITIONS (1 << 30) /* S of the 4-bit attention, the weights and the eviction */
+#define SPEC_MAX_PREFIXES 256     /* prefixes of spec_tree_attention_shared   */
 #define SPEC_EAGLE2_MAX_TOPK 32   /* children per expanded EAGLE-2 node    */
 #define SPEC_EAGLE2_MAX_WIDTH 2048 /* nodes kept per EAGLE-2 layer          */
 #define SPEC_EAGLE2_MAX_CANDIDATES 4096 /* EAGLE-2 candidates per sequence */
@@ -587,6 +588,56 @@ int spec_kv_evict(const float* weights, const int32_t* length, int B, int Hkv,
 int spec_philox_uniforms(uint64_t seed, uint32_t offset, const int32_t* b,
                          const int32_t* idx, const int32_t* slot, int n,
                          float* out, void* stream);
+
+/*
+ * spec_tree_attention for sequences that share long prefixes (several samples
+ * of one prompt): a prefix's keys and values are held and read once for all of
+ * its sequences.  N = 1 with mask bit 0 set is plain single-token decoding.
+ *
+ * Prefix g (g < groups) holds shared_len[g] shared positions and belongs to the
+ * sequences group_start[g] .. group_start[g+1] - 1.  Sequence b of prefix g, with
+ * P = prefix_len[b] positions of its own behind it, gives for drafted node i
+ *
+ *   o[b,i,h] = sum_s softmax_s(scale * q[b,i,h] . k_s) v_s
+ *   over the shared positions, its own positions s < P, and s = P + j for every
+ *   bit j set in mask_bits[b, i]
+ *
+ * Layout (device, bf16 stored as uint16, row-major, contiguous): q and out
+ *   [B, N, Hq, D]; k_prefix and v_prefix [groups, Hkv, Sp, D]; k_cache and
+ *   v_cache [B, Hkv, S, D], the drafted nodes' entries at P .. P + N - 1;
+ *   shared_len [groups], group_start [groups+1] (ascending, clamped to [0, B]),
+ *   prefix_len [B] int32 (clamped to [0, S - N]; shared_len to [0, Sp]);
+ *   mask_bits [B, N] uint64.
+ * lse [B, N, Hq] float32 (out, may be NULL): the rows' base-2 log normalisers.
+ * Sequences outside every group are not written.  A row that sees nothing gives
+ * zeros and lse = -inf (a key whose score is -inf counts as not seen).  What cache
+ * positions behind shared_len or prefix_len + N hold does not matter, and NaN or
+ * infinite keys and values reach only the rows that see them.
+ * Softmax, sums and the join of split work in float32, weights rounded to bf16
+ * for the second product, the output to bf16.  Deterministic.
+ * Workspace: spec_tree_attention_shared_workspace_bytes(...) bytes, 256-byte
+ * aligned, uninitialised (0: invalid sizes, or B = 0, which needs none).
+ * Errors: SPEC_ERR_SHAPE unless 0 <= B <= 65535, 1 <= N <= 64, Hq % Hkv == 0 with
+ * Hq / Hkv <= 128, 1 <= groups <= SPEC_MAX_PREFIXES, 0 <= Sp, N <= S, Sp and S <=
+ * SPEC_MAX_POSITIONS, or when B * Hkv or groups * Hkv reaches 2^31;
+ * SPEC_ERR_UNSUPPORTED unless D is 64 or 128; SPEC_ERR_ARG for scale <= 0 or not
+ * finite, a NULL pointer (B > 0; the prefix arrays may be NULL if Sp is 0), q, out
+ * or caches not 16-byte aligned, int32 arrays or lse not 4-byte, mask_bits not
+ * 8-byte aligned; SPEC_ERR_WORKSPACE; SPEC_ERR_CUDA.  B == 0 does nothing.
+ * Runs on the tensor cores (tcgen05).  Its waits are bounded; rows of a CTA whose
+ * wait gave up (after about a second) are NaN, as there is no status word.
+ */
+size_t spec_tree_attention_shared_workspace_bytes(int B, int N, int Hq, int Hkv,
+                                                  int D, int groups, int Sp,
+                                                  int S);
+int spec_tree_attention_shared(const void* q, const void* k_prefix,
+                               const void* v_prefix, const int32_t* shared_len,
+                               const int32_t* group_start, const void* k_cache,
+                               const void* v_cache, const int32_t* prefix_len,
+                               const uint64_t* mask_bits, int B, int N, int Hq,
+                               int Hkv, int D, int groups, int Sp, int S,
+                               float scale, void* out, float* lse,
+                               void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Causal attention over whole prompts, packed one after another: the pass that

@@ -30,6 +30,7 @@ SPEC_MAX_VOCAB = 1 << 24
 SPEC_MAX_TOP_K = 128
 SPEC_MAX_CHILDREN = 64
 SPEC_MAX_TREE_NODES = 1024
+SPEC_MAX_PREFIXES = 256
 SPEC_EAGLE2_MAX_TOPK = 32
 SPEC_MAX_POSITIONS = 1 << 30
 SPEC_NOALLOC_MAX_ROWS = 8192
@@ -132,6 +133,9 @@ _SIGNATURES = {
     "spec_kv_evict": (_I, [_P, _P, _I, _I, _I, _I, _I, _I,
                            ctypes.POINTER(_P), ctypes.POINTER(_P),
                            ctypes.POINTER(_I), _I, _P, _P, _P, _P]),
+    "spec_tree_attention_shared_workspace_bytes": (_SZ, [_I] * 8),
+    "spec_tree_attention_shared": (_I, [_P] * 9 + [_I] * 8 +
+                                   [_F, _P, _P, _P, _SZ, _P]),
     "spec_prompt_attention": (_I, [_P, _L, _P, _L, _P, _L, _P, _I, _I, _I, _I,
                                    _I, _F, _P, _P, _P]),
     "spec_token_logprobs": (_I, [_P, _I, _L, _I, _I, _P, _I, _P, _I, _I, _F,

@@ -658,6 +658,59 @@ def spec_kv_evict(weights, length, planes, *, budget, recent, planes_out=None,
     return kept, new_len
 
 
+@functools.lru_cache(maxsize=256)
+def _shared_workspace_bytes(*sizes):
+    return int(_lib.call("spec_tree_attention_shared_workspace_bytes", *sizes))
+
+
+def spec_tree_attention_shared(q, k_prefix, v_prefix, shared_len, group_start,
+                               k_cache, v_cache, prefix_len, mask_bits, *,
+                               scale=None, lse=False, out=None, ws=None,
+                               stream=None):
+    """spec_tree_attention of sequences that share prefixes (see the C
+    declaration): q [B, N, Hq, D]; k_prefix and v_prefix [groups, Hkv, Sp, D]
+    with shared_len [groups] int32 and group_start [groups+1] int32 (prefix g
+    belongs to sequences group_start[g] .. group_start[g+1]-1); k_cache and
+    v_cache [B, Hkv, S, D] hold what follows it, prefix_len [B] int32 and the
+    drafted nodes; mask_bits [B, N] int64; all bf16, D 64 or 128.  lse: True,
+    or a [B, N, Hq] float32 tensor, for the rows' base-2 log normalisers.
+    Returns (out [B, N, Hq, D] bf16, lse or None)."""
+    B, N, Hq, D = shape = q.shape
+    _, Hkv, S, _ = k_cache.shape
+    groups, _, Sp, _ = k_prefix.shape
+    dev = _index(q)
+    bf, i32 = torch.bfloat16, torch.int32
+    pre, own = (groups, Hkv, Sp, D), (B, Hkv, S, D)
+    args = (_arg(q, bf, shape, dev, "q"),
+            _arg(k_prefix, bf, pre, dev, "k_prefix"),
+            _arg(v_prefix, bf, pre, dev, "v_prefix"),
+            _arg(shared_len, i32, (groups,), dev, "shared_len"),
+            _arg(group_start, i32, (groups + 1,), dev, "group_start"),
+            _arg(k_cache, bf, own, dev, "k_cache"),
+            _arg(v_cache, bf, own, dev, "v_cache"),
+            _arg(prefix_len, i32, (B,), dev, "prefix_len"),
+            _arg(mask_bits, torch.int64, (B, N), dev, "mask_bits"))
+    if out is None:
+        out = _alloc(shape, bf, dev, stream)
+    if lse is True:
+        lse = _alloc((B, N, Hq), torch.float32, dev, stream)
+    elif lse is False:
+        lse = None
+    if ws is None:
+        nbytes = _shared_workspace_bytes(B, N, Hq, Hkv, D, groups, Sp, S)
+        ws = _alloc(nbytes, torch.uint8, dev, stream)
+    else:
+        nbytes = ws.numel()
+    if scale is None:
+        scale = D ** -0.5
+    _enqueue("spec_tree_attention_shared", dev, stream, *args, B, N, Hq, Hkv,
+             D, groups, Sp, S, scale, _arg(out, bf, shape, dev, "out"),
+             None if lse is None else _arg(lse, torch.float32, (B, N, Hq), dev,
+                                           "lse"),
+             _arg(ws, torch.uint8, (nbytes,), dev, "ws"), nbytes)
+    return out, lse
+
+
 def _packed(t, H, T, D, dev, name):
     """Address and token stride (elements) of a [T, H, D] bf16 tensor whose
     tokens are contiguous and lie at one stride."""

@@ -54,7 +54,7 @@ struct PromptWalk {
     const int n = start_of(p, b + 1) - start_of(p, b);
     return n <= 0 ? 0 : (n - 1) / (2 * p.tpt) + 1;
   }
-  __device__ __forceinline__ static void setup(const Params& p, Shared& sh) {
+  __device__ __forceinline__ static void setup(const Params& p, Shared& sh, void*) {
     if (threadIdx.x == 0) sh.most = 0;
     __syncthreads();
     if (p.B <= kLevelMax)

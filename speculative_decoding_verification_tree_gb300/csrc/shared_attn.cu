@@ -1,0 +1,563 @@
+// spec_tree_attention_shared: tree / single-token attention of sequences that share
+// a long prefix and have keys of their own behind it (tile_attn.cuh has the kernel).
+//
+// For sequence b of prefix g, with n = shared_len[g] shared keys, P = prefix_len[b]
+// own keys and drafted node i:
+//
+//   o[b,i,h] = sum_s softmax_s(scale q[b,i,h] . k_s) v_s over the n shared keys, the
+//              P own ones and the own keys P + j of every bit j of mask_bits[b, i]
+//
+// The query rows of all sequences of a prefix are packed into one unit after another
+// of up to 256 rows, so a prefix is read once per unit instead of once per sequence.
+// A unit's steps are the prefix's 128-key blocks, which all of its rows see, and then
+// the own blocks of its sequences one by one, which the rows of the other sequences
+// do not see: their P is 0 there.  (A sequence alone would take the same products: a
+// tile has 128 rows whether or not they are used; what a step costs is its 64 KB of
+// keys and values.)
+//
+// Work is split by steps, not units: all steps of all units form a line that is cut
+// into equal pieces, one per CTA, since a few units of a long prefix are the usual
+// case.  A unit that a cut leaves in several pieces is joined by a second kernel from
+// float32 outputs and (reference, sum) pairs, both in a fixed order.  A cut unit of at
+// most one tile of rows puts them in both tiles, which take its steps in turn: one
+// tile's softmax then runs beside the other's products.
+#include "tile_attn.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kMaxPrefixes = SPEC_MAX_PREFIXES;
+constexpr int kMinSteps = 4;     // steps of a piece, at least
+
+struct SharedHead {  // the unit that begins in a piece and ends in a later one
+  int slot;          // -1: there is none
+  int tok0, ntok, h, both, last;
+  int pad[2];
+};
+struct SharedPart {  // partial results of the pieces: [piece][slot][tile]
+  SharedHead* head;  // [piece]
+  float2* ml;        // [..][128]
+  float4* o;         // [..][D / 4][128]
+};
+
+struct SharedWalk {
+  struct Params {
+    CUtensorMap q, ks, vs, ko, vo;
+    const int32_t *shared_len, *group_start, *prefix_len;
+    const uint64_t* mask_bits;
+    const uint16_t *vs_ptr, *vo_ptr;
+    uint16_t* out;
+    float* lse;
+    SharedPart part;
+    int B, N, Hq, Hkv, G, tpt, groups, Sp, S;
+    int spu, chunks;  // sequences per unit; units per sequence (one of them is 1)
+    float scale_log2;
+  };
+  struct Shared {
+    int tiles[kMaxPrefixes + 1];  // units (per key/value head) before each prefix
+    int64_t len, p0, p1;          // steps per piece; this CTA's piece of the line
+    int64_t cum;                  // steps (of one head) before the unit that holds p0
+    int tile;                     // that unit
+  };
+
+  const Params& p;
+  const Shared& sh;
+  // cursor
+  int64_t at, tb;    // line position; position of the unit row's first step
+  int tile, turn;
+  // the unit row (the same for all heads) and the unit
+  int g, b0, nb, tok0, ntok, slen, nsb, nblk;
+  int h, j0, j1;
+  bool whole, both;  // not cut; cut and in both tiles
+  uint32_t have, act;
+  // the step
+  int j, key0, keys;
+  bool full, own;
+  int b, jb, nob, P;  // the sequence whose own block it is
+
+  __device__ __forceinline__ static int first_of(const Params& p, int g) {
+    return min(max(p.group_start[g], 0), p.B);
+  }
+  __device__ __forceinline__ static int shared_of(const Params& p, int g) {
+    return min(max(p.shared_len[g], 0), p.Sp);
+  }
+  __device__ __forceinline__ static int prefix_of(const Params& p, int b) {
+    return min(max(p.prefix_len[b], 0), p.S - p.N);
+  }
+  __device__ __forceinline__ static int own_blocks(const Params& p, int b) {
+    return (prefix_of(p, b) + p.N + kKeys - 1) / kKeys;
+  }
+  // prefix and sequences of unit row i
+  __device__ __forceinline__ static void rows_of(const Params& p, const Shared& sh, int i, int& g,
+                                                 int& b0, int& nb, int& part) {
+    int lo = 0, hi = p.groups - 1;  // the last prefix with tiles[g] <= i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (sh.tiles[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    g = lo;
+    const int k = i - sh.tiles[g], first = first_of(p, g);
+    b0 = first + (p.chunks > 1 ? k / p.chunks : k * p.spu);
+    part = p.chunks > 1 ? k % p.chunks : 0;
+    nb = min(p.spu, first_of(p, g + 1) - b0);
+  }
+  __device__ static void setup(const Params& p, Shared& sh, void* scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t* before = reinterpret_cast<int64_t*>(scratch);  // [threads]
+    int64_t* tmp = before + kTaThreads;
+    for (int g = tid; g < p.groups; g += kTaThreads) {
+      const int n = max(0, first_of(p, g + 1) - first_of(p, g));
+      sh.tiles[g + 1] = p.chunks > 1 ? n * p.chunks : (n + p.spu - 1) / p.spu;
+    }
+    launch_dependents();
+    if (tid == 0) {
+      sh.tiles[0] = 0;
+      p.part.head[blockIdx.x].slot = -1;
+    }
+    __syncthreads();
+    if (warp == 0) {  // running sum
+      int carry = 0;
+      for (int i0 = 1; i0 <= p.groups; i0 += 32) {
+        int v = i0 + lane <= p.groups ? sh.tiles[i0 + lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += u;
+        }
+        if (i0 + lane <= p.groups) sh.tiles[i0 + lane] = carry + v;
+        carry += __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
+    const int total = sh.tiles[p.groups];
+    const int per = (total + kTaThreads - 1) / kTaThreads;
+    auto steps = [&](int i) {
+      int g, b0, nb, part;
+      rows_of(p, sh, i, g, b0, nb, part);
+      int64_t n = (shared_of(p, g) + kKeys - 1) / kKeys;
+      for (int b = b0; b < b0 + nb; ++b) n += own_blocks(p, b);
+      return n;
+    };
+    const int first = min(total, tid * per), last = min(total, first + per);
+    int64_t v = 0;
+    for (int i = first; i < last; ++i) v += steps(i);
+    int64_t s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) tmp[warp] = s;
+    __syncthreads();
+    int64_t base = 0, all = 0;
+    for (int w = 0; w < kTaThreads / 32; ++w) {
+      if (w < warp) base += tmp[w];
+      all += tmp[w];
+    }
+    s += base;
+    const int64_t line = all * p.Hkv;
+    int64_t len = (line + gridDim.x - 1) / gridDim.x;
+    if (len < kMinSteps) len = kMinSteps;
+    const int64_t p0 = min(line, len * blockIdx.x), p1 = min(line, p0 + len);
+    if (tid == 0) {
+      sh.len = len;
+      sh.p0 = p0;
+      sh.p1 = p1;
+      sh.tile = 0;
+      sh.cum = 0;
+    }
+    __syncthreads();
+    // the thread whose unit rows hold the piece's first step finds it
+    const int64_t want = p0 / p.Hkv;
+    if (p0 < line && s - v <= want && want < s) {
+      int64_t x = s - v;
+      int i = first;
+      for (;; ++i) {
+        const int64_t n = steps(i);
+        if (want < x + n) break;
+        x += n;
+      }
+      sh.tile = i;
+      sh.cum = x;
+    }
+    __syncthreads();
+  }
+  __device__ __forceinline__ SharedWalk(const Params& p_, const Shared& sh_)
+      : p(p_), sh(sh_), at(sh_.p0), tb(sh_.cum * p_.Hkv), tile(sh_.tile), turn(0) {
+    if (at < sh.p1) load_rows();
+  }
+
+  __device__ __forceinline__ void load_rows() {
+    const int lane = threadIdx.x & 31;
+    int part;
+    rows_of(p, sh, tile, g, b0, nb, part);
+    tok0 = b0 * p.N + part * 2 * p.tpt;
+    ntok = p.chunks > 1 ? min(2 * p.tpt, p.N - part * 2 * p.tpt) : nb * p.N;
+    slen = shared_of(p, g);
+    nsb = (slen + kKeys - 1) / kKeys;
+    int n = 0;
+    for (int i = lane; i < nb; i += 32) n += own_blocks(p, b0 + i);
+    nblk = nsb + __reduce_add_sync(0xffffffffu, n);
+  }
+  __device__ __forceinline__ bool next_unit() {
+    if (at >= sh.p1) return false;
+    if (at >= tb + (int64_t)p.Hkv * nblk) {
+      tb += (int64_t)p.Hkv * nblk;
+      ++tile;
+      load_rows();
+    }
+    const int64_t off = at - tb;
+    h = (int)(off / nblk);
+    j0 = (int)(off - (int64_t)h * nblk);
+    j1 = (int)min((int64_t)nblk, j0 + (sh.p1 - at));
+    at += j1 - j0;
+    whole = j0 == 0 && j1 == nblk;
+    both = !whole && ntok <= p.tpt;
+    have = both || ntok > p.tpt ? 3u : 1u;
+    ++turn;
+    if (threadIdx.x == 0 && j0 == 0 && !whole)
+      p.part.head[blockIdx.x] = SharedHead{slot(), tok0, ntok, h, both,
+                                           (int)((tb + (int64_t)(h + 1) * nblk - 1) / sh.len)};
+    restart();
+    return true;
+  }
+  // a cut unit is the first of its piece (slot 0) or the last (slot 1)
+  __device__ __forceinline__ int slot() const { return turn == 1 ? 0 : 1; }
+  __device__ __forceinline__ void restart() {
+    j = j0 - 1;
+    b = -1;
+  }
+  // the sequence that holds own block k of the unit
+  __device__ __forceinline__ void seek(int k) {
+    const int lane = threadIdx.x & 31;
+    for (int i0 = 0;; i0 += 32) {
+      const int mine = i0 + lane < nb ? own_blocks(p, b0 + i0 + lane) : 0;
+      int s = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, k < s);
+      if (m || i0 + 32 >= nb) {
+        const int src = m ? __ffs(m) - 1 : 0;
+        b = b0 + i0 + src;
+        jb = k - __shfl_sync(0xffffffffu, s - mine, src);
+        return;
+      }
+      k -= __shfl_sync(0xffffffffu, s, 31);
+    }
+  }
+  __device__ __forceinline__ bool next_step() {
+    if (++j >= j1) return false;
+    own = j >= nsb;
+    if (!own) {
+      key0 = j * kKeys;
+      keys = min(kKeys, slen - key0);
+      full = keys == kKeys;
+      act = both ? 1u << ((j - j0) & 1) : have;
+      return true;
+    }
+    if (b < 0) {
+      seek(j - nsb);
+    } else if (++jb == nob) {
+      jb = 0;
+      ++b;
+    }
+    P = prefix_of(p, b);
+    nob = (P + p.N + kKeys - 1) / kKeys;
+    key0 = jb * kKeys;
+    keys = min(kKeys, P + p.N - key0);
+    full = nb == 1 && key0 + kKeys <= P;
+    if (both) {
+      act = 1u << ((j - j0) & 1);
+    } else {
+      const int lo = b * p.N - tok0;  // the sequence's tokens in the unit
+      act = (lo < p.tpt ? 1u : 0u) | (lo + p.N > p.tpt ? 2u : 0u);
+      act &= have;
+    }
+    return true;
+  }
+  __device__ __forceinline__ uint32_t q_bytes() const { return (uint32_t)(p.tpt * p.G * 128); }
+  __device__ __forceinline__ void load_q(int t, uint32_t dst, int x, uint64_t* bar) const {
+    tma3d(dst, &p.q, x, h * p.G, tok0 + (both ? 0 : t * p.tpt), bar);
+  }
+  __device__ __forceinline__ void load_k(uint32_t dst, int x, uint64_t* bar) const {
+    tma3d(dst, own ? &p.ko : &p.ks, x, key0, (own ? b : g) * p.Hkv + h, bar);
+  }
+  __device__ __forceinline__ void load_v(uint32_t dst, int x, uint64_t* bar) const {
+    tma3d(dst, own ? &p.vo : &p.vs, x, key0, (own ? b : g) * p.Hkv + h, bar);
+  }
+
+  struct Row {
+    int r, tok, head;  // row of the tile, token in the tile, head in the group
+    int token, seq;
+    bool valid;
+    uint64_t mb;       // drafted keys it sees
+    float mul;
+    int64_t dst;       // row of out, or of the partial results
+    __device__ __forceinline__ Row(const Params& p, int r_)
+        : r(r_), tok(r_ / p.G), head(r_ % p.G) {}
+  };
+  __device__ __forceinline__ void set_row(Row& row, int t) const {
+    const int i = (both ? 0 : t * p.tpt) + row.tok;
+    row.valid = row.tok < p.tpt && i < ntok;
+    row.token = row.valid ? tok0 + i : 0;
+    row.seq = row.token / p.N;
+    row.mb = row.valid ? p.mask_bits[row.token] & (p.N >= 64 ? ~0ull : (1ull << p.N) - 1ull) : 0ull;
+  }
+  __device__ __forceinline__ bool warp_blind(const Row& row) const {
+    if (!own || full) return false;
+    return !__any_sync(0xffffffffu, row.valid && row.seq == b);
+  }
+  // visibility of the step's keys 32 i .. 32 i + 31
+  __device__ __forceinline__ uint32_t word(const Row& row, int i) const {
+    const int k0 = key0 + 32 * i;
+    const int end = (own ? P : slen) - k0;
+    const uint32_t pre = end >= 32 ? ~0u : (end <= 0 ? 0u : (1u << end) - 1u);
+    if (!own) return pre;
+    if (!row.valid || row.seq != b) return 0u;
+    const int off = k0 - P;
+    const uint32_t dr = off >= 0 ? (off < 64 ? (uint32_t)(row.mb >> off) : 0u)
+                                 : (off > -32 ? (uint32_t)(row.mb << -off) : 0u);
+    return pre | dr;
+  }
+  __device__ __forceinline__ void hide(const Row& row, float (&s)[kKeys]) const {
+#pragma unroll
+    for (int i = 0; i < kKeys / 32; ++i) {
+      const uint32_t w = word(row, i);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) s[32 * i + e] = (w >> e) & 1u ? s[32 * i + e] : neg_inf();
+    }
+  }
+  __device__ __forceinline__ bool sees(const Row& row, int i) const {
+    return row.valid && ((word(row, i >> 5) >> (i & 31)) & 1u);
+  }
+};
+
+template <int D>
+struct SharedWalkD : SharedWalk {
+  using SharedWalk::SharedWalk;
+  __device__ __forceinline__ const uint16_t* value(int i) const {
+    return own ? p.vo_ptr + (((int64_t)b * p.Hkv + h) * p.S + key0 + i) * D
+               : p.vs_ptr + (((int64_t)g * p.Hkv + h) * p.Sp + key0 + i) * D;
+  }
+  __device__ __forceinline__ void begin_finish(Row& row, int t, float mref, float l) const {
+    if (!whole) {
+      const int64_t s = ((int64_t)blockIdx.x * 2 + slot()) * 2 + t;
+      p.part.ml[s * kRows + row.r] = make_float2(mref, l);
+      row.dst = s * (D / 4) * kRows + row.r;
+      return;
+    }
+    row.mul = l == 0.f ? 0.f : 1.f / l;
+    row.dst = (int64_t)row.token * p.Hq + h * p.G + row.head;
+    if (row.valid && p.lse) p.lse[row.dst] = mref + log2f(l);
+  }
+  __device__ __forceinline__ void finish(const Row& row, int, int c, const float (&o)[32]) const {
+    if (!whole) {  // 16 bytes of 32 rows side by side
+#pragma unroll
+      for (int v = 0; v < 8; ++v)
+        p.part.o[row.dst + (8 * c + v) * kRows] =
+            make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+      return;
+    }
+    if (!row.valid) return;
+    uint4* dst = reinterpret_cast<uint4*>(p.out + row.dst * D) + 4 * c;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int i = 8 * v;
+      dst[v] = make_uint4(pack_bf16(o[i] * row.mul, o[i + 1] * row.mul),
+                          pack_bf16(o[i + 2] * row.mul, o[i + 3] * row.mul),
+                          pack_bf16(o[i + 4] * row.mul, o[i + 5] * row.mul),
+                          pack_bf16(o[i + 6] * row.mul, o[i + 7] * row.mul));
+    }
+  }
+};
+
+// Joins the pieces of cut units: CTA (piece in which the unit begins, 8 head dims),
+// thread (tile, row).
+template <int D>
+__global__ void __launch_bounds__(2 * kRows)
+    shared_join(SharedPart part, int tpt, int G, int Hq, uint16_t* __restrict__ out,
+                float* __restrict__ lse) {
+  __shared__ float other[10][kRows];
+  grid_dependency_wait();
+  const SharedHead u = part.head[blockIdx.x];
+  if (u.slot < 0) return;
+  const int t = threadIdx.x / kRows, r = threadIdx.x % kRows;
+  auto place = [&](int c) { return ((int64_t)c * 2 + (c == (int)blockIdx.x ? u.slot : 0)) * 2 + t; };
+  float M = neg_inf();
+  for (int c = blockIdx.x; c <= u.last; ++c) M = fmaxf(M, part.ml[place(c) * kRows + r].x);
+  float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const float ref = M == neg_inf() ? 0.f : M;
+#pragma unroll 4
+  for (int c = blockIdx.x; c <= u.last; ++c) {
+    const int64_t s = place(c);
+    const float2 ml = part.ml[s * kRows + r];
+    const float4* src = part.o + (s * (D / 4) + 2 * blockIdx.y) * kRows + r;
+    const float4 x = src[0], y = src[kRows];
+    // (a piece that saw something keeps a positive weight: infinite values stay)
+    const float w = ml.x == neg_inf() ? (ml.y == 0.f ? 0.f : 1.f) : fmaxf(ex2(ml.x - ref), FLT_MIN);
+    l = fmaf(ml.y, w, l);
+    o[0] = fmaf(x.x, w, o[0]); o[1] = fmaf(x.y, w, o[1]);
+    o[2] = fmaf(x.z, w, o[2]); o[3] = fmaf(x.w, w, o[3]);
+    o[4] = fmaf(y.x, w, o[4]); o[5] = fmaf(y.y, w, o[5]);
+    o[6] = fmaf(y.z, w, o[6]); o[7] = fmaf(y.w, w, o[7]);
+  }
+  if (u.both) {  // the two tiles hold the same rows
+    if (t == 1) {
+      other[0][r] = M;
+      other[1][r] = l;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) other[2 + i][r] = o[i];
+    }
+    __syncthreads();
+    if (t == 1) return;
+    const float m1 = other[0][r], m = fmaxf(M, m1);
+    const float rf = m == neg_inf() ? 0.f : m;
+    const float w0 = M == neg_inf() ? (l == 0.f ? 0.f : 1.f) : fmaxf(ex2(M - rf), FLT_MIN);
+    const float w1 = m1 == neg_inf() ? (other[1][r] == 0.f ? 0.f : 1.f)
+                                     : fmaxf(ex2(m1 - rf), FLT_MIN);
+    l = l * w0 + other[1][r] * w1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = o[i] * w0 + other[2 + i][r] * w1;
+    M = m;
+  }
+  const int tok = r / G, i = (u.both ? 0 : t * tpt) + tok;
+  if (tok >= tpt || i >= u.ntok) return;
+  const int64_t row = (int64_t)(u.tok0 + i) * Hq + u.h * G + r % G;
+  const float mul = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint4*>(out + row * D + 8 * blockIdx.y) =
+      make_uint4(pack_bf16(o[0] * mul, o[1] * mul), pack_bf16(o[2] * mul, o[3] * mul),
+                 pack_bf16(o[4] * mul, o[5] * mul), pack_bf16(o[6] * mul, o[7] * mul));
+  if (lse && blockIdx.y == 0) lse[row] = M + log2f(l);
+}
+
+// Sizes of a call: how rows are packed, and how many pieces the line can have.
+struct SharedPlan {
+  int G, tpt, spu, chunks, pieces;
+  size_t off_ml, off_o, bytes;
+};
+bool shared_sizes_ok(int B, int N, int Hq, int Hkv, int groups, int Sp, int S) {
+  return B >= 0 && B <= 65535 && N >= 1 && N <= 64 && Hq >= 1 && Hkv >= 1 && Hq % Hkv == 0 &&
+         Hq / Hkv <= kRows && groups >= 1 && groups <= kMaxPrefixes && Sp >= 0 &&
+         Sp <= SPEC_MAX_POSITIONS && S >= N && S <= SPEC_MAX_POSITIONS &&
+         (int64_t)B * Hkv < (int64_t)1 << 31 && (int64_t)groups * Hkv < (int64_t)1 << 31;
+}
+SharedPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int groups, int Sp, int S) {
+  SharedPlan s;
+  s.G = Hq / Hkv;
+  s.tpt = kRows / s.G;
+  s.spu = N <= 2 * s.tpt ? 2 * s.tpt / N : 1;
+  s.chunks = (N + 2 * s.tpt - 1) / (2 * s.tpt);
+  int64_t tiles = s.chunks > 1 ? (int64_t)B * s.chunks : (int64_t)B / s.spu + groups;
+  if (tiles > (int64_t)B * s.chunks) tiles = (int64_t)B * s.chunks;
+  const int64_t steps = Hkv * (tiles * ((Sp + kKeys - 1) / kKeys) +
+                               (int64_t)B * s.chunks * ((S + kKeys - 1) / kKeys));
+  const int64_t most = (steps + kMinSteps - 1) / kMinSteps;
+  s.pieces = (int)(most < 1 ? 1 : (most < kTaCtas ? most : kTaCtas));
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  s.off_ml = up((size_t)s.pieces * sizeof(SharedHead));
+  s.off_o = s.off_ml + up((size_t)s.pieces * 4 * kRows * sizeof(float2));
+  s.bytes = s.off_o + (size_t)s.pieces * 4 * kRows * D * sizeof(float);
+  return s;
+}
+
+template <int D>
+int launch(const SharedWalk::Params& prm, const SharedPlan& plan, cudaStream_t st) {
+  constexpr int kKs = D == 128 ? 2 : 5, kVs = D == 128 ? 3 : 5;
+  using Geo = TileGeo<D, kKs, kVs>;
+  constexpr size_t smem =
+      (size_t)Geo::kOffCtl + sizeof(TileCtl<kKs, kVs>) + sizeof(SharedWalk::Shared) + 1024;
+  static_assert(smem <= 232448, "shared memory of a block");
+  auto kernel = tile_attn<D, kKs, kVs, SharedWalkD<D>>;
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem((const void*)kernel, (int)smem, done) != cudaSuccess) return SPEC_ERR_CUDA;
+  kernel<<<plan.pieces, kTaThreads, smem, st>>>(prm);
+  if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
+  if (plan.pieces == 1) return SPEC_OK;  // nothing is cut
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)plan.pieces, D / 8);
+  cfg.blockDim = dim3(2 * kRows);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_join<D>, prm.part, prm.tpt, prm.G, prm.Hq, prm.out,
+                            prm.lse) == cudaSuccess
+             ? SPEC_OK
+             : SPEC_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t spec_tree_attention_shared_workspace_bytes(int B, int N, int Hq, int Hkv, int D,
+                                                             int groups, int Sp, int S) {
+  if (!shared_sizes_ok(B, N, Hq, Hkv, groups, Sp, S) || (D != 64 && D != 128) || B == 0) return 0;
+  return shared_plan(B, N, Hq, Hkv, D, groups, Sp, S).bytes;
+}
+
+extern "C" int spec_tree_attention_shared(
+    const void* q, const void* k_prefix, const void* v_prefix, const int32_t* shared_len,
+    const int32_t* group_start, const void* k_cache, const void* v_cache, const int32_t* prefix_len,
+    const uint64_t* mask_bits, int B, int N, int Hq, int Hkv, int D, int groups, int Sp, int S,
+    float scale, void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  if (!shared_sizes_ok(B, N, Hq, Hkv, groups, Sp, S)) return SPEC_ERR_SHAPE;
+  if (D != 64 && D != 128) return SPEC_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || !(scale < 3.4e38f)) return SPEC_ERR_ARG;
+  if (B == 0) return SPEC_OK;
+  if (!q || (Sp > 0 && (!k_prefix || !v_prefix)) || !shared_len || !group_start || !k_cache ||
+      !v_cache || !prefix_len || !mask_bits || !out)
+    return SPEC_ERR_ARG;
+  if (((uintptr_t)q | (uintptr_t)k_prefix | (uintptr_t)v_prefix | (uintptr_t)k_cache |
+       (uintptr_t)v_cache | (uintptr_t)out) % 16 != 0 ||
+      ((uintptr_t)shared_len | (uintptr_t)group_start | (uintptr_t)prefix_len | (uintptr_t)lse) %
+              4 != 0 ||
+      (uintptr_t)mask_bits % 8 != 0)
+    return SPEC_ERR_ARG;
+  const SharedPlan plan = shared_plan(B, N, Hq, Hkv, D, groups, Sp, S);
+  if (!workspace || (uintptr_t)workspace % 256 != 0 || ws_bytes < plan.bytes)
+    return SPEC_ERR_WORKSPACE;
+  SharedWalk::Params prm;
+  prm.G = plan.G;
+  prm.tpt = plan.tpt;
+  prm.spu = plan.spu;
+  prm.chunks = plan.chunks;
+  const int64_t row = (int64_t)D * 2;
+  // (without shared keys their maps stand for the caches and are not used)
+  const void *ks = Sp > 0 ? k_prefix : k_cache, *vs = Sp > 0 ? v_prefix : v_cache;
+  const int64_t sp = Sp > 0 ? Sp : S, np = Sp > 0 ? (int64_t)groups * Hkv : (int64_t)B * Hkv;
+  if (!ta_map(&prm.q, q, D, Hq, (int64_t)B * N, row, Hq * row, prm.G, prm.tpt) ||
+      !ta_map(&prm.ks, ks, D, sp, np, row, sp * row, kKeys, 1) ||
+      !ta_map(&prm.vs, vs, D, sp, np, row, sp * row, kKeys, 1) ||
+      !ta_map(&prm.ko, k_cache, D, S, (int64_t)B * Hkv, row, S * row, kKeys, 1) ||
+      !ta_map(&prm.vo, v_cache, D, S, (int64_t)B * Hkv, row, S * row, kKeys, 1))
+    return SPEC_ERR_CUDA;
+  prm.shared_len = shared_len;
+  prm.group_start = group_start;
+  prm.prefix_len = prefix_len;
+  prm.mask_bits = mask_bits;
+  prm.vs_ptr = (const uint16_t*)vs;
+  prm.vo_ptr = (const uint16_t*)v_cache;
+  prm.out = (uint16_t*)out;
+  prm.lse = lse;
+  char* ws = (char*)workspace;
+  prm.part.head = (SharedHead*)ws;
+  prm.part.ml = (float2*)(ws + plan.off_ml);
+  prm.part.o = (float4*)(ws + plan.off_o);
+  prm.B = B;
+  prm.N = N;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.groups = groups;
+  prm.Sp = Sp;
+  prm.S = S;
+  prm.scale_log2 = fminf(scale * kLog2e, FLT_MAX);
+  cudaStream_t st = (cudaStream_t)stream;
+  return D == 128 ? launch<128>(prm, plan, st) : launch<64>(prm, plan, st);
+}

@@ -110,7 +110,8 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
 }
 
 // The Walk of a caller W offers, to whole warps:
-//   bool next_unit(), bool next_step();
+//   static setup(prm, shared, scratch)   once, before the roles part
+//   bool next_unit(), bool next_step(), restart() (the unit's steps from the start)
 //   have   tiles of the unit (bits);  act   tiles that take part in the step
 //   full   no row of the unit lacks a key of the step
 //   load_q / load_k / load_v  the producer's copies
@@ -157,7 +158,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  W::setup(prm, ws);  // every thread; ends with a barrier
+  W::setup(prm, ws, bp);  // every thread; may use the tiles' space; ends with a barrier
+  fence_async_smem();
   fence_before();
   __syncthreads();
   fence_after();
