@@ -175,10 +175,10 @@ struct PromptWalk {
     row.valid = row.tok < p.tpt && row.pos < L;
   }
   __device__ __forceinline__ bool warp_blind(const Row&) const { return false; }
-  __device__ __forceinline__ void hide(const Row& row, float (&s)[kKeys]) const {
-    const int lim = row.pos - key0;
+  __device__ __forceinline__ void hide(const Row& row, int half, float (&s)[kHalfKeys]) const {
+    const int lim = row.pos - key0 - kHalfKeys * half;
 #pragma unroll
-    for (int i = 0; i < kKeys; ++i) s[i] = i <= lim ? s[i] : neg_inf();
+    for (int i = 0; i < kHalfKeys; ++i) s[i] = i <= lim ? s[i] : neg_inf();
   }
   __device__ __forceinline__ bool sees(const Row& row, int i) const {
     return row.valid && key0 + i <= row.pos;
@@ -216,7 +216,7 @@ int launch(const PromptWalk::Params& prm, cudaStream_t st) {
   constexpr int kKs = D == 128 ? 2 : 5, kVs = D == 128 ? 3 : 5;
   using Geo = TileGeo<D, kKs, kVs>;
   constexpr size_t smem =
-      (size_t)Geo::kOffCtl + sizeof(TileCtl<kKs, kVs>) + sizeof(PromptWalk::Shared) + 1024;
+      (size_t)Geo::kOffCtl + sizeof(TileCtl<kKs, kVs>) + sizeof(PromptWalk::Shared);
   static_assert(smem <= 232448, "shared memory of a block");
   auto kernel = tile_attn<D, kKs, kVs, PromptWalkD<D>>;
   static std::atomic<uint64_t> done{0};

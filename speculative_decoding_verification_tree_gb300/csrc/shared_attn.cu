@@ -54,7 +54,8 @@ struct SharedWalk {
     float scale_log2;
   };
   struct Shared {
-    int tiles[kMaxPrefixes + 1];  // units (per key/value head) before each prefix
+    // unit rows before each prefix, in parts of `chunks` (at most B: 16 bits)
+    uint16_t tiles[kMaxPrefixes + 1];
     int64_t len, p0, p1;          // steps per piece; this CTA's piece of the line
     int64_t cum;                  // steps (of one head) before the unit that holds p0
     int tile;                     // that unit
@@ -90,15 +91,15 @@ struct SharedWalk {
   // prefix and sequences of unit row i
   __device__ __forceinline__ static void rows_of(const Params& p, const Shared& sh, int i, int& g,
                                                  int& b0, int& nb, int& part) {
-    int lo = 0, hi = p.groups - 1;  // the last prefix with tiles[g] <= i
+    const int k = i / p.chunks;
+    part = i - k * p.chunks;
+    int lo = 0, hi = p.groups - 1;  // the last prefix with tiles[g] <= k
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (sh.tiles[mid] <= i) lo = mid; else hi = mid - 1;
+      if (sh.tiles[mid] <= k) lo = mid; else hi = mid - 1;
     }
     g = lo;
-    const int k = i - sh.tiles[g], first = first_of(p, g);
-    b0 = first + (p.chunks > 1 ? k / p.chunks : k * p.spu);
-    part = p.chunks > 1 ? k % p.chunks : 0;
+    b0 = first_of(p, g) + (k - sh.tiles[g]) * p.spu;
     nb = min(p.spu, first_of(p, g + 1) - b0);
   }
   __device__ static void setup(const Params& p, Shared& sh, void* scratch) {
@@ -107,7 +108,7 @@ struct SharedWalk {
     int64_t* tmp = before + kTaThreads;
     for (int g = tid; g < p.groups; g += kTaThreads) {
       const int n = max(0, first_of(p, g + 1) - first_of(p, g));
-      sh.tiles[g + 1] = p.chunks > 1 ? n * p.chunks : (n + p.spu - 1) / p.spu;
+      sh.tiles[g + 1] = (uint16_t)((n + p.spu - 1) / p.spu);
     }
     launch_dependents();
     if (tid == 0) {
@@ -124,12 +125,12 @@ struct SharedWalk {
           const int u = __shfl_up_sync(0xffffffffu, v, o);
           if (lane >= o) v += u;
         }
-        if (i0 + lane <= p.groups) sh.tiles[i0 + lane] = carry + v;
+        if (i0 + lane <= p.groups) sh.tiles[i0 + lane] = (uint16_t)min(carry + v, 65535);
         carry += __shfl_sync(0xffffffffu, v, 31);
       }
     }
     __syncthreads();
-    const int total = sh.tiles[p.groups];
+    const int total = sh.tiles[p.groups] * p.chunks;
     const int per = (total + kTaThreads - 1) / kTaThreads;
     auto steps = [&](int i) {
       int g, b0, nb, part;
@@ -322,10 +323,10 @@ struct SharedWalk {
                                  : (off > -32 ? (uint32_t)(row.mb << -off) : 0u);
     return pre | dr;
   }
-  __device__ __forceinline__ void hide(const Row& row, float (&s)[kKeys]) const {
+  __device__ __forceinline__ void hide(const Row& row, int half, float (&s)[kHalfKeys]) const {
 #pragma unroll
-    for (int i = 0; i < kKeys / 32; ++i) {
-      const uint32_t w = word(row, i);
+    for (int i = 0; i < kHalfKeys / 32; ++i) {
+      const uint32_t w = word(row, 2 * half + i);
 #pragma unroll
       for (int e = 0; e < 32; ++e) s[32 * i + e] = (w >> e) & 1u ? s[32 * i + e] : neg_inf();
     }
@@ -468,7 +469,7 @@ int launch(const SharedWalk::Params& prm, const SharedPlan& plan, cudaStream_t s
   constexpr int kKs = D == 128 ? 2 : 5, kVs = D == 128 ? 3 : 5;
   using Geo = TileGeo<D, kKs, kVs>;
   constexpr size_t smem =
-      (size_t)Geo::kOffCtl + sizeof(TileCtl<kKs, kVs>) + sizeof(SharedWalk::Shared) + 1024;
+      (size_t)Geo::kOffCtl + sizeof(TileCtl<kKs, kVs>) + sizeof(SharedWalk::Shared);
   static_assert(smem <= 232448, "shared memory of a block");
   auto kernel = tile_attn<D, kKs, kVs, SharedWalkD<D>>;
   static std::atomic<uint64_t> done{0};

@@ -10,21 +10,21 @@
 //
 //   warp 0      producer: K and V of each step (TMA, 128-byte swizzle) into rings of
 //               tiles, Q of each unit as a box of tokens x G heads;
-//   warp 1      issues S_t = Q_t K^T and O_t += P_t V (tcgen05.mma M 128, float32 in
-//               TMEM) for both tiles from one thread: P V of the step before first,
-//               then S of this one, tile by tile, so that one tile's products run
+//   warps 1-2   tile t's issuer of O_t += P_t V (of the step before) and S_t = Q_t K^T
+//               (tcgen05.mma M 128, float32 in TMEM), so that one tile's products run
 //               while the other's softmax does;
-//   warps 2-3   every V tile on its way to the products: rows behind the last key
+//   warp 3      every V tile on its way to the products: rows behind the last key
 //               become zeros, and in steps that some row does not see in full so do
 //               NaN and infinite elements (0 times them would reach rows that do not
 //               see them; rows that do see them get them back at the end);
-//   warps 4-11  softmax, a thread per row: S from TMEM, online base-2 softmax against
-//               a reference maximum that moves only when a row's maximum grows by
-//               more than 2^8 (O is then rescaled in TMEM), P as bf16 pairs into the
-//               TMEM columns of S; at a unit's end O / l.
+//   warps 4-19  softmax, two threads per row with 64 keys of a step each: S from TMEM,
+//               online base-2 softmax against a reference maximum that moves only when
+//               a row's maximum (exchanged through shared memory) grows by more than
+//               2^8 (O is then rescaled in TMEM), P as bf16 pairs into the TMEM columns
+//               of S; at a unit's end O / l, half of the dims each.
 //
 // TMEM (512 columns): S_t at 128 t, P_t over its first half, O_t at 256 + 128 t.
-// One issuing thread keeps the order that this needs: S_t of a step is issued after
+// One issuer per tile keeps the order that this needs: S_t of a step is issued after
 // P_t V of the step before, which reads P_t from the same columns, and a commit of S_t
 // covers that P V, so a softmax warp that sees S_t may also rescale O_t.
 // Sums, statistics and outputs are float32; P is rounded to bf16 for the product and
@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kRows = 128;       // query rows per tile
 constexpr int kKeys = 128;       // keys per step
+constexpr int kHalfKeys = kKeys / 2;  // keys of a half step
 constexpr int kTaThreads = 384;
 // Registers per thread after the split: 128 x 72 + 256 x 216 = 384 x 168, what the
 // block is launched with.
@@ -67,7 +68,7 @@ struct TileGeo {
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffCtl = kOffRing + (kKs + kVs) * kTile;
   static constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) |
-                                      ((uint32_t)(kKeys >> 3) << 17) |
+                                      ((uint32_t)(kHalfKeys >> 3) << 17) |
                                       ((uint32_t)(kRows >> 4) << 24);
   // B (V as stored) is MN-major
   static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) |
@@ -78,7 +79,7 @@ template <int kKs, int kVs>
 struct __align__(8) TileCtl {
   uint64_t full[kKs + kVs], empty[kKs + kVs];  // K stages, then V stages
   uint64_t clean[kVs];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], drain;
+  uint64_t qfull[2], qempty[2], sfull[2][2], pfull[2][2], pvdone[2], ofull[2], drain;
   uint32_t tmem_base;
   uint32_t dead;  // a wait gave up
   uint32_t bad;   // a NaN or infinite element of V was taken out
@@ -104,9 +105,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// True in one lane of a warp that is whole here.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
 // bit 15 / 31 set where a bf16 half is NaN or infinite
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+// NaN and infinite halves as 0
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  return w & ~((not_finite2(w) >> 15) * 0xffffu);
 }
 
 // The Walk of a caller W offers, to whole warps:
@@ -118,7 +131,7 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
 //   keys   keys of the step that exist (the rest of the 128 is not in the sequence)
 // and, per softmax thread, a Row (set_row at a unit's start):
 //   bool warp_blind(row)          no row of this warp sees anything of the step
-//   void hide(row, s)             scores of keys the row does not see become -inf
+//   void hide(row, half, s)       scores of keys 64 half + i that it does not see: -inf
 //   bool sees(row, i), const uint16_t* value(i)   key i of the step; its V row
 //   void finish(...)              what becomes of the row
 template <int D, int kKs, int kVs, class W>
@@ -126,10 +139,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     tile_attn(const __grid_constant__ typename W::Params prm) {
   using Geo = TileGeo<D, kKs, kVs>;
   using Ctl = TileCtl<kKs, kVs>;
-  extern __shared__ __align__(1024) unsigned char araw[];
-  const uint32_t raw = smem_u32(araw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  unsigned char* bp = araw + (base - raw);
+  extern __shared__ __align__(1024) unsigned char bp[];  // the swizzle wants 1024 bytes
+  const uint32_t base = smem_u32(bp);
   Ctl& sm = *reinterpret_cast<Ctl*>(bp + Geo::kOffCtl);
   typename W::Shared& ws = *reinterpret_cast<typename W::Shared*>(bp + Geo::kOffCtl + sizeof(Ctl));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -137,17 +148,20 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kKs + kVs; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.empty[s], 2);  // given back by both issuers
     }
-    for (int s = 0; s < kVs; ++s) mbar_init(&sm.clean[s], 2);
+    for (int s = 0; s < kVs; ++s) mbar_init(&sm.clean[s], 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.qfull[t], 1);
       mbar_init(&sm.qempty[t], 1);
-      mbar_init(&sm.sfull[t], 1);
-      mbar_init(&sm.pfull[t], kRows);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sm.sfull[t][h], 1);
+        mbar_init(&sm.pfull[t][h], kRows);
+      }
+      mbar_init(&sm.pvdone[t], 1);
       mbar_init(&sm.ofull[t], 2);
     }
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain, 2);
     sm.dead = sm.bad = 0;
     fence_mbar_init();
   }
@@ -220,98 +234,102 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         for (uint32_t s = 0; s < (uint32_t)kVs && s < n; ++s)
           mbar_wait_bounded(&sm.full[kKs + s], ((n - s - 1) / kVs) & 1u);
       }
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ issuer
+    } else if (warp <= 2) {
+      // ------------------------------------------------- tile t's issuer
+      // (the whole warp runs this and one elected lane issues: the operands of an
+      // issue are then uniform over the warp)
+      const int t = warp - 1;
       const uint64_t dring = desc_kmajor(base + Geo::kOffRing);
-      const uint64_t dq0 = desc_kmajor(base);
+      const uint64_t dq = desc_kmajor(base + (uint32_t)(t * Geo::kTile));
       const uint64_t dvring = desc_mnmajor(base + Geo::kOffRing + kKs * Geo::kTile, Geo::kHalf);
+      const uint32_t tS = tmem + 128u * t, tO = tmem + 256u + 128u * t;
       uint32_t n = 0, qpar = 0, ppar = 0;
-      uint32_t pend = 0, pacc = 0, ends = 0, pv = 0;
-      auto put_pv = [&](int t) {  // O_t += P_t V of the step before
-        await(sm, &sm.clean[pv % kVs], (pv / kVs) & 1u);
-        await(sm, &sm.pfull[t], (ppar >> t) & 1u);
+      bool pend = false, acc = false, ends = false;
+      // O += P V over one half of the keys of the step before
+      auto put_pv = [&](int h) {
+        await(sm, &sm.pfull[t][h], ppar);
         fence_after();
-        const uint64_t dv = dvring + (uint64_t)((pv % kVs) * Geo::kTile >> 4);
-        const uint32_t acc = (pacc >> t) & 1u;
+        const uint64_t dv = dvring + (uint64_t)(((n - 1) % kVs) * Geo::kTile >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_f16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * k, dv + (uint64_t)(k * 128),
-                     Geo::kIdescPV, k > 0 ? 1u : acc);
-      };
-      auto end_tile = [&](int t) {  // every product of the tile's unit is issued
-        mma_commit(&sm.ofull[t]);
-        // (a plain arrival too: it hands on what this thread saw of the V tiles)
-        mbar_arrive(&sm.ofull[t]);
-      };
-      auto put_s = [&](int t, uint32_t& seen) {
-        await(sm, &sm.full[n % kKs], (n / kKs) & 1u);
-        if (!((seen >> t) & 1u)) {
-          await(sm, &sm.qfull[t], (qpar >> t) & 1u);
-          seen |= 1u << t;
+          for (int k = 0; k < kHalfKeys / 16; ++k)
+            mma_f16_ts(tO, tS + (uint32_t)(64 * h + 8 * k), dv + (uint64_t)((4 * h + k) * 128),
+                       Geo::kIdescPV, h > 0 || k > 0 || acc ? 1u : 0u);
+          mma_commit(&sm.pvdone[t]);
         }
+        __syncwarp();
+      };
+      // S of one half of the keys of this step
+      auto put_s = [&](int h) {
         fence_after();
-        const uint64_t dk = dring + (uint64_t)((n % kKs) * Geo::kTile >> 4);
-        const uint64_t dq = dq0 + (uint64_t)(t * Geo::kTile >> 4);
+        const uint64_t dk = dring + (uint64_t)((n % kKs) * Geo::kTile >> 4) +
+                            (uint64_t)(h * kHalfKeys * 128 >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint64_t off = (uint64_t)((i >> 2) * Geo::kHalf + (i & 3) * 32) >> 4;
-          mma_f16(tmem + 128u * t, dq + off, dk + off, Geo::kIdescS, i > 0 ? 1u : 0u);
+          for (int i = 0; i < D / 16; ++i) {
+            const uint64_t off = (uint64_t)((i >> 2) * Geo::kHalf + (i & 3) * 32) >> 4;
+            mma_f16(tS + 64u * h, dq + off, dk + off, Geo::kIdescS, i > 0 ? 1u : 0u);
+          }
+          mma_commit(&sm.sfull[t][h]);
         }
-        mma_commit(&sm.sfull[t]);
+        __syncwarp();
+      };
+      // the V tile of the step before, given back, and a unit that ended with it.  (An
+      // issuer whose tile takes no part waits for the tiles all the same: it must not
+      // give the next fill of a stage back in place of this one.)
+      auto give_v = [&]() {
+        if (elect_one()) {
+          if (n > 0) mma_commit(&sm.empty[kKs + (n - 1) % kVs]);
+          if (ends) {  // every product of the tile's unit is issued
+            mma_commit(&sm.ofull[t]);
+            // (a plain arrival too: it hands on what this warp saw of the V tiles)
+            mbar_arrive(&sm.ofull[t]);
+          }
+        }
+        __syncwarp();
       };
       while (w.next_unit()) {
-        uint32_t started = 0, seen = 0;
+        const bool have = (w.have >> t) & 1u;
+        bool started = false;
+        if (have) await(sm, &sm.qfull[t], qpar);
         while (w.next_step()) {
-          if (lane == 0) {
-            uint32_t todo = w.act;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (((todo & ~pend) >> t) & 1u) {
-                put_s(t, seen);
-                todo &= ~(1u << t);
-              }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if ((pend >> t) & 1u) put_pv(t);
-              if ((ends >> t) & 1u) end_tile(t);
-              if ((todo >> t) & 1u) put_s(t, seen);
-            }
-            if (pend) mma_commit(&sm.empty[kKs + pv % kVs]);
-            mma_commit(&sm.empty[n % kKs]);
+          const bool act = (w.act >> t) & 1u;
+          if (n > 0) await(sm, &sm.clean[(n - 1) % kVs], ((n - 1) / kVs) & 1u);
+          if (pend) put_pv(0);
+          await(sm, &sm.full[n % kKs], (n / kKs) & 1u);
+          if (act) put_s(0);
+          if (pend) {
+            put_pv(1);
+            ppar ^= 1u;
           }
-          ppar ^= pend;
-          pend = w.act;
-          pacc = started;
-          started |= w.act;
-          pv = n;
-          ends = 0;
-          ++n;
+          give_v();
+          if (act) put_s(1);
+          if (elect_one()) mma_commit(&sm.empty[n % kKs]);
           __syncwarp();
+          pend = act;
+          acc = started;
+          started |= act;
+          ends = false;
+          ++n;
         }
-        if (lane == 0) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if ((w.have >> t) & 1u) {
-              if (!((seen >> t) & 1u)) await(sm, &sm.qfull[t], (qpar >> t) & 1u);
-              mma_commit(&sm.qempty[t]);
-            }
+        if (have) {
+          if (elect_one()) mma_commit(&sm.qempty[t]);
+          __syncwarp();
+          qpar ^= 1u;
         }
-        qpar ^= w.have;
-        ends = w.have;
-        __syncwarp();
+        ends = have;
       }
-      if (lane == 0) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if ((pend >> t) & 1u) put_pv(t);
-          if ((ends >> t) & 1u) end_tile(t);
-        }
-        mma_commit(&sm.drain);
-        mbar_wait_bounded(&sm.drain, 0);
+      if (n > 0) await(sm, &sm.clean[(n - 1) % kVs], ((n - 1) / kVs) & 1u);
+      if (pend) {
+        put_pv(0);
+        put_pv(1);
       }
+      give_v();
+      if (elect_one()) mma_commit(&sm.drain);
+      __syncwarp();
+      mbar_wait_bounded(&sm.drain, 0);
     } else {
       // ----------------------------------------------------------- V tiles
-      const int tid = (warp - 2) * 32 + lane;
       uint32_t n = 0;
       while (w.next_unit())
         while (w.next_step()) {
@@ -321,27 +339,28 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             unsigned char* vt = bp + Geo::kOffRing + (kKs + s) * Geo::kTile;
             bool bad = false;
 #pragma unroll 1
-            for (int r = tid; r < kKeys; r += 64) {
+            for (int r = lane; r < kKeys; r += 32) {
               const bool gone = r >= w.keys;
-#pragma unroll 1
-              for (int c = 0; c < 8 * Geo::kHalves; ++c) {
-                uint4* p = reinterpret_cast<uint4*>(vt + (c >> 3) * Geo::kHalf + swz(r, c & 7));
-                if (gone) {
-                  *p = make_uint4(0u, 0u, 0u, 0u);
-                  continue;
+#pragma unroll
+              for (int hf = 0; hf < Geo::kHalves; ++hf) {
+                uint4* p[8];
+                uint4 v[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  p[c] = reinterpret_cast<uint4*>(vt + hf * Geo::kHalf + swz(r, c));
+                  v[c] = gone ? make_uint4(0u, 0u, 0u, 0u) : *p[c];
                 }
-                uint4 v = *p;
-                const uint32_t f0 = not_finite2(v.x), f1 = not_finite2(v.y),
-                               f2 = not_finite2(v.z), f3 = not_finite2(v.w);
-                if (f0 | f1 | f2 | f3) {
-                  bad = true;
-                  // 0x8000 per half -> 0xffff per half
-                  v.x &= ~((f0 >> 15) * 0xffffu);
-                  v.y &= ~((f1 >> 15) * 0xffffu);
-                  v.z &= ~((f2 >> 15) * 0xffffu);
-                  v.w &= ~((f3 >> 15) * 0xffffu);
-                  *p = v;
-                }
+                uint32_t any = 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  any |= not_finite2(v[c].x) | not_finite2(v[c].y) | not_finite2(v[c].z) |
+                         not_finite2(v[c].w);
+                if (!gone && !any) continue;
+                bad |= any != 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *p[c] = make_uint4(finite2(v[c].x), finite2(v[c].y), finite2(v[c].z),
+                                     finite2(v[c].w));
               }
             }
             if (bad) *(volatile uint32_t*)&sm.bad = 1;
@@ -362,7 +381,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const uint32_t tS = tmem + lanes + 128u * t;
     const uint32_t tO = tmem + lanes + 256u + 128u * t;
     const float sc = prm.scale_log2;
-    uint32_t spar = 0, upar = 0;
+    uint32_t steps = 0, upar = 0;  // steps of this tile; parity of its next unit's end
     typename W::Row row(prm, r);
     while (w.next_unit()) {
       if (!((w.have >> t) & 1u)) continue;
@@ -371,74 +390,87 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       bool any = false;
       while (w.next_step()) {
         if (!((w.act >> t) & 1u)) continue;
-        await(sm, &sm.sfull[t], spar);
-        spar ^= 1u;
-        fence_after();
-        if (w.warp_blind(row)) {
-          uint32_t z[32];
+        const bool blind = w.warp_blind(row);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = 0u;
-          tst32(tS, z);
-          tst32(tS + 32u, z);
-        } else {
-          uint32_t a[4][32];
+        for (int h = 0; h < 2; ++h) {
+          await(sm, &sm.sfull[t][h], steps & 1u);
+          fence_after();
+          if (blind) {
+            uint32_t z[32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tld32(tS + 32u * c, a[c]);
-          tld_wait();
-          float s[kKeys];
-#pragma unroll
-          for (int i = 0; i < kKeys; ++i) s[i] = __uint_as_float(a[i >> 5][i & 31]);
-          if (!w.full) w.hide(row, s);
-          // the scale is positive: the maximum is taken on the raw scores
-          float m4[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) m4[c] = fmax3f(s[c], s[c + 4], s[c + 8]);
-#pragma unroll
-          for (int i = 12; i < kKeys - 4; i += 8)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) m4[c] = fmax3f(m4[c], s[i + c], s[i + 4 + c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], s[kKeys - 4 + c]);
-          const float bm = fmaxf(fmax3f(m4[0], m4[1], m4[2]), m4[3]) * sc;
-          const bool move = bm > mref + 8.f;  // (also at the first visible key)
-          const float mnew = move ? bm : mref;
-          const float corr = (move && mref != neg_inf()) ? ex2(mref - mnew) : 1.f;
-          mref = mnew;
-          const float nmu = mref == neg_inf() ? 0.f : -mref;
-          if (any && __any_sync(0xffffffffu, corr != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              tld16(tO + 16u * c, o);
+            for (int i = 0; i < 32; ++i) z[i] = 0u;
+            tst32(tS + 64u * h, z);
+          } else {
+            float s[kHalfKeys];
+            {
+              uint32_t a[2][32];
+              tld32(tS + 64u * h, a[0]);
+              tld32(tS + 64u * h + 32u, a[1]);
               tld_wait();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-              tst16(tO + 16u * c, o);
+              for (int i = 0; i < kHalfKeys; ++i) s[i] = __uint_as_float(a[i >> 5][i & 31]);
             }
-          }
-          const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nmu, nmu);
-          float2 ls4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                           make_float2(0.f, 0.f)};
+            if (!w.full) w.hide(row, h, s);
+            // the scale is positive: the maximum is taken on the raw scores
+            float m4[4];
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            uint32_t pk[16];
+            for (int c = 0; c < 4; ++c) m4[c] = fmax3f(s[c], s[c + 4], s[c + 8]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int j = 32 * c + 2 * i;
-              const float2 e = ffma2(make_float2(s[j], s[j + 1]), sc2, nm2);
-              const float p0 = ex2(e.x), p1 = ex2(e.y);
-              ls4[i & 3] = fadd2(ls4[i & 3], make_float2(p0, p1));
-              pk[i] = pack_bf16(p0, p1);
+            for (int i = 12; i < kHalfKeys - 4; i += 8)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) m4[c] = fmax3f(m4[c], s[i + c], s[i + 4 + c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], s[kHalfKeys - 4 + c]);
+            const float bm = fmaxf(fmax3f(m4[0], m4[1], m4[2]), m4[3]) * sc;
+            float corr = 1.f;
+            // (also at a row's first visible key)
+            if (__any_sync(0xffffffffu, bm > mref + 8.f)) {
+              const float mnew = bm > mref + 8.f ? bm : mref;
+              if (mref != neg_inf()) corr = ex2(mref - mnew);
+              mref = mnew;
+              if (any || h > 0) {
+                // the P V of the half step before must be done (that of the one before
+                // it is: it was issued before these scores)
+                await(sm, &sm.pvdone[t], (h + 1) & 1u);
+                fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t o[16];
+                  tld16(tO + 16u * c, o);
+                  tld_wait();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+                  tst16(tO + 16u * c, o);
+                }
+              }
             }
-            tst16(tS + 16u * c, pk);
+            const float nmu = mref == neg_inf() ? 0.f : -mref;
+            const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(nmu, nmu);
+            float2 ls4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                             make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int c = 0; c < kHalfKeys / 32; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int j = 32 * c + 2 * i;
+                const float2 e = ffma2(make_float2(s[j], s[j + 1]), sc2, nm2);
+                const float p0 = ex2(e.x), p1 = ex2(e.y);
+                ls4[i & 3] = fadd2(ls4[i & 3], make_float2(p0, p1));
+                pk[i] = pack_bf16(p0, p1);
+              }
+              tst16(tS + (uint32_t)(64 * h + 16 * c), pk);
+            }
+            const float2 lsa = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
+            l = fmaf(l, corr, lsa.x + lsa.y);
           }
-          const float2 lsa = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
-          l = fmaf(l, corr, lsa.x + lsa.y);
+          tst_wait();
+          fence_before();
+          mbar_arrive(&sm.pfull[t][h]);
         }
         any = true;
-        tst_wait();
-        fence_before();
-        mbar_arrive(&sm.pfull[t]);
+        ++steps;
       }
       await(sm, &sm.ofull[t], upar);
       upar ^= 1u;
