@@ -166,7 +166,7 @@ struct PromptWalk {
     int pos;         // position in the prompt
     bool valid;
     float mul;
-    uint4* dst;
+    uint4* dst[4];   // rows of out that this lane helps to write
     __device__ __forceinline__ Row(const Params& p, int r)
         : tok(r / p.G), head(r % p.G) {}
   };
@@ -195,19 +195,16 @@ struct PromptWalkD : PromptWalk {
   __device__ __forceinline__ void begin_finish(Row& row, int, float mref, float l) const {
     row.mul = l == 0.f ? 0.f : 1.f / l;
     const int64_t at_ = (int64_t)(a + row.pos) * p.Hq + h * p.G + row.head;
-    row.dst = reinterpret_cast<uint4*>(p.out + at_ * D);
+    share_rows(row.valid ? reinterpret_cast<uint4*>(p.out + at_ * D) : nullptr, row.dst);
     if (row.valid && p.lse) p.lse[at_] = mref + log2f(l);
   }
-  __device__ __forceinline__ void finish(const Row& row, int, int c, const float (&o)[32]) const {
-    if (!row.valid) return;
+  __device__ __forceinline__ void finish(Row& row, int, int, const float (&o)[32]) const {
+    uint4 v[4];
+    pack_row(o, row.mul, v);
+    store_rows(row.dst, v);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int i = 8 * v;
-      row.dst[4 * c + v] = make_uint4(pack_bf16(o[i] * row.mul, o[i + 1] * row.mul),
-                                      pack_bf16(o[i + 2] * row.mul, o[i + 3] * row.mul),
-                                      pack_bf16(o[i + 4] * row.mul, o[i + 5] * row.mul),
-                                      pack_bf16(o[i + 6] * row.mul, o[i + 7] * row.mul));
-    }
+    for (int i = 0; i < 4; ++i)
+      if (row.dst[i]) row.dst[i] += 4;  // the next 32 dims
   }
 };
 

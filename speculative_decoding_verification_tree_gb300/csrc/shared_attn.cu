@@ -102,46 +102,10 @@ struct SharedWalk {
     b0 = first_of(p, g) + (k - sh.tiles[g]) * p.spu;
     nb = min(p.spu, first_of(p, g + 1) - b0);
   }
-  __device__ static void setup(const Params& p, Shared& sh, void* scratch) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t* before = reinterpret_cast<int64_t*>(scratch);  // [threads]
-    int64_t* tmp = before + kTaThreads;
-    for (int g = tid; g < p.groups; g += kTaThreads) {
-      const int n = max(0, first_of(p, g + 1) - first_of(p, g));
-      sh.tiles[g + 1] = (uint16_t)((n + p.spu - 1) / p.spu);
-    }
-    launch_dependents();
-    if (tid == 0) {
-      sh.tiles[0] = 0;
-      p.part.head[blockIdx.x].slot = -1;
-    }
-    __syncthreads();
-    if (warp == 0) {  // running sum
-      int carry = 0;
-      for (int i0 = 1; i0 <= p.groups; i0 += 32) {
-        int v = i0 + lane <= p.groups ? sh.tiles[i0 + lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += u;
-        }
-        if (i0 + lane <= p.groups) sh.tiles[i0 + lane] = (uint16_t)min(carry + v, 65535);
-        carry += __shfl_sync(0xffffffffu, v, 31);
-      }
-    }
-    __syncthreads();
-    const int total = sh.tiles[p.groups] * p.chunks;
-    const int per = (total + kTaThreads - 1) / kTaThreads;
-    auto steps = [&](int i) {
-      int g, b0, nb, part;
-      rows_of(p, sh, i, g, b0, nb, part);
-      int64_t n = (shared_of(p, g) + kKeys - 1) / kKeys;
-      for (int b = b0; b < b0 + nb; ++b) n += own_blocks(p, b);
-      return n;
-    };
-    const int first = min(total, tid * per), last = min(total, first + per);
-    int64_t v = 0;
-    for (int i = first; i < last; ++i) v += steps(i);
+  // Exclusive running sum of v over the threads; tmp: a value per warp.  Ends with a
+  // barrier.
+  __device__ __forceinline__ static int64_t scan(int64_t v, int64_t* tmp, int64_t* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t s = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -150,12 +114,55 @@ struct SharedWalk {
     }
     if (lane == 31) tmp[warp] = s;
     __syncthreads();
-    int64_t base = 0, all = 0;
+    int64_t base = 0, sum = 0;
+#pragma unroll
     for (int w = 0; w < kTaThreads / 32; ++w) {
       if (w < warp) base += tmp[w];
-      all += tmp[w];
+      sum += tmp[w];
     }
-    s += base;
+    *all = sum;
+    __syncthreads();
+    return base + s - v;
+  }
+  __device__ static void setup(const Params& p, Shared& sh, void* scratch) {
+    const int tid = threadIdx.x;
+    int64_t* tmp = reinterpret_cast<int64_t*>(scratch);  // [32]
+    int64_t* seqs = tmp + 32;  // own steps before sequence tid * ps, [threads + 1]
+    launch_dependents();
+    if (tid == 0) p.part.head[blockIdx.x].slot = -1;
+    // steps of the sequences' own keys before every ps-th sequence
+    const int ps = (p.B + kTaThreads - 1) / kTaThreads;
+    int64_t v = 0, all;
+    for (int b = tid * ps; b < min(p.B, (tid + 1) * ps); ++b) v += own_blocks(p, b);
+    seqs[tid] = scan(v, tmp, &all);
+    if (tid == 0) seqs[kTaThreads] = all;
+    // unit rows before every prefix
+    int total = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += kTaThreads) {
+      const int g = g0 + tid;
+      const int n = g < p.groups ? max(0, first_of(p, g + 1) - first_of(p, g)) : 0;
+      const int u = (int)scan((n + p.spu - 1) / p.spu, tmp, &all);
+      if (g < p.groups) sh.tiles[g] = (uint16_t)min(total + u, 65535);
+      total = (int)min((int64_t)total + all, (int64_t)65535);
+    }
+    if (tid == 0) sh.tiles[p.groups] = (uint16_t)total;
+    __syncthreads();
+    auto before = [&](int b) {  // own steps before sequence b
+      int64_t n = seqs[b / ps];
+      for (int x = b / ps * ps; x < b; ++x) n += own_blocks(p, x);
+      return n;
+    };
+    auto steps = [&](int i) {  // of unit row i
+      int g, b0, nb, part;
+      rows_of(p, sh, i, g, b0, nb, part);
+      return (shared_of(p, g) + kKeys - 1) / kKeys + before(b0 + nb) - before(b0);
+    };
+    total *= p.chunks;
+    const int per = (total + kTaThreads - 1) / kTaThreads;
+    const int first = min(total, tid * per), last = min(total, first + per);
+    v = 0;
+    for (int i = first; i < last; ++i) v += steps(i);
+    const int64_t mine = scan(v, tmp, &all);
     const int64_t line = all * p.Hkv;
     int64_t len = (line + gridDim.x - 1) / gridDim.x;
     if (len < kMinSteps) len = kMinSteps;
@@ -164,17 +171,14 @@ struct SharedWalk {
       sh.len = len;
       sh.p0 = p0;
       sh.p1 = p1;
-      sh.tile = 0;
-      sh.cum = 0;
     }
-    __syncthreads();
     // the thread whose unit rows hold the piece's first step finds it
     const int64_t want = p0 / p.Hkv;
-    if (p0 < line && s - v <= want && want < s) {
-      int64_t x = s - v;
+    if (p0 < line && mine <= want && want < mine + v) {
+      int64_t x = mine;
       int i = first;
       for (;; ++i) {
-        const int64_t n = steps(i);
+        const int64_t n = per > 1 ? steps(i) : v;
         if (want < x + n) break;
         x += n;
       }
@@ -259,14 +263,16 @@ struct SharedWalk {
       act = both ? 1u << ((j - j0) & 1) : have;
       return true;
     }
-    if (b < 0) {
-      seek(j - nsb);
-    } else if (++jb == nob) {
-      jb = 0;
-      ++b;
+    if (b < 0 || ++jb == nob) {  // another sequence
+      if (b < 0) {
+        seek(j - nsb);
+      } else {
+        jb = 0;
+        ++b;
+      }
+      P = prefix_of(p, b);
+      nob = (P + p.N + kKeys - 1) / kKeys;
     }
-    P = prefix_of(p, b);
-    nob = (P + p.N + kKeys - 1) / kKeys;
     key0 = jb * kKeys;
     keys = min(kKeys, P + p.N - key0);
     full = nb == 1 && key0 + kKeys <= P;
@@ -296,7 +302,8 @@ struct SharedWalk {
     bool valid;
     uint64_t mb;       // drafted keys it sees
     float mul;
-    int64_t dst;       // row of out, or of the partial results
+    int64_t dst;       // row of the partial results
+    uint4* rows[4];    // rows of out that this lane helps to write
     __device__ __forceinline__ Row(const Params& p, int r_)
         : r(r_), tok(r_ / p.G), head(r_ % p.G) {}
   };
@@ -351,10 +358,11 @@ struct SharedWalkD : SharedWalk {
       return;
     }
     row.mul = l == 0.f ? 0.f : 1.f / l;
-    row.dst = (int64_t)row.token * p.Hq + h * p.G + row.head;
-    if (row.valid && p.lse) p.lse[row.dst] = mref + log2f(l);
+    const int64_t at_ = (int64_t)row.token * p.Hq + h * p.G + row.head;
+    share_rows(row.valid ? reinterpret_cast<uint4*>(p.out + at_ * D) : nullptr, row.rows);
+    if (row.valid && p.lse) p.lse[at_] = mref + log2f(l);
   }
-  __device__ __forceinline__ void finish(const Row& row, int, int c, const float (&o)[32]) const {
+  __device__ __forceinline__ void finish(Row& row, int, int c, const float (&o)[32]) const {
     if (!whole) {  // 16 bytes of 32 rows side by side
 #pragma unroll
       for (int v = 0; v < 8; ++v)
@@ -362,16 +370,12 @@ struct SharedWalkD : SharedWalk {
             make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
       return;
     }
-    if (!row.valid) return;
-    uint4* dst = reinterpret_cast<uint4*>(p.out + row.dst * D) + 4 * c;
+    uint4 v[4];
+    pack_row(o, row.mul, v);
+    store_rows(row.rows, v);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int i = 8 * v;
-      dst[v] = make_uint4(pack_bf16(o[i] * row.mul, o[i + 1] * row.mul),
-                          pack_bf16(o[i + 2] * row.mul, o[i + 3] * row.mul),
-                          pack_bf16(o[i + 4] * row.mul, o[i + 5] * row.mul),
-                          pack_bf16(o[i + 6] * row.mul, o[i + 7] * row.mul));
-    }
+    for (int i = 0; i < 4; ++i)
+      if (row.rows[i]) row.rows[i] += 4;  // the next 32 dims
   }
 };
 
@@ -388,6 +392,7 @@ __global__ void __launch_bounds__(2 * kRows)
   const int t = threadIdx.x / kRows, r = threadIdx.x % kRows;
   auto place = [&](int c) { return ((int64_t)c * 2 + (c == (int)blockIdx.x ? u.slot : 0)) * 2 + t; };
   float M = neg_inf();
+#pragma unroll 8
   for (int c = blockIdx.x; c <= u.last; ++c) M = fmaxf(M, part.ml[place(c) * kRows + r].x);
   float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const float ref = M == neg_inf() ? 0.f : M;

@@ -52,10 +52,6 @@ constexpr int kRows = 128;       // query rows per tile
 constexpr int kKeys = 128;       // keys per step
 constexpr int kHalfKeys = kKeys / 2;  // keys of a half step
 constexpr int kTaThreads = 384;
-// Registers per thread after the split: 128 x 72 + 256 x 216 = 384 x 168, what the
-// block is launched with.
-constexpr int kCtlRegs = 72, kSoftRegs = 216;
-static_assert(128 * kCtlRegs + 256 * kSoftRegs <= kTaThreads * 168, "register split");
 constexpr int kTaCtas = 152;     // one per SM
 constexpr uint32_t kTaTmemCols = 512;
 
@@ -105,6 +101,51 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Rows of 64 bytes, a lane each, written so that four lanes write one row at a time:
+// place[i] is the row of lane 4 (lane / 4) + i (its 64 bytes; null: not written).  A
+// store then covers 8 rows instead of 16 bytes of each of 32.
+__device__ __forceinline__ uint4 pick(bool second, const uint4& a, const uint4& b) {
+  return make_uint4(second ? b.x : a.x, second ? b.y : a.y, second ? b.z : a.z,
+                    second ? b.w : a.w);
+}
+__device__ __forceinline__ uint4 swap_lanes(const uint4& v, int mask) {
+  return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask),
+                    __shfl_xor_sync(0xffffffffu, v.z, mask), __shfl_xor_sync(0xffffffffu, v.w, mask));
+}
+__device__ __forceinline__ void store_rows(uint4* const (&place)[4], uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {  // 2 x 2 blocks across neighbours
+    const uint4 got = swap_lanes(pick(odd, v[i + 1], v[i]), 1);
+    v[i] = pick(odd, v[i], got);
+    v[i + 1] = pick(odd, got, v[i + 1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {     // and across pairs
+    const uint4 got = swap_lanes(pick(high, v[i + 2], v[i]), 2);
+    v[i] = pick(high, v[i], got);
+    v[i + 2] = pick(high, got, v[i + 2]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (place[i]) place[i][lane & 3] = v[i];
+}
+__device__ __forceinline__ void share_rows(uint4* mine, uint4* (&place)[4]) {
+  const uint64_t p = reinterpret_cast<uint64_t>(mine);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    place[i] = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, p, (threadIdx.x & 28) + i));
+}
+// 32 values scaled, as 64 bytes of bf16
+__device__ __forceinline__ void pack_row(const float (&o)[32], float mul, uint4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = make_uint4(pack_bf16(o[8 * i] * mul, o[8 * i + 1] * mul),
+                      pack_bf16(o[8 * i + 2] * mul, o[8 * i + 3] * mul),
+                      pack_bf16(o[8 * i + 4] * mul, o[8 * i + 5] * mul),
+                      pack_bf16(o[8 * i + 6] * mul, o[8 * i + 7] * mul));
+}
 // True in one lane of a warp that is whole here.
 __device__ __forceinline__ bool elect_one() {
   uint32_t e;
@@ -116,6 +157,12 @@ __device__ __forceinline__ bool elect_one() {
 // bit 15 / 31 set where a bf16 half is NaN or infinite
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+// acc + 0 w, bf16 pairs
+__device__ __forceinline__ uint32_t times_zero(uint32_t w, uint32_t acc) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(acc));
+  return d;
 }
 // NaN and infinite halves as 0
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -180,7 +227,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   const uint32_t tmem = sm.tmem_base;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
     W w(prm, ws);
     if (warp == 0) {
       // ---------------------------------------------------------- producer
@@ -337,33 +383,40 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           await(sm, &sm.full[kKs + s], (n / kVs) & 1u);
           if (!w.full) {
             unsigned char* vt = bp + Geo::kOffRing + (kKs + s) * Geo::kTile;
-            bool bad = false;
+            // x * 0 is NaN where x is not finite, and stays so in a sum
+            uint32_t nan[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 1
             for (int r = lane; r < kKeys; r += 32) {
-              const bool gone = r >= w.keys;
 #pragma unroll
               for (int hf = 0; hf < Geo::kHalves; ++hf) {
-                uint4* p[8];
-                uint4 v[8];
+                uint4* row = reinterpret_cast<uint4*>(vt + hf * Geo::kHalf + r * 128);
+                if (r >= w.keys) {  // behind the last key
+#pragma unroll
+                  for (int c = 0; c < 8; ++c) row[c] = make_uint4(0u, 0u, 0u, 0u);
+                  continue;
+                }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                  p[c] = reinterpret_cast<uint4*>(vt + hf * Geo::kHalf + swz(r, c));
-                  v[c] = gone ? make_uint4(0u, 0u, 0u, 0u) : *p[c];
+                  const uint4 v = row[c ^ (r & 7)];
+                  nan[0] = times_zero(v.x, nan[0]);
+                  nan[1] = times_zero(v.y, nan[1]);
+                  nan[2] = times_zero(v.z, nan[2]);
+                  nan[3] = times_zero(v.w, nan[3]);
                 }
-                uint32_t any = 0;
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  any |= not_finite2(v[c].x) | not_finite2(v[c].y) | not_finite2(v[c].z) |
-                         not_finite2(v[c].w);
-                if (!gone && !any) continue;
-                bad |= any != 0;
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *p[c] = make_uint4(finite2(v[c].x), finite2(v[c].y), finite2(v[c].z),
-                                     finite2(v[c].w));
               }
             }
-            if (bad) *(volatile uint32_t*)&sm.bad = 1;
+            if (not_finite2(nan[0]) | not_finite2(nan[1]) | not_finite2(nan[2]) |
+                not_finite2(nan[3])) {
+              *(volatile uint32_t*)&sm.bad = 1;
+#pragma unroll 1
+              for (int i = lane; i < kKeys * 32 * Geo::kHalves; i += 32) {
+                // (row of 32 words, as this lane has read it)
+                const int r = (i & 31) + ((i >> 5) & 3) * 32, word = i >> 7;
+                uint32_t* x = reinterpret_cast<uint32_t*>(vt + (word >> 5) * Geo::kHalf + r * 128) +
+                              (word & 31);
+                *x = finite2(*x);
+              }
+            }
             fence_async_smem();
           }
           __syncwarp();
@@ -373,7 +426,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     W w(prm, ws);
     const int t = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;
