@@ -54,6 +54,16 @@ struct PromptWalk {
     const int n = start_of(p, b + 1) - start_of(p, b);
     return n <= 0 ? 0 : (n - 1) / (2 * p.tpt) + 1;
   }
+  __device__ __forceinline__ static void prefetch_maps(const Params& p) {
+    prefetch_map(&p.k);
+    prefetch_map(&p.q);
+    prefetch_map(&p.v);
+  }
+  // n / d for 0 <= n, 0 < d
+  __device__ __forceinline__ static int64_t over(int64_t n, int64_t d) {
+    return n < ((int64_t)1 << 31) && d < ((int64_t)1 << 31) ? (int64_t)((uint32_t)n / (uint32_t)d)
+                                                             : n / d;
+  }
   __device__ __forceinline__ static void setup(const Params& p, Shared& sh, void*) {
     if (threadIdx.x == 0) sh.most = 0;
     __syncthreads();
@@ -100,7 +110,7 @@ struct PromptWalk {
         below = __reduce_max_sync(0xffffffffu, below);
         const int64_t per = (int64_t)n * p.Hkv;
         if (at < per * (level - below + 1)) {
-          const int down = (int)(at / per);
+          const int down = (int)over(at, per);
           level -= down;
           at -= per * down;
           int k = (int)at / p.Hkv;  // the k-th prompt that has this level
@@ -108,7 +118,10 @@ struct PromptWalk {
             const uint32_t m =
                 __ballot_sync(0xffffffffu, b0 + lane < p.B && sh.tiles[b0 + lane] > level);
             if (k < __popc(m)) {
-              take(b0 + (int)__fns(m, 0, k + 1), level, (int)at % p.Hkv);
+              // the lane whose bit has k set ones below it
+              const uint32_t at_k = __ballot_sync(
+                  0xffffffffu, ((m >> lane) & 1u) && __popc(m & ((1u << lane) - 1u)) == k);
+              take(b0 + __ffs(at_k) - 1, level, (int)at % p.Hkv);
               return true;
             }
             k -= __popc(m);

@@ -27,7 +27,7 @@ namespace sv {
 namespace {
 
 constexpr int kMaxPrefixes = SPEC_MAX_PREFIXES;
-constexpr int kMinSteps = 4;     // steps of a piece, at least
+constexpr int kMinSteps = 2;     // steps of a piece, at least
 
 struct SharedHead {  // the unit that begins in a piece and ends in a later one
   int slot;          // -1: there is none
@@ -56,6 +56,8 @@ struct SharedWalk {
   struct Shared {
     // unit rows before each prefix, in parts of `chunks` (at most B: 16 bits)
     uint16_t tiles[kMaxPrefixes + 1];
+    int firsts[kMaxPrefixes + 1];  // each prefix's first sequence (clamped)
+    int slen[kMaxPrefixes];        // and its shared keys (clamped)
     int64_t len, p0, p1;          // steps per piece; this CTA's piece of the line
     int64_t cum;                  // steps (of one head) before the unit that holds p0
     int tile;                     // that unit
@@ -76,6 +78,13 @@ struct SharedWalk {
   bool full, own;
   int b, jb, nob, P;  // the sequence whose own block it is
 
+  __device__ __forceinline__ static void prefetch_maps(const Params& p) {
+    prefetch_map(&p.ks);
+    prefetch_map(&p.q);
+    prefetch_map(&p.vs);
+    prefetch_map(&p.ko);
+    prefetch_map(&p.vo);
+  }
   __device__ __forceinline__ static int first_of(const Params& p, int g) {
     return min(max(p.group_start[g], 0), p.B);
   }
@@ -88,10 +97,10 @@ struct SharedWalk {
   __device__ __forceinline__ static int own_blocks(const Params& p, int b) {
     return (prefix_of(p, b) + p.N + kKeys - 1) / kKeys;
   }
-  // prefix and sequences of unit row i
-  __device__ __forceinline__ static void rows_of(const Params& p, const Shared& sh, int i, int& g,
-                                                 int& b0, int& nb, int& part) {
-    const int k = i / p.chunks;
+  // prefix of unit row i, the row's number there and which part of a sequence it is
+  __device__ __forceinline__ static void prefix_of_row(const Params& p, const Shared& sh, int i,
+                                                       int& g, int& k, int& part) {
+    k = p.chunks > 1 ? i / p.chunks : i;
     part = i - k * p.chunks;
     int lo = 0, hi = p.groups - 1;  // the last prefix with tiles[g] <= k
     while (lo < hi) {
@@ -99,72 +108,91 @@ struct SharedWalk {
       if (sh.tiles[mid] <= k) lo = mid; else hi = mid - 1;
     }
     g = lo;
-    b0 = first_of(p, g) + (k - sh.tiles[g]) * p.spu;
-    nb = min(p.spu, first_of(p, g + 1) - b0);
+    k -= sh.tiles[g];
   }
-  // Exclusive running sum of v over the threads; tmp: a value per warp.  Ends with a
-  // barrier.
-  __device__ __forceinline__ static int64_t scan(int64_t v, int64_t* tmp, int64_t* all) {
+  // Exclusive running sums over the threads of two values at once; tmp: [64].  Ends with
+  // a barrier.
+  __device__ __forceinline__ static void scan(int64_t& a, int64_t& b, int64_t* tmp,
+                                              int64_t& all_a, int64_t& all_b) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t s = v;
+    constexpr int kW = kTaThreads / 32;
+    int64_t x = a, y = b;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += u;
+      const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) {
+        x += u;
+        y += v;
+      }
     }
-    if (lane == 31) tmp[warp] = s;
+    if (lane == 31) {
+      tmp[warp] = x;
+      tmp[32 + warp] = y;
+    }
     __syncthreads();
-    int64_t base = 0, sum = 0;
+    x -= a;
+    y -= b;
+    all_a = all_b = 0;
 #pragma unroll
-    for (int w = 0; w < kTaThreads / 32; ++w) {
-      if (w < warp) base += tmp[w];
-      sum += tmp[w];
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) {
+        x += tmp[w];
+        y += tmp[32 + w];
+      }
+      all_a += tmp[w];
+      all_b += tmp[32 + w];
     }
-    *all = sum;
+    a = x;
+    b = y;
     __syncthreads();
-    return base + s - v;
+  }
+  __device__ __forceinline__ static int64_t over(int64_t n, int d) {  // n / d
+    return n < ((int64_t)1 << 31) ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
   }
   __device__ static void setup(const Params& p, Shared& sh, void* scratch) {
     const int tid = threadIdx.x;
-    int64_t* tmp = reinterpret_cast<int64_t*>(scratch);  // [32]
-    int64_t* seqs = tmp + 32;  // own steps before sequence tid * ps, [threads + 1]
+    int64_t* tmp = reinterpret_cast<int64_t*>(scratch);           // [64]
+    int64_t* seqs = tmp + 64;      // own steps before sequence tid * ps, [threads + 1]
+    static_assert(kMaxPrefixes < kTaThreads, "a thread per prefix");
     launch_dependents();
     if (tid == 0) p.part.head[blockIdx.x].slot = -1;
-    // steps of the sequences' own keys before every ps-th sequence
+    // a thread's sequences and its prefix
     const int ps = (p.B + kTaThreads - 1) / kTaThreads;
-    int64_t v = 0, all;
-    for (int b = tid * ps; b < min(p.B, (tid + 1) * ps); ++b) v += own_blocks(p, b);
-    seqs[tid] = scan(v, tmp, &all);
-    if (tid == 0) seqs[kTaThreads] = all;
-    // unit rows before every prefix
-    int total = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += kTaThreads) {
-      const int g = g0 + tid;
-      const int n = g < p.groups ? max(0, first_of(p, g + 1) - first_of(p, g)) : 0;
-      const int u = (int)scan((n + p.spu - 1) / p.spu, tmp, &all);
-      if (g < p.groups) sh.tiles[g] = (uint16_t)min(total + u, 65535);
-      total = (int)min((int64_t)total + all, (int64_t)65535);
+    int64_t own = 0, rows = 0, all, total;
+    if (tid < p.groups) {
+      const int lo = first_of(p, tid), hi = first_of(p, tid + 1);
+      sh.firsts[tid] = lo;
+      if (tid == p.groups - 1) sh.firsts[tid + 1] = hi;
+      sh.slen[tid] = shared_of(p, tid);
+      rows = hi > lo ? (uint32_t)(hi - lo + p.spu - 1) / (uint32_t)p.spu : 0;
     }
-    if (tid == 0) sh.tiles[p.groups] = (uint16_t)total;
+    for (int b = tid * ps; b < min(p.B, (tid + 1) * ps); ++b) own += own_blocks(p, b);
+    scan(own, rows, tmp, all, total);
+    seqs[tid] = own;
+    if (tid == 0) seqs[kTaThreads] = all;
+    if (tid <= p.groups) sh.tiles[tid] = (uint16_t)min(rows, (int64_t)65535);
     __syncthreads();
     auto before = [&](int b) {  // own steps before sequence b
+      if (ps == 1) return seqs[b];
       int64_t n = seqs[b / ps];
       for (int x = b / ps * ps; x < b; ++x) n += own_blocks(p, x);
       return n;
     };
     auto steps = [&](int i) {  // of unit row i
-      int g, b0, nb, part;
-      rows_of(p, sh, i, g, b0, nb, part);
-      return (shared_of(p, g) + kKeys - 1) / kKeys + before(b0 + nb) - before(b0);
+      int g, k, part;
+      prefix_of_row(p, sh, i, g, k, part);
+      const int b0 = sh.firsts[g] + k * p.spu, b1 = min(sh.firsts[g + 1], b0 + p.spu);
+      return (sh.slen[g] + kKeys - 1) / kKeys + before(b1) - before(b0);
     };
-    total *= p.chunks;
-    const int per = (total + kTaThreads - 1) / kTaThreads;
-    const int first = min(total, tid * per), last = min(total, first + per);
-    v = 0;
-    for (int i = first; i < last; ++i) v += steps(i);
-    const int64_t mine = scan(v, tmp, &all);
+    const int n = (int)min(total, (int64_t)65535) * p.chunks;
+    const int per = (n + kTaThreads - 1) / kTaThreads;
+    const int first = min(n, tid * per), last = min(n, first + per);
+    int64_t mine = 0, none = 0;
+    for (int i = first; i < last; ++i) mine += steps(i);
+    const int64_t v = mine;
+    scan(mine, none, tmp, all, total);
     const int64_t line = all * p.Hkv;
-    int64_t len = (line + gridDim.x - 1) / gridDim.x;
+    int64_t len = over(line + gridDim.x - 1, (int)gridDim.x);
     if (len < kMinSteps) len = kMinSteps;
     const int64_t p0 = min(line, len * blockIdx.x), p1 = min(line, p0 + len);
     if (tid == 0) {
@@ -173,14 +201,14 @@ struct SharedWalk {
       sh.p1 = p1;
     }
     // the thread whose unit rows hold the piece's first step finds it
-    const int64_t want = p0 / p.Hkv;
+    const int64_t want = over(p0, p.Hkv);
     if (p0 < line && mine <= want && want < mine + v) {
       int64_t x = mine;
       int i = first;
       for (;; ++i) {
-        const int64_t n = per > 1 ? steps(i) : v;
-        if (want < x + n) break;
-        x += n;
+        const int64_t s = per > 1 ? steps(i) : v;
+        if (want < x + s) break;
+        x += s;
       }
       sh.tile = i;
       sh.cum = x;
@@ -194,11 +222,13 @@ struct SharedWalk {
 
   __device__ __forceinline__ void load_rows() {
     const int lane = threadIdx.x & 31;
-    int part;
-    rows_of(p, sh, tile, g, b0, nb, part);
+    int k, part;
+    prefix_of_row(p, sh, tile, g, k, part);
+    b0 = sh.firsts[g] + k * p.spu;
+    nb = min(p.spu, sh.firsts[g + 1] - b0);
     tok0 = b0 * p.N + part * 2 * p.tpt;
     ntok = p.chunks > 1 ? min(2 * p.tpt, p.N - part * 2 * p.tpt) : nb * p.N;
-    slen = shared_of(p, g);
+    slen = sh.slen[g];
     nsb = (slen + kKeys - 1) / kKeys;
     int n = 0;
     for (int i = lane; i < nb; i += 32) n += own_blocks(p, b0 + i);
@@ -212,7 +242,7 @@ struct SharedWalk {
       load_rows();
     }
     const int64_t off = at - tb;
-    h = (int)(off / nblk);
+    h = (int)over(off, nblk);
     j0 = (int)(off - (int64_t)h * nblk);
     j1 = (int)min((int64_t)nblk, j0 + (sh.p1 - at));
     at += j1 - j0;

@@ -96,6 +96,9 @@ __device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* map, int 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -170,7 +173,7 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 }
 
 // The Walk of a caller W offers, to whole warps:
-//   static setup(prm, shared, scratch)   once, before the roles part
+//   static setup(prm, shared, scratch), prefetch_maps(prm)   once, before the roles part
 //   bool next_unit(), bool next_step(), restart() (the unit's steps from the start)
 //   have   tiles of the unit (bits);  act   tiles that take part in the step
 //   full   no row of the unit lacks a key of the step
@@ -219,6 +222,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (threadIdx.x == kTaThreads - 1) W::prefetch_maps(prm);
   W::setup(prm, ws, bp);  // every thread; may use the tiles' space; ends with a barrier
   fence_async_smem();
   fence_before();
@@ -340,18 +344,29 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         if (have) await(sm, &sm.qfull[t], qpar);
         while (w.next_step()) {
           const bool act = (w.act >> t) & 1u;
+          auto give_k = [&]() {
+            if (elect_one()) mma_commit(&sm.empty[n % kKs]);
+            __syncwarp();
+          };
+          if (!act) {  // its keys are for the other tile only
+            await(sm, &sm.full[n % kKs], (n / kKs) & 1u);
+            give_k();
+          }
           if (n > 0) await(sm, &sm.clean[(n - 1) % kVs], ((n - 1) / kVs) & 1u);
           if (pend) put_pv(0);
-          await(sm, &sm.full[n % kKs], (n / kKs) & 1u);
-          if (act) put_s(0);
+          if (act) {
+            await(sm, &sm.full[n % kKs], (n / kKs) & 1u);
+            put_s(0);
+          }
           if (pend) {
             put_pv(1);
             ppar ^= 1u;
           }
           give_v();
-          if (act) put_s(1);
-          if (elect_one()) mma_commit(&sm.empty[n % kKs]);
-          __syncwarp();
+          if (act) {
+            put_s(1);
+            give_k();
+          }
           pend = act;
           acc = started;
           started |= act;

@@ -12,11 +12,13 @@
 // a factor of 2^10: sums stay far inside float32, and moving is rare (a running
 // maximum moves in some lane of a warp at nearly every step).  Bound by reading the logits once.
 //
-// Alternatives: each thread also keeps its largest logit.  The top-th largest
-// of those is a lower bound of the top-th largest logit of the CTA's part, so
-// only threads whose largest reaches the bound hold candidates; their logits
-// are read again (by a warp each, from L2) and the few candidates ranked by
-// (value, lower index).  Parts where that leaves too few or too many candidates
+// Alternatives: each thread also keeps its largest logit.  At least `top` of those
+// are at or above the smallest of the eight warps' ceil(top / 8)-th largest, so that one is a
+// lower bound of the top-th largest logit of the CTA's part (the exact top-th of the
+// 256 costs five times the instructions, and was what a CTA of a short part spent most
+// of its time on); only threads whose largest reaches it hold candidates.  Their
+// logits are read again, from L2, and the few candidates ranked by (value, lower
+// index).  Parts where that leaves too few or too many candidates
 // (ties, NaN, masked vocabularies) take an exact radix selection instead.
 //
 // Few rows are split over the CTAs of a cluster, joined through distributed
@@ -39,6 +41,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = SPEC_MAX_TOP_K;
 constexpr int kCandCap = 1024;
+constexpr int kAgain = 4;  // groups of flagged threads in flight when they are read again
 constexpr int kMaxCluster = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMove = 10.f;    // base-2 distance at which a reference moves
@@ -55,6 +58,9 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   if (isnan(v)) return 0u;
   const uint32_t b = __float_as_uint(v + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
 template <typename T>
@@ -117,30 +123,37 @@ struct RowSpan {
   __device__ __forceinline__ int place(int i) const { return i < head ? i : tail + i - head; }
 };
 
-struct Cand {
-  uint32_t key;
-  int32_t idx;
-};
-__device__ __forceinline__ bool ahead(Cand a, Cand b) {
-  return a.key > b.key || (a.key == b.key && a.idx < b.idx);
+// A candidate as one number: the larger, the further ahead (value, then lower index).
+// 0: none.
+using Cand = uint64_t;
+__device__ __forceinline__ Cand make_cand(uint32_t key, int idx) {
+  return ((uint64_t)key << 32) | (0xFFFFFFFFu - (uint32_t)idx);
 }
+__device__ __forceinline__ int cand_idx(Cand c) { return (int)(0xFFFFFFFFu - (uint32_t)c); }
+__device__ __forceinline__ uint32_t cand_key(Cand c) { return (uint32_t)(c >> 32); }
 
+struct Sums {
+  float m, s, a;
+};
 struct LpSmem {
+  Sums part[kMaxCluster];  // rank 0: the parts of the row
   float rm[kWarps], rs[kWarps], ra[kWarps];
   float m, s, a;        // this CTA's part
-  uint32_t tau;
-  int nflag, ncand, ntop;
-  uint32_t key[kThreads];
+  uint32_t tau[32];
+  int nflag, ncand;
   uint16_t flag[kThreads];
-  Cand cand[kCandCap];
+  __align__(16) Cand cand[kCandCap];
   Cand best[kMaxTop];   // this CTA's part, best first
   int hist[256];
   int digit, above, base;
 };
 
-struct Sums {
-  float m, s, a;
-};
+__device__ __forceinline__ void st_dsmem(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_dsmem64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
 __device__ __forceinline__ Sums join(Sums x, Sums y) {
   const float m = fmaxf(x.m, y.m);
   if (m == neg_inf()) return {m, x.s + y.s, x.a + y.a};
@@ -194,7 +207,7 @@ __device__ void select_exact(LpSmem& sm, int n, int k, At at, Idx idx) {
   __syncthreads();
   for (int i = tid; i < n; i += kThreads) {
     const uint32_t key = order_key(at(i));
-    if (key > prefix) sm.cand[atomicAdd(&sm.ncand, 1)] = Cand{key, idx(i)};
+    if (key > prefix) sm.cand[atomicAdd(&sm.ncand, 1)] = make_cand(key, idx(i));
   }
   __syncthreads();
   const int above = sm.ncand;
@@ -211,7 +224,7 @@ __device__ void select_exact(LpSmem& sm, int n, int k, At at, Idx idx) {
         all += sm.hist[w];
       }
       before += __popc(bal & ((1u << lane) - 1u));
-      if (eq && before < need) sm.cand[above + before] = Cand{prefix, idx(i)};
+      if (eq && before < need) sm.cand[above + before] = make_cand(prefix, idx(i));
       __syncthreads();
       if (tid == 0) sm.base += all;
       __syncthreads();
@@ -225,14 +238,14 @@ __device__ void select_exact(LpSmem& sm, int n, int k, At at, Idx idx) {
 
 // One row per cluster.  kEnt: also the entropy.  kTop: also alternatives.
 template <typename T, bool kEnt, bool kTop>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 4)
     token_logprobs(const T* __restrict__ logits, int64_t ld, int R, int V,
                    const int32_t* __restrict__ rows, const int32_t* __restrict__ tokens, int n,
                    int top, float kt, float* __restrict__ logprob, float* __restrict__ row_lse,
                    float* __restrict__ entropy, int32_t* __restrict__ top_ids,
                    float* __restrict__ top_lp) {
   constexpr int kN = Vec<T>::kN;
-  constexpr int kBatch = 4;  // groups in flight per thread
+  constexpr int kBatch = 8;  // groups in flight per thread
   __shared__ LpSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster_nctarank(), rank = (int)cluster_ctarank();
@@ -260,6 +273,14 @@ __global__ void __launch_bounds__(kThreads, 5)
   // rank 0 also takes the logits around the groups
   const int loose = rank == 0 ? span.loose(V) : 0;
 
+  // the given token of a thread, on its way while the row is read
+  int token = -1;
+  float given = 0.f;
+  if (rank == 0 && tid < n) {
+    token = tokens[out * n + tid];
+    if (token >= 0 && token < V) given = ElemIO<T>::get(row, token);
+    else token = -1;
+  }
   float ref = neg_inf(), refz = 0.f, mx = neg_inf();
   float2 s2 = make_float2(0.f, 0.f), a2 = make_float2(0.f, 0.f);
   const float2 kt2 = make_float2(kt, kt);
@@ -327,12 +348,25 @@ __global__ void __launch_bounds__(kThreads, 5)
     sm.rs[warp] = t.s;
     sm.ra[warp] = t.a;
   }
-  if (kTop) {
-    sm.key[tid] = order_key(mx);
-    if (tid == 0) {
-      sm.tau = 0u;
-      sm.nflag = sm.ncand = 0;
-    }
+  const uint32_t mine = kTop ? order_key(mx) : 0u;
+  // how the alternatives' bound is found: the top-th of the warps' `each` largest
+  // maxima together (at most 32), or the smallest of the warps' each-th
+  const int busy = min(kWarps, (g1 - g0) / 32);
+  const bool few = busy > 0 && top <= 32 / busy * busy;
+  const int each = busy == 0 ? 0 : (few ? 32 / busy : (top + busy - 1) / busy);
+  if constexpr (kTop) {
+    // the warps' largest maxima, lanes dropping out one by one (only warps in which
+    // every lane has logits; a part without one is selected exactly)
+    uint32_t left = mine, rth = 0u;
+    if (warp < busy)
+      for (int i = 0; i < each; ++i) {
+        rth = __reduce_max_sync(0xffffffffu, left);
+        const uint32_t who = __ballot_sync(0xffffffffu, left == rth);
+        if (lane == __ffs(who) - 1) left = 0u;
+        if (few && lane == 0) sm.tau[warp * each + i] = rth;
+      }
+    if (!few && lane == 0) sm.tau[warp] = warp < busy ? rth : 0xFFFFFFFFu;
+    if (tid == 0) sm.nflag = sm.ncand = 0;
   }
   __syncthreads();
   if (tid == 0) {
@@ -343,17 +377,21 @@ __global__ void __launch_bounds__(kThreads, 5)
     sm.a = all.a;
   }
   if constexpr (kTop) {
-    // the bound: the top-th largest of the threads' maxima
-    const uint32_t mine = sm.key[tid];
-    int rk = 0;
-#pragma unroll 8
-    for (int j = 0; j < kThreads; ++j) {
-      const uint32_t kj = sm.key[j];
-      rk += (kj > mine || (kj == mine && j < tid)) ? 1 : 0;
+    uint32_t tau = 0u;
+    if (few) {
+      const uint32_t e = lane < busy * each ? sm.tau[lane] : 0u;
+      int ahead = 0;
+#pragma unroll
+      for (int o = 0; o < 32; ++o) {
+        const uint32_t x = __shfl_sync(0xffffffffu, e, o);
+        ahead += x > e || (x == e && o < lane) ? 1 : 0;
+      }
+      tau = __shfl_sync(0xffffffffu, e, __ffs(__ballot_sync(0xffffffffu, ahead == top - 1)) - 1);
+    } else if (each > 0 && each <= 32) {
+      tau = sm.tau[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) tau = min(tau, sm.tau[w]);
     }
-    if (rk == top - 1) sm.tau = mine;
-    __syncthreads();
-    const uint32_t tau = sm.tau;
     constexpr uint32_t kNegInf = 0x007FFFFFu;  // order_key(-inf)
     bool exact = tau <= kNegInf;
     if (!exact) {
@@ -363,24 +401,36 @@ __global__ void __launch_bounds__(kThreads, 5)
         const uint32_t key = order_key(ElemIO<T>::get(row, x));
         if (key >= tau) {
           const int p = atomicAdd(&sm.ncand, 1);
-          if (p < kCandCap) sm.cand[p] = Cand{key, x};
+          if (p < kCandCap) sm.cand[p] = make_cand(key, x);
         }
       }
       __syncthreads();
-      const int nf = sm.nflag;
-      for (int f = warp; f < nf; f += kWarps)
-        for (int gg = g0 + sm.flag[f] + lane * kThreads; gg < g1; gg += 32 * kThreads) {
-          float v[kN];
-          Vec<T>::get(vec[gg], v);
+      const int per_thread = (g1 - g0 + kThreads - 1) / kThreads;
+      const int items = sm.nflag * per_thread;
+      for (int i0 = tid; i0 < items; i0 += kAgain * kThreads) {
+        uint4 raw[kAgain];
+        int where[kAgain];
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const uint32_t key = order_key(v[i]);
+        for (int q = 0; q < kAgain; ++q) {
+          const int i = i0 + q * kThreads, f = i / per_thread;
+          where[q] = i < items ? g0 + sm.flag[f] + (i - f * per_thread) * kThreads : g1;
+          if (where[q] < g1) raw[q] = vec[where[q]];
+        }
+#pragma unroll
+        for (int q = 0; q < kAgain; ++q) {
+          if (where[q] >= g1) continue;
+          float v[kN];
+          Vec<T>::get(raw[q], v);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) {
+            const uint32_t key = order_key(v[e]);
             if (key >= tau) {
               const int p = atomicAdd(&sm.ncand, 1);
-              if (p < kCandCap) sm.cand[p] = Cand{key, span.head + gg * kN + i};
+              if (p < kCandCap) sm.cand[p] = make_cand(key, span.head + where[q] * kN + e);
             }
           }
         }
+      }
       __syncthreads();
       exact = sm.ncand > kCandCap;
     }
@@ -399,68 +449,64 @@ __global__ void __launch_bounds__(kThreads, 5)
           [&](int i) { return ElemIO<T>::get(row, place(i)); }, place);
     }
     const int nc = sm.ncand;
+    if (tid == 0 && (nc & 1)) sm.cand[nc] = 0;  // (nc = kCandCap is even)
+    for (int j = tid; j < top; j += kThreads) sm.best[j] = 0;
+    __syncthreads();
+    const ulonglong2* two = reinterpret_cast<const ulonglong2*>(sm.cand);
     for (int i = tid; i < nc; i += kThreads) {
       const Cand c = sm.cand[i];
       int r = 0;
-      for (int j = 0; j < nc; ++j) r += ahead(sm.cand[j], c) ? 1 : 0;
+#pragma unroll 8
+      for (int j = 0; j < (nc + 1) / 2; ++j) {
+        const ulonglong2 o = two[j];
+        r += (o.x > c) + (o.y > c);
+      }
       if (r < top) sm.best[r] = c;
     }
-    if (tid == 0) sm.ntop = min(nc, top);
   }
   __syncthreads();
 
   Sums all{sm.m, sm.s, sm.a};
   if (C > 1) {
+    // every part into rank 0's shared memory: its sums, and its list beside the others'
+    // (at most kMaxCluster kMaxTop entries: the candidates' own space, which each CTA
+    // has finished with when all have arrived)
     cluster_sync();
-    if (rank == 0) {
-      if (warp == 0) {
-        Sums x{neg_inf(), 0.f, 0.f};
-        if (lane < C) {
-          x.m = ld_dsmem_f32(mapa(smem_u32(&sm.m), lane));
-          x.s = ld_dsmem_f32(mapa(smem_u32(&sm.s), lane));
-          x.a = ld_dsmem_f32(mapa(smem_u32(&sm.a), lane));
-        }
-#pragma unroll
-        for (int o = kMaxCluster / 2; o > 0; o >>= 1)
-          x = join(x, Sums{__shfl_xor_sync(0xffffffffu, x.m, o), __shfl_xor_sync(0xffffffffu, x.s, o),
-                           __shfl_xor_sync(0xffffffffu, x.a, o)});
-        if (lane == 0) {
-          sm.rm[0] = x.m;
-          sm.rs[0] = x.s;
-          sm.ra[0] = x.a;
-        }
-      }
-      if (kTop) {
-        // the parts' lists side by side (at most kMaxCluster kMaxTop entries)
-        for (int i = tid; i < C * top; i += kThreads) {
-          const int c = i / top, j = i % top;
-          Cand v{0u, -1};
-          if (j < (int)ld_dsmem_u32(mapa(smem_u32(&sm.ntop), c))) {
-            v.key = ld_dsmem_u32(mapa(smem_u32(&sm.best[j].key), c));
-            v.idx = (int)ld_dsmem_u32(mapa(smem_u32(&sm.best[j].idx), c));
-          }
-          sm.cand[i] = v;
-        }
-      }
-      __syncthreads();
-      all = Sums{sm.rm[0], sm.rs[0], sm.ra[0]};
+    if (tid == 0) {
+      st_dsmem(mapa(smem_u32(&sm.part[rank].m), 0), __float_as_uint(all.m));
+      st_dsmem(mapa(smem_u32(&sm.part[rank].s), 0), __float_as_uint(all.s));
+      st_dsmem(mapa(smem_u32(&sm.part[rank].a), 0), __float_as_uint(all.a));
     }
-    cluster_sync();  // the peers' shared memory is no longer read
-    if (rank != 0) return;
     if (kTop) {
-      const int nc = C * top;
-      if (tid == 0) sm.ntop = 0;
+      for (int j = tid; j < top; j += kThreads)
+        st_dsmem64(mapa(smem_u32(&sm.cand[rank * top + j]), 0), sm.best[j]);
+    }
+    cluster_sync();
+    if (rank != 0) return;
+    all = sm.part[0];
+    for (int c = 1; c < C; ++c) all = join(all, sm.part[c]);
+    if (kTop) {
+      // a candidate's place: its own in its list, and in every other list the number
+      // ahead of it (binary searches side by side)
+      for (int j = tid; j < top; j += kThreads) sm.best[j] = 0;
       __syncthreads();
-      for (int i = tid; i < nc; i += kThreads) {
+      int most = 1;
+      while (2 * most <= top) most *= 2;
+      for (int i = tid; i < C * top; i += kThreads) {
         const Cand c = sm.cand[i];
-        if (c.idx < 0) continue;
+        if (c == 0) continue;
+        int at[kMaxCluster];
+#pragma unroll
+        for (int l = 0; l < kMaxCluster; ++l) at[l] = 0;
+        for (int step = most; step > 0; step >>= 1)
+#pragma unroll
+          for (int l = 0; l < kMaxCluster; ++l)
+            if (l < C && at[l] + step <= top && sm.cand[l * top + at[l] + step - 1] > c)
+              at[l] += step;
         int r = 0;
-        for (int j = 0; j < nc; ++j)
-          r += sm.cand[j].idx >= 0 && ahead(sm.cand[j], c) ? 1 : 0;
-        if (r < top) {
-          sm.best[r] = c;
-          atomicAdd(&sm.ntop, 1);
-        }
+#pragma unroll
+        for (int l = 0; l < kMaxCluster; ++l) r += at[l];
+        if (r < top) sm.best[r] = c;
       }
       __syncthreads();
     }
@@ -468,19 +514,14 @@ __global__ void __launch_bounds__(kThreads, 5)
   // (a row of nothing but -inf: reference 0, S = 0, lse = -inf)
   const float m = all.m == neg_inf() ? 0.f : all.m;
   const float ls = log2f(all.s);
-  for (int j = tid; j < n; j += kThreads) {
-    const int x = tokens[out * n + j];
-    float lp = 0.f;
-    if (x >= 0 && x < V) lp = kLn2 * (fmaf(ElemIO<T>::get(row, x), kt, -m) - ls);
-    logprob[out * n + j] = lp;
-  }
+  if (tid < n) logprob[out * n + tid] = token >= 0 ? kLn2 * (fmaf(given, kt, -m) - ls) : 0.f;
   if (kTop) {
     for (int j = tid; j < top; j += kThreads) {
-      const bool have = j < sm.ntop;
-      const int x = have ? sm.best[j].idx : -1;
-      top_ids[out * top + j] = x;
+      const Cand c = sm.best[j];
+      const bool have = c != 0;
+      top_ids[out * top + j] = have ? cand_idx(c) : -1;
       top_lp[out * top + j] =
-          have ? kLn2 * (fmaf(ElemIO<T>::get(row, x), kt, -m) - ls) : __int_as_float(0x7fffffff);
+          have ? kLn2 * (fmaf(key_value(cand_key(c)), kt, -m) - ls) : __int_as_float(0x7fffffff);
     }
   }
   if (tid == 0) {
@@ -628,11 +669,11 @@ cudaError_t launch_lp_t(bool ent, bool with_top, const void* logits, int64_t ld,
            top_lp, C, st);
 }
 
-// CTAs per row.  Rows that fill the GPU take one each; fewer are split so that
-// about two CTAs run on every SM, down to parts of 8 KB.
+// CTAs per row.  Rows that fill the GPU take one each; fewer are split until about as
+// many CTAs run as fit (four on each of 152 SMs), down to parts of 8 KB.
 int row_ctas(int M, int V, int el) {
   int C = 1;
-  while (C < kMaxCluster && (int64_t)M * C < 304 && (int64_t)V * el / (2 * C) >= 8192) C *= 2;
+  while (C < kMaxCluster && (int64_t)M * C * 2 <= 608 && (int64_t)V * el / (2 * C) >= 8192) C *= 2;
   return C;
 }
 
