@@ -27,6 +27,7 @@ namespace sv {
 namespace {
 
 constexpr int kMaxPrefixes = SPEC_MAX_PREFIXES;
+static_assert(kTaCtas <= 256, "the join's threads find the cut units");
 constexpr int kMinSteps = 2;     // steps of a piece, at least
 
 struct SharedHead {  // the unit that begins in a piece and ends in a later one
@@ -409,58 +410,97 @@ struct SharedWalkD : SharedWalk {
   }
 };
 
-// Joins the pieces of cut units: CTA (piece in which the unit begins, 8 head dims),
-// thread (tile, row).
-template <int D>
-__global__ void __launch_bounds__(2 * kRows)
-    shared_join(SharedPart part, int tpt, int G, int Hq, uint16_t* __restrict__ out,
+// Joins the pieces of cut units: CTA (cut unit, 8 head dims), thread (share of the pieces,
+// tile, row).  All partial results of a row are weighted against one reference, so their
+// sums over the shares (and over the tiles that hold the same rows) simply add up.
+// Every thread has kAhead pieces' loads in flight, the first before the references are
+// exchanged.  With few units of many pieces latency is what it costs, and two shares of
+// four loads at a time are quickest (8 units of 19 pieces: 13 us with one share, one load
+// at a time; 7 now); with many units of two or three pieces it is the CTAs' number, and
+// two shares of 512 threads would take 23 us more than one (128 units).
+template <int D, int kShares, int kAhead>
+__global__ void __launch_bounds__(kShares * 2 * kRows)
+    shared_join(SharedPart part, int pieces, int tpt, int G, int Hq, uint16_t* __restrict__ out,
                 float* __restrict__ lse) {
-  __shared__ float other[10][kRows];
+  constexpr int kGroups = 2 * kShares;
+  __shared__ float top[kGroups][kRows], sum[kGroups][9][kRows];
+  __shared__ int cut, before[8];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int r = tid % kRows, group = tid / kRows, t = group & 1, share = group >> 1;
   grid_dependency_wait();
-  const SharedHead u = part.head[blockIdx.x];
-  if (u.slot < 0) return;
-  const int t = threadIdx.x / kRows, r = threadIdx.x % kRows;
-  auto place = [&](int c) { return ((int64_t)c * 2 + (c == (int)blockIdx.x ? u.slot : 0)) * 2 + t; };
+  // the blockIdx.x-th piece in which a cut unit begins
+  bool have = false;
+  if (tid < 256) {  // (a thread per piece)
+    have = tid < pieces && part.head[tid].slot >= 0;
+    const uint32_t b = __ballot_sync(0xffffffffu, have);
+    if (lane == 0) before[tid >> 5] = __popc(b);
+    if (tid == 0) cut = -1;
+    __syncthreads();
+    int n = __popc(b & ((1u << lane) - 1u));
+    for (int w = 0; w < tid >> 5; ++w) n += before[w];
+    if (have && n == (int)blockIdx.x) cut = tid;
+  } else {
+    __syncthreads();
+  }
+  __syncthreads();
+  const int c0 = cut;
+  if (c0 < 0) return;
+  const SharedHead u = part.head[c0];
+  auto place = [&](int c) { return ((int64_t)c * 2 + (c == c0 ? u.slot : 0)) * 2 + t; };
   float M = neg_inf();
 #pragma unroll 8
-  for (int c = blockIdx.x; c <= u.last; ++c) M = fmaxf(M, part.ml[place(c) * kRows + r].x);
+  for (int c = c0 + share; c <= u.last; c += kShares) M = fmaxf(M, part.ml[place(c) * kRows + r].x);
   float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const float ref = M == neg_inf() ? 0.f : M;
-#pragma unroll 4
-  for (int c = blockIdx.x; c <= u.last; ++c) {
-    const int64_t s = place(c);
-    const float2 ml = part.ml[s * kRows + r];
-    const float4* src = part.o + (s * (D / 4) + 2 * blockIdx.y) * kRows + r;
-    const float4 x = src[0], y = src[kRows];
-    // (a piece that saw something keeps a positive weight: infinite values stay)
-    const float w = ml.x == neg_inf() ? (ml.y == 0.f ? 0.f : 1.f) : fmaxf(ex2(ml.x - ref), FLT_MIN);
-    l = fmaf(ml.y, w, l);
-    o[0] = fmaf(x.x, w, o[0]); o[1] = fmaf(x.y, w, o[1]);
-    o[2] = fmaf(x.z, w, o[2]); o[3] = fmaf(x.w, w, o[3]);
-    o[4] = fmaf(y.x, w, o[4]); o[5] = fmaf(y.y, w, o[5]);
-    o[6] = fmaf(y.z, w, o[6]); o[7] = fmaf(y.w, w, o[7]);
-  }
-  if (u.both) {  // the two tiles hold the same rows
-    if (t == 1) {
-      other[0][r] = M;
-      other[1][r] = l;
+  float2 ml[kAhead];
+  float4 x[kAhead], y[kAhead];
+  auto load = [&](int c) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) other[2 + i][r] = o[i];
+    for (int i = 0; i < kAhead; ++i) {
+      ml[i] = make_float2(neg_inf(), 0.f);
+      x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + kShares * i > u.last) continue;
+      const int64_t s = place(c + kShares * i);
+      const float4* src = part.o + (s * (D / 4) + 2 * blockIdx.y) * kRows + r;
+      ml[i] = part.ml[s * kRows + r];
+      x[i] = src[0];
+      y[i] = src[kRows];
     }
-    __syncthreads();
-    if (t == 1) return;
-    const float m1 = other[0][r], m = fmaxf(M, m1);
-    const float rf = m == neg_inf() ? 0.f : m;
-    const float w0 = M == neg_inf() ? (l == 0.f ? 0.f : 1.f) : fmaxf(ex2(M - rf), FLT_MIN);
-    const float w1 = m1 == neg_inf() ? (other[1][r] == 0.f ? 0.f : 1.f)
-                                     : fmaxf(ex2(m1 - rf), FLT_MIN);
-    l = l * w0 + other[1][r] * w1;
+  };
+  load(c0 + share);
+  top[group][r] = M;
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * w0 + other[2 + i][r] * w1;
-    M = m;
+  for (int g = 0; g < kGroups; ++g)
+    if (u.both || (g & 1) == t) M = fmaxf(M, top[g][r]);
+  const float ref = M == neg_inf() ? 0.f : M;
+  for (int c = c0 + share; c <= u.last; c += kShares * kAhead) {
+    if (c != c0 + share) load(c);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      // (a piece that saw something keeps a positive weight: infinite values stay)
+      const float w = ml[i].x == neg_inf() ? (ml[i].y == 0.f ? 0.f : 1.f)
+                                           : fmaxf(ex2(ml[i].x - ref), FLT_MIN);
+      l = fmaf(ml[i].y, w, l);
+      o[0] = fmaf(x[i].x, w, o[0]); o[1] = fmaf(x[i].y, w, o[1]);
+      o[2] = fmaf(x[i].z, w, o[2]); o[3] = fmaf(x[i].w, w, o[3]);
+      o[4] = fmaf(y[i].x, w, o[4]); o[5] = fmaf(y[i].y, w, o[5]);
+      o[6] = fmaf(y[i].z, w, o[6]); o[7] = fmaf(y[i].w, w, o[7]);
+    }
   }
+  sum[group][8][r] = l;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[group][i][r] = o[i];
+  __syncthreads();
+  if (share > 0 || (u.both && t == 1)) return;
   const int tok = r / G, i = (u.both ? 0 : t * tpt) + tok;
   if (tok >= tpt || i >= u.ntok) return;
+#pragma unroll
+  for (int g = 1; g < kGroups; ++g)
+    if (g != t && (u.both || (g & 1) == t)) {
+      l += sum[g][8][r];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += sum[g][e][r];
+    }
   const int64_t row = (int64_t)(u.tok0 + i) * Hq + u.h * G + r % G;
   const float mul = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint4*>(out + row * D + 8 * blockIdx.y) =
@@ -472,6 +512,7 @@ __global__ void __launch_bounds__(2 * kRows)
 // Sizes of a call: how rows are packed, and how many pieces the line can have.
 struct SharedPlan {
   int G, tpt, spu, chunks, pieces;
+  int cuts;  // units that can be cut, at most
   size_t off_ml, off_o, bytes;
 };
 bool shared_sizes_ok(int B, int N, int Hq, int Hkv, int groups, int Sp, int S) {
@@ -492,6 +533,8 @@ SharedPlan shared_plan(int B, int N, int Hq, int Hkv, int D, int groups, int Sp,
                                (int64_t)B * s.chunks * ((S + kKeys - 1) / kKeys));
   const int64_t most = (steps + kMinSteps - 1) / kMinSteps;
   s.pieces = (int)(most < 1 ? 1 : (most < kTaCtas ? most : kTaCtas));
+  const int64_t units = tiles * Hkv;
+  s.cuts = (int)(units < s.pieces - 1 ? units : s.pieces - 1);
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   s.off_ml = up((size_t)s.pieces * sizeof(SharedHead));
   s.off_o = s.off_ml + up((size_t)s.pieces * 4 * kRows * sizeof(float2));
@@ -511,17 +554,19 @@ int launch(const SharedWalk::Params& prm, const SharedPlan& plan, cudaStream_t s
   if (allow_smem((const void*)kernel, (int)smem, done) != cudaSuccess) return SPEC_ERR_CUDA;
   kernel<<<plan.pieces, kTaThreads, smem, st>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return SPEC_ERR_CUDA;
-  if (plan.pieces == 1) return SPEC_OK;  // nothing is cut
+  if (plan.cuts == 0) return SPEC_OK;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)plan.pieces, D / 8);
-  cfg.blockDim = dim3(2 * kRows);
+  cfg.gridDim = dim3((unsigned)plan.cuts, D / 8);
+  const bool many = plan.pieces >= 4 * plan.cuts;  // pieces of a unit
+  cfg.blockDim = dim3((many ? 4 : 2) * kRows);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_join<D>, prm.part, prm.tpt, prm.G, prm.Hq, prm.out,
+  auto join = many ? shared_join<D, 2, 4> : shared_join<D, 1, 2>;
+  return cudaLaunchKernelEx(&cfg, join, prm.part, plan.pieces, prm.tpt, prm.G, prm.Hq, prm.out,
                             prm.lse) == cudaSuccess
              ? SPEC_OK
              : SPEC_ERR_CUDA;

@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               const float mnew = bm > mref + 8.f ? bm : mref;
               if (mref != neg_inf()) corr = ex2(mref - mnew);
               mref = mnew;
-              if (any || h > 0) {
+              // (rows that have seen nothing hold zeros)
+              if (__any_sync(0xffffffffu, corr != 1.f)) {
                 // the P V of the half step before must be done (that of the one before
                 // it is: it was issued before these scores)
                 await(sm, &sm.pvdone[t], (h + 1) & 1u);
