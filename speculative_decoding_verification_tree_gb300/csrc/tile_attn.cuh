@@ -10,23 +10,34 @@
 //
 //   warp 0      producer: K and V of each step (TMA, 128-byte swizzle) into rings of
 //               tiles, Q of each unit as a box of tokens x G heads;
-//   warps 1-2   tile t's issuer of O_t += P_t V (of the step before) and S_t = Q_t K^T
-//               (tcgen05.mma M 128, float32 in TMEM), so that one tile's products run
-//               while the other's softmax does;
+//   warps 1-2   tile t's issuer of S_t = Q_t K^T and O_t += P_t V (tcgen05.mma M 128,
+//               float32 in TMEM); the whole warp runs its loop and one elected lane issues
+//               (8192 tokens, 32 / 8 heads, D 128, one issuer for both tiles: 537 us when a
+//               lone thread runs it, whose operands the compiler cannot know to be
+//               uniform, 456 this way);
 //   warp 3      every V tile on its way to the products: rows behind the last key
 //               become zeros, and in steps that some row does not see in full so do
 //               NaN and infinite elements (0 times them would reach rows that do not
 //               see them; rows that do see them get them back at the end);
-//   warps 4-19  softmax, two threads per row with 64 keys of a step each: S from TMEM,
-//               online base-2 softmax against a reference maximum that moves only when
-//               a row's maximum (exchanged through shared memory) grows by more than
-//               2^8 (O is then rescaled in TMEM), P as bf16 pairs into the TMEM columns
-//               of S; at a unit's end O / l, half of the dims each.
+//   warps 4-11  softmax, a thread per row: S from TMEM, online base-2 softmax against
+//               a reference maximum that moves only when a row's maximum grows by
+//               more than 2^8 (O is then rescaled in TMEM), P as bf16 pairs into the
+//               TMEM columns of S; at a unit's end O / l.
 //
-// TMEM (512 columns): S_t at 128 t, P_t over its first half, O_t at 256 + 128 t.
-// One issuer per tile keeps the order that this needs: S_t of a step is issued after
-// P_t V of the step before, which reads P_t from the same columns, and a commit of S_t
-// covers that P V, so a softmax warp that sees S_t may also rescale O_t.
+// A step's scores come in two halves of 64 keys, each with its own columns and its own
+// P: while the softmax works on one half, P V of the other and the next scores of the
+// other run.  With whole steps a tile's products and softmax take turns: 418 us for the
+// 8192 tokens above instead of 380, although the 64-key products read Q from shared
+// memory twice as often.  Also tried there: two softmax threads per row (16 warps, maxima
+// exchanged through shared memory: 484 us); four warps of their own for finished rows (no
+// gain at any length: registers for the softmax get scarce); registers moved from the
+// other warps to the softmax's (no gain: it needs 138).
+//
+// TMEM (512 columns): S_t's halves at 128 t and 128 t + 64, P_t over the first 32 columns
+// of each, O_t at 256 + 128 t.  One issuer per tile keeps the order that this needs:
+// S of a half is issued after P V of the same half of the step before, which reads P from
+// the same columns, and its commit covers that P V.  A softmax warp that rescales O_t waits
+// for the P V of the half before as well.
 // Sums, statistics and outputs are float32; P is rounded to bf16 for the product and
 // the output to bf16 at the end.
 //
