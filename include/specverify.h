@@ -609,6 +609,7 @@ int spec_philox_uniforms(uint64_t seed, uint32_t offset, const int32_t* b,
  *   prefix_len [B] int32 (clamped to [0, S - N]; shared_len to [0, Sp]);
  *   mask_bits [B, N] uint64.
  * lse [B, N, Hq] float32 (out, may be NULL): the rows' base-2 log normalisers.
+ * out, lse and the workspace must not overlap the inputs or one another.
  * Sequences outside every group are not written.  A row that sees nothing gives
  * zeros and lse = -inf (a key whose score is -inf counts as not seen).  What cache
  * positions behind shared_len or prefix_len + N hold does not matter, and NaN or
@@ -657,7 +658,8 @@ int spec_tree_attention_shared(const void* q, const void* k_prefix,
  *   gets the result of either.
  * lse [T, Hq] float32 (out, may be NULL): the rows' base-2 log normalisers, as
  *   spec_tree_attention_lse writes them.
- * Tokens outside every prompt are not written.  Empty prompts are fine.
+ * Tokens outside every prompt are not written.  Empty prompts are fine.  out and
+ *   lse must not overlap the inputs or one another.
  * Softmax and accumulation in float32, weights rounded to bf16 for the second
  * product, the output to bf16.  A token's NaN or infinite key or value reaches
  * its own and later tokens of its prompt only.  Deterministic.

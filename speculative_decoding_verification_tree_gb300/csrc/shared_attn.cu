@@ -216,8 +216,8 @@ struct SharedWalk {
     if (p0 < line && mine <= want && want < mine + v) {
       int64_t x = mine;
       int i = first;
-      for (;; ++i) {
-        const int64_t s = per > 1 ? steps(i) : v;
+      for (; i + 1 < last; ++i) {
+        const int64_t s = steps(i);
         if (want < x + s) break;
         x += s;
       }

@@ -246,20 +246,27 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       uint32_t n = 0, upar = 0;  // steps; parity of each Q tile's next wait
+      uint32_t nk = 0, nv = 0;   // copies begun
+      // whether stage s may be filled (once a wait has given up, nothing is copied any
+      // more: copies without waits would pile up on a barrier)
       auto slot = [&](int s, uint32_t fill) {
         await(sm, &sm.empty[s], (fill & 1u) ^ 1u);
+        if (*(volatile uint32_t*)&sm.dead) return false;
         mbar_expect_tx(&sm.full[s], (uint32_t)Geo::kTile);
-        return s;
+        return true;
       };
       while (w.next_unit()) {
         bool first = true;
         while (w.next_step()) {
           if (lane == 0) {
-            const int s = slot((int)(n % kKs), n / kKs);
-            const uint32_t dst = base + Geo::kOffRing + (uint32_t)(s * Geo::kTile);
+            const int s = (int)(n % kKs);
+            if (slot(s, n / kKs)) {
+              const uint32_t dst = base + Geo::kOffRing + (uint32_t)(s * Geo::kTile);
 #pragma unroll
-            for (int h = 0; h < Geo::kHalves; ++h)
-              w.load_k(dst + h * Geo::kHalf, 64 * h, &sm.full[s]);
+              for (int h = 0; h < Geo::kHalves; ++h)
+                w.load_k(dst + h * Geo::kHalf, 64 * h, &sm.full[s]);
+              ++nk;
+            }
           }
           if (first) {  // (after the first keys: they need no wait for the unit before)
             first = false;
@@ -268,6 +275,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
               for (int t = 0; t < 2; ++t) {
                 if (!((w.have >> t) & 1u)) continue;
                 await(sm, &sm.qempty[t], ((upar >> t) & 1u) ^ 1u);
+                if (*(volatile uint32_t*)&sm.dead) continue;
                 mbar_expect_tx(&sm.qfull[t], w.q_bytes() * Geo::kHalves);
 #pragma unroll
                 for (int h = 0; h < Geo::kHalves; ++h)
@@ -278,11 +286,14 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             upar ^= w.have;
           }
           if (lane == 0) {
-            const int s = slot(kKs + (int)(n % kVs), n / kVs);
-            const uint32_t dst = base + Geo::kOffRing + (uint32_t)(s * Geo::kTile);
+            const int s = (int)(n % kVs);
+            if (slot(kKs + s, n / kVs)) {
+              const uint32_t dst = base + Geo::kOffRing + (uint32_t)((kKs + s) * Geo::kTile);
 #pragma unroll
-            for (int h = 0; h < Geo::kHalves; ++h)
-              w.load_v(dst + h * Geo::kHalf, 64 * h, &sm.full[s]);
+              for (int h = 0; h < Geo::kHalves; ++h)
+                w.load_v(dst + h * Geo::kHalf, 64 * h, &sm.full[kKs + s]);
+              ++nv;
+            }
           }
           ++n;
           __syncwarp();
@@ -290,10 +301,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       }
       // this CTA's last copy into each stage has landed before it exits
       if (lane == 0) {
-        for (uint32_t s = 0; s < (uint32_t)kKs && s < n; ++s)
-          mbar_wait_bounded(&sm.full[s], ((n - s - 1) / kKs) & 1u);
-        for (uint32_t s = 0; s < (uint32_t)kVs && s < n; ++s)
-          mbar_wait_bounded(&sm.full[kKs + s], ((n - s - 1) / kVs) & 1u);
+        for (uint32_t s = 0; s < (uint32_t)kKs && s < nk; ++s)
+          mbar_wait_bounded(&sm.full[s], ((nk - s - 1) / kKs) & 1u);
+        for (uint32_t s = 0; s < (uint32_t)kVs && s < nv; ++s)
+          mbar_wait_bounded(&sm.full[kKs + s], ((nv - s - 1) / kVs) & 1u);
       }
     } else if (warp <= 2) {
       // ------------------------------------------------- tile t's issuer
@@ -352,7 +363,6 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       while (w.next_unit()) {
         const bool have = (w.have >> t) & 1u;
         bool started = false;
-        if (have) await(sm, &sm.qfull[t], qpar);
         while (w.next_step()) {
           const bool act = (w.act >> t) & 1u;
           auto give_k = [&]() {
@@ -367,6 +377,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           if (pend) put_pv(0);
           if (act) {
             await(sm, &sm.full[n % kKs], (n / kKs) & 1u);
+            // (not before the unit before is settled: its rows wait for that)
+            if (!started) await(sm, &sm.qfull[t], qpar);
             put_s(0);
           }
           if (pend) {
@@ -385,6 +397,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           ++n;
         }
         if (have) {
+          if (!started) await(sm, &sm.qfull[t], qpar);
           if (elect_one()) mma_commit(&sm.qempty[t]);
           __syncwarp();
           qpar ^= 1u;
@@ -560,7 +573,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
       gave_up |= blockIdx.x == 0;
 #endif
       if (gave_up) l = __int_as_float(0x7fffffff);
-      const bool bad = *(volatile uint32_t*)&sm.bad != 0;
+      // (one answer for the warp: the next unit's tiles may be under way)
+      const bool bad = __any_sync(0xffffffffu, *(volatile uint32_t*)&sm.bad != 0);
       w.begin_finish(row, t, mref, l);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {

@@ -186,6 +186,32 @@ def test_nan_and_infinity_reach_later_tokens_only(D):
     assert torch.isfinite(out[300:]).all()
 
 
+@pytest.mark.parametrize("D", [128, 64])
+def test_many_nan_values_over_many_units(D):
+    """Scattered NaN values in prompts of many units: each reaches its own and
+    later tokens of its prompt, in its head's column, while CTAs go on to their
+    next units."""
+    lens, Hkv = [3000, 1, 700, 2500, 64], 8
+    T = sum(lens)
+    q, k, v = make(T, 16, Hkv, D, seed=12)
+    rng = np.random.default_rng(12)
+    at = (rng.integers(0, T, 400), rng.integers(0, Hkv, 400),
+          rng.integers(0, D, 400))
+    at = tuple(torch.from_numpy(x).cuda() for x in at)
+    starts = np.concatenate([[0], np.cumsum(lens)])
+    v[at] = 0
+    base, lse0 = api().spec_prompt_attention(q, k, v, i32(starts), lse=True)
+    v[at] = float("nan")
+    out, lse = api().spec_prompt_attention(q, k, v, i32(starts), lse=True)
+    assert torch.equal(lse, lse0)
+    hit = torch.isnan(v)                            # [T, Hkv, D]
+    for a, z in zip(starts, starts[1:]):
+        hit[a:z] = hit[a:z].cumsum(0) > 0
+    hit = hit.repeat_interleave(2, 1)
+    assert torch.isnan(out[hit]).all()
+    assert torch.equal(out[~hit], base[~hit])
+
+
 def test_rows_past_2_31_elements():
     """600 K tokens of 32 heads: q and out pass 2^31 elements."""
     n, L = 2350, 257
