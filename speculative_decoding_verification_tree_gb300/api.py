@@ -474,6 +474,23 @@ def _alloc(shape, dtype, dev, stream, make=torch.empty):
         return make(shape, dtype=dtype, device=dev)
 
 
+def _output(t, shape, dtype, dev, stream, name):
+    """An output and its address: the caller's tensor after the checks of _arg,
+    or a new one."""
+    if t is not None:
+        return t, _arg(t, dtype, shape, dev, name)
+    t = _alloc(shape, dtype, dev, stream)
+    return t, t.data_ptr()
+
+
+def _lse_output(lse, shape, dev, stream):
+    """Normalisers asked for by True, given as a tensor, or not wanted."""
+    if lse is False or lse is None:
+        return None, None
+    return _output(None if lse is True else lse, shape, torch.float32, dev,
+                   stream, "lse")
+
+
 def _enqueue(name, dev, stream, *args):
     """Call an entry point (without its last argument, the stream) on
     cuda:`dev`."""
@@ -690,24 +707,15 @@ def spec_tree_attention_shared(q, k_prefix, v_prefix, shared_len, group_start,
             _arg(v_cache, bf, own, dev, "v_cache"),
             _arg(prefix_len, i32, (B,), dev, "prefix_len"),
             _arg(mask_bits, torch.int64, (B, N), dev, "mask_bits"))
-    if out is None:
-        out = _alloc(shape, bf, dev, stream)
-    if lse is True:
-        lse = _alloc((B, N, Hq), torch.float32, dev, stream)
-    elif lse is False:
-        lse = None
-    if ws is None:
-        nbytes = _shared_workspace_bytes(B, N, Hq, Hkv, D, groups, Sp, S)
-        ws = _alloc(nbytes, torch.uint8, dev, stream)
-    else:
-        nbytes = ws.numel()
+    out, oa = _output(out, shape, bf, dev, stream, "out")
+    lse, la = _lse_output(lse, (B, N, Hq), dev, stream)
+    nbytes = (_shared_workspace_bytes(B, N, Hq, Hkv, D, groups, Sp, S)
+              if ws is None else ws.numel())
+    _, wa = _output(ws, (nbytes,), torch.uint8, dev, stream, "ws")
     if scale is None:
         scale = D ** -0.5
     _enqueue("spec_tree_attention_shared", dev, stream, *args, B, N, Hq, Hkv,
-             D, groups, Sp, S, scale, _arg(out, bf, shape, dev, "out"),
-             None if lse is None else _arg(lse, torch.float32, (B, N, Hq), dev,
-                                           "lse"),
-             _arg(ws, torch.uint8, (nbytes,), dev, "ws"), nbytes)
+             D, groups, Sp, S, scale, oa, la, wa, nbytes)
     return out, lse
 
 
@@ -742,18 +750,12 @@ def spec_prompt_attention(q, k, v, seq_start, *, scale=None, lse=False,
     args = (*_packed(q, Hq, T, D, dev, "q"), *_packed(k, Hkv, T, D, dev, "k"),
             *_packed(v, Hkv, T, D, dev, "v"),
             _arg(seq_start, torch.int32, (B + 1,), dev, "seq_start"))
-    if out is None:
-        out = _alloc((T, Hq, D), torch.bfloat16, dev, stream)
-    if lse is True:
-        lse = _alloc((T, Hq), torch.float32, dev, stream)
-    elif lse is False:
-        lse = None
+    out, oa = _output(out, (T, Hq, D), torch.bfloat16, dev, stream, "out")
+    lse, la = _lse_output(lse, (T, Hq), dev, stream)
     if scale is None:
         scale = D ** -0.5
     _enqueue("spec_prompt_attention", dev, stream, *args, B, T, Hq, Hkv, D,
-             scale, _arg(out, torch.bfloat16, (T, Hq, D), dev, "out"),
-             None if lse is None else _arg(lse, torch.float32, (T, Hq), dev,
-                                           "lse"))
+             scale, oa, la)
     return out, lse
 
 
