@@ -41,7 +41,8 @@ struct PromptWalk {
   };
   struct Shared {
     int most;              // units of the longest prompt
-    int tiles[kLevelMax]; // units of each prompt, per key/value head
+    int tiles[kLevelMax];  // units of each prompt, per key/value head
+    int starts[kLevelMax + 1];  // (of at most kLevelMax prompts)
   };
 
   const Params& p;
@@ -78,7 +79,9 @@ struct PromptWalk {
     if (threadIdx.x == 0) sh.most = 0;
     __syncthreads();
     if (p.B <= kLevelMax)
-      for (int b = threadIdx.x; b < p.B; b += kTaThreads) {
+      for (int b = threadIdx.x; b <= p.B; b += kTaThreads) {
+        sh.starts[b] = start_of(p, b);
+        if (b == p.B) break;
         const int n = tiles_of(p, b);
         sh.tiles[b] = n;
         atomicMax(&sh.most, n);
@@ -90,8 +93,9 @@ struct PromptWalk {
 
   // takes unit `tile` of prompt b, key/value head `head`
   __device__ __forceinline__ void take(int b, int tile, int head) {
-    a = start_of(p, b);
-    L = start_of(p, b + 1) - a;
+    const bool held = p.B <= kLevelMax;
+    a = held ? sh.starts[b] : start_of(p, b);
+    L = (held ? sh.starts[b + 1] : start_of(p, b + 1)) - a;
     pos0 = tile * 2 * p.tpt;
     h = head;
     have = pos0 + p.tpt < L ? 3u : 1u;
