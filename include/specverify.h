@@ -699,8 +699,12 @@ int spec_prompt_attention(const void* q, int64_t q_token, const void* k,
  *     the `top` most probable tokens, best first, equal logits by lower index
  *     (0 and -0 are equal).
  * Sums are float32; no atomics order a result, so equal calls give equal bits.
- * A logit of -inf is a token of probability 0.  A row with NaN or +inf, or with
- * nothing but -inf, has NaN log probabilities and entropy (alternatives are
+ * A logit of -inf is a token of probability 0.  Masks may also be finite, down to
+ * the type's lowest value: distances between logits are formed before they are
+ * scaled, so rows may hold logits of any size (a row of one value throughout is
+ * uniform); what passes float32's range, row_lse among them, is infinite.  A row
+ * with NaN or +inf, or with nothing but -inf, has NaN log probabilities and
+ * entropy (alternatives are
  * still ordered by logit; NaN is never one, and where numbers run out ids are
  * -1 with NaN).
  * Errors: SPEC_ERR_DTYPE; SPEC_ERR_SHAPE for sizes < 0, V outside [1,

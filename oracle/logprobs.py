@@ -14,11 +14,12 @@ import numpy as np
 
 
 def log_softmax(z, T):
-    """ln p of every token, and the natural log normaliser, row by row."""
+    """ln p of every token, and the natural log normaliser, row by row.  (The
+    maximum is taken off first: beside logits of 1e20 it would swallow ln S.)"""
     z = np.asarray(z, dtype=np.float64) / T
     m = z.max(-1, keepdims=True)
-    lse = m + np.log(np.exp(z - m).sum(-1, keepdims=True))
-    return z - lse, lse[..., 0]
+    ln = np.log(np.exp(z - m).sum(-1, keepdims=True))
+    return z - m - ln, (m + ln)[..., 0]
 
 
 def token_logprobs(z, tokens, T=1.0, top=0):

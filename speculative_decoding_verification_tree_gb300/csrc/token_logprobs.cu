@@ -2,17 +2,20 @@
 // tokens, the rows' entropy and most probable alternatives, and the gradient of
 // log probabilities and entropies with respect to the logits.
 //
-// With s_x = z_x log2(e) / T, m any reference, S = sum_x 2^(s_x - m) and
-// A = sum_x 2^(s_x - m) (s_x - m):
-//   lse = m + log2 S                      (base 2)
-//   ln p(t) = ln 2 (s_t - m - log2 S)
+// With k = log2(e) / T, m any logit of the row as reference, d_x = (z_x - m) k,
+// S = sum_x 2^d_x and A = sum_x 2^d_x d_x:
+//   lse = m k + log2 S                    (base 2)
+//   ln p(t) = ln 2 (d_t - log2 S)
 //   H = ln 2 (log2 S - A / S)
-// so one pass over a row gives all three.  A thread's reference is the maximum
-// of its first logits and moves only when a later one is above it by more than
-// a factor of 2^10: sums stay far inside float32, and moving is rare (a running
-// maximum moves in some lane of a warp at nearly every step).  Bound by reading the
-// logits once: 8192 rows of 128256 bf16 logits 299 us, 7.0 TB/s, a little above the
-// measured copy rate.
+// so one pass over a row gives all three.  The reference is kept as the logit itself
+// and subtracted before the scale: a distance is then off by a relative 2^-23 whatever
+// the logits' size, and 0 at the reference.  (z k - m k in one FMA is off by the rounding
+// of m k, which for a vocabulary masked with -1e10 is hundreds of powers of two.)  A
+// thread's reference is the maximum of its first logits and moves only when a later one
+// is above it by more than a factor of 2^10: sums stay far inside float32, and moving is
+// rare (a running maximum moves in some lane of a warp at nearly every step).  Bound by
+// reading the logits once: 8192 rows of 128256 bf16 logits 313 us, 6.7 TB/s, the measured
+// copy rate (303 with the one FMA, which is no choice).
 //
 // Alternatives: each thread also keeps its largest logit.  The top-th largest of the
 // warps' four largest of those (or, for more than 32 alternatives, the smallest of the
@@ -21,12 +24,12 @@
 // read again, from L2, and the few candidates ranked by (value, lower index).  The exact
 // top-th of the 256 maxima, by counting, cost more than it saved (224 rows of 128256, 20
 // alternatives: 26.8 us; with the smallest of the warps' third largest 28.9, for more is
-// read again; now 20.7, of which 14.3 without alternatives).  Parts where the bound leaves
+// read again; now 21.9, of which 14.3 without alternatives).  Parts where the bound leaves
 // too few or too many candidates (ties, NaN, masked vocabularies) take an exact radix
 // selection instead.
 //
 // Few rows are split over the CTAs of a cluster, joined through distributed
-// shared memory (one row of 32000 float32 logits, 5 alternatives: 7.6 us; 128: 21).
+// shared memory (one row of 32000 float32 logits, 5 alternatives: 7.8 us; 128: 21).
 //
 // Gradient: dz_x = (1/T) (sum_j g_j 1[t_j = x] - p_x (sum_j g_j + g_H (ln p_x + H))).
 // One read and one write of the row; the given tokens' own terms are put in
@@ -52,7 +55,7 @@ constexpr int kAgain = 4;  // groups of flagged threads in flight when they are 
 constexpr int kMaxCluster = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMove = 10.f;    // base-2 distance at which a reference moves
-constexpr float kFloor = -200.f; // 2^kFloor is 0: s - m of -inf becomes finite
+constexpr float kFloor = -200.f; // 2^kFloor is 0: a distance of -inf becomes finite
 
 // A NaN operand gives NaN (fmaxf would drop it).
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -140,7 +143,7 @@ __device__ __forceinline__ int cand_idx(Cand c) { return (int)(0xFFFFFFFFu - (ui
 __device__ __forceinline__ uint32_t cand_key(Cand c) { return (uint32_t)(c >> 32); }
 
 struct Sums {
-  float m, s, a;
+  float m, s, a;  // reference (a logit; -inf: none yet), S, A
 };
 struct LpSmem {
   Sums part[kMaxCluster];  // rank 0: the parts of the row
@@ -161,13 +164,14 @@ __device__ __forceinline__ void st_dsmem(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void st_dsmem64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
-__device__ __forceinline__ Sums join(Sums x, Sums y) {
+__device__ __forceinline__ Sums join(Sums x, Sums y, float kt) {
   const float m = fmaxf(x.m, y.m);
   if (m == neg_inf()) return {m, x.s + y.s, x.a + y.a};
   // a part without finite logits has s = a = 0 (or NaN); its distance is cut
   // so that 0 times it stays 0
-  const float dx = fmaxf(x.m - m, kFloor), dy = fmaxf(y.m - m, kFloor);
-  const float cx = ex2(x.m - m), cy = ex2(y.m - m);
+  const float rx = (x.m - m) * kt, ry = (y.m - m) * kt;
+  const float dx = fmaxf(rx, kFloor), dy = fmaxf(ry, kFloor);
+  const float cx = ex2(rx), cy = ex2(ry);
   return {m, x.s * cx + y.s * cy, (x.a + x.s * dx) * cx + (y.a + y.s * dy) * cy};
 }
 
@@ -248,9 +252,9 @@ template <typename T, bool kEnt, bool kTop>
 __global__ void __launch_bounds__(kThreads, 4)
     token_logprobs(const T* __restrict__ logits, int64_t ld, int R, int V,
                    const int32_t* __restrict__ rows, const int32_t* __restrict__ tokens, int n,
-                   int top, float kt, float* __restrict__ logprob, float* __restrict__ row_lse,
-                   float* __restrict__ entropy, int32_t* __restrict__ top_ids,
-                   float* __restrict__ top_lp) {
+                   int top, float kt, float invT, float move, float* __restrict__ logprob,
+                   float* __restrict__ row_lse, float* __restrict__ entropy,
+                   int32_t* __restrict__ top_ids, float* __restrict__ top_lp) {
   constexpr int kN = Vec<T>::kN;
   constexpr int kBatch = 8;  // groups in flight per thread
   __shared__ LpSmem sm;
@@ -288,25 +292,28 @@ __global__ void __launch_bounds__(kThreads, 4)
     if (token >= 0 && token < V) given = ElemIO<T>::get(row, token);
     else token = -1;
   }
-  float ref = neg_inf(), refz = 0.f, mx = neg_inf();
+  // the reference (0 while there is none: every logit was -inf or NaN) and the logit
+  // above which it moves
+  float ref = 0.f, limit = neg_inf(), mx = neg_inf();
   float2 s2 = make_float2(0.f, 0.f), a2 = make_float2(0.f, 0.f);
   const float2 kt2 = make_float2(kt, kt);
   auto move_ref = [&](float gm) {
-    const float was = ref;
-    ref = gm * kt;
-    refz = ref == neg_inf() ? 0.f : ref;
-    if (was != neg_inf()) {
-      const float d = was - ref, c = ex2(d);
+    if (limit != neg_inf()) {
+      // (what a far reference leaves is 0, not 0 times an infinite distance)
+      const float d = (ref - gm) * kt, c = ex2(d);
       if (kEnt) {
-        a2.x = (a2.x + s2.x * d) * c;
-        a2.y = (a2.y + s2.y * d) * c;
+        const float cut = fmaxf(d, kFloor);
+        a2.x = (a2.x + s2.x * cut) * c;
+        a2.y = (a2.y + s2.y * cut) * c;
       }
       s2.x *= c;
       s2.y *= c;
     }
+    ref = gm;
+    limit = gm + move;
   };
   auto pair = [&](float z0, float z1) {
-    float2 d = ffma2(make_float2(z0, z1), kt2, make_float2(-refz, -refz));
+    float2 d = fmul2(fadd2(make_float2(z0, z1), make_float2(-ref, -ref)), kt2);
     if (kEnt) {
       d.x = max_nan(d.x, kFloor);
       d.y = max_nan(d.y, kFloor);
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   for (int i = tid; i < loose; i += kThreads) {
     const float z = ElemIO<T>::get(row, span.place(i));
     if (kTop) mx = fmaxf(mx, z);
-    if (z * kt > ref + kMove || ref == neg_inf()) move_ref(z);
+    if (z > limit) move_ref(z);
     pair(z, neg_inf());
   }
   auto group = [&](const uint4& r) {
@@ -330,8 +337,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     else
       gm = fmax3f(fmaxf(v[0], v[1]), v[2], v[3]);
     if (kTop) mx = fmaxf(mx, gm);
-    // (ref = -inf: the sum is -inf and any number is above it)
-    if (gm * kt > ref + kMove) move_ref(gm);
+    if (gm > limit) move_ref(gm);
 #pragma unroll
     for (int i = 0; i < kN; i += 2) pair(v[i], v[i + 1]);
   };
@@ -345,11 +351,11 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
   for (; g < g1; g += kThreads) group(ldg_once(vec + g));
 
-  Sums t{ref, s2.x + s2.y, a2.x + a2.y};
+  Sums t{limit == neg_inf() ? neg_inf() : ref, s2.x + s2.y, a2.x + a2.y};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     t = join(t, Sums{__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.s, o),
-                     __shfl_xor_sync(0xffffffffu, t.a, o)});
+                     __shfl_xor_sync(0xffffffffu, t.a, o)}, kt);
   if (lane == 0) {
     sm.rm[warp] = t.m;
     sm.rs[warp] = t.s;
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   __syncthreads();
   if (tid == 0) {
     Sums all{sm.rm[0], sm.rs[0], sm.ra[0]};
-    for (int w = 1; w < kWarps; ++w) all = join(all, Sums{sm.rm[w], sm.rs[w], sm.ra[w]});
+    for (int w = 1; w < kWarps; ++w) all = join(all, Sums{sm.rm[w], sm.rs[w], sm.ra[w]}, kt);
     sm.m = all.m;
     sm.s = all.s;
     sm.a = all.a;
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     cluster_sync();
     if (rank != 0) return;
     all = sm.part[0];
-    for (int c = 1; c < C; ++c) all = join(all, sm.part[c]);
+    for (int c = 1; c < C; ++c) all = join(all, sm.part[c], kt);
     if (kTop) {
       // a candidate's place: its own in its list, and in every other list the number
       // ahead of it (binary searches side by side)
@@ -520,19 +526,20 @@ __global__ void __launch_bounds__(kThreads, 4)
   }
   // (a row of nothing but -inf: reference 0, S = 0, lse = -inf)
   const float m = all.m == neg_inf() ? 0.f : all.m;
-  const float ls = log2f(all.s);
-  if (tid < n) logprob[out * n + tid] = token >= 0 ? kLn2 * (fmaf(given, kt, -m) - ls) : 0.f;
+  const float ls = log2f(all.s), ln = kLn2 * ls;
+  // (by 1 / T: z - m may be as large as float32 goes)
+  if (tid < n) logprob[out * n + tid] = token >= 0 ? fmaf(given - m, invT, -ln) : 0.f;
   if (kTop) {
     for (int j = tid; j < top; j += kThreads) {
       const Cand c = sm.best[j];
       const bool have = c != 0;
       top_ids[out * top + j] = have ? cand_idx(c) : -1;
       top_lp[out * top + j] =
-          have ? kLn2 * (fmaf(key_value(cand_key(c)), kt, -m) - ls) : __int_as_float(0x7fffffff);
+          have ? fmaf(key_value(cand_key(c)) - m, invT, -ln) : __int_as_float(0x7fffffff);
     }
   }
   if (tid == 0) {
-    if (row_lse) row_lse[out] = m + ls;
+    if (row_lse) row_lse[out] = fmaf(m, kt, ls);
     if (kEnt) entropy[out] = kLn2 * (ls - all.a / all.s);
   }
 }
@@ -648,9 +655,9 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, bool kEnt, bool kTop>
 cudaError_t launch_lp(const void* logits, int64_t ld, int R, int V, const int32_t* rows, int M,
-                      const int32_t* tokens, int n, int top, float kt, float* logprob,
-                      float* row_lse, float* entropy, int32_t* top_ids, float* top_lp, int C,
-                      cudaStream_t st) {
+                      const int32_t* tokens, int n, int top, float kt, float invT, float move,
+                      float* logprob, float* row_lse, float* entropy, int32_t* top_ids,
+                      float* top_lp, int C, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)M * C));
   cfg.blockDim = dim3(kThreads);
@@ -662,18 +669,19 @@ cudaError_t launch_lp(const void* logits, int64_t ld, int R, int V, const int32_
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, token_logprobs<T, kEnt, kTop>, (const T*)logits, ld, R, V, rows,
-                            tokens, n, top, kt, logprob, row_lse, entropy, top_ids, top_lp);
+                            tokens, n, top, kt, invT, move, logprob, row_lse, entropy, top_ids,
+                            top_lp);
 }
 
 template <typename T>
 cudaError_t launch_lp_t(bool ent, bool with_top, const void* logits, int64_t ld, int R, int V,
                         const int32_t* rows, int M, const int32_t* tokens, int n, int top,
-                        float kt, float* logprob, float* row_lse, float* entropy,
-                        int32_t* top_ids, float* top_lp, int C, cudaStream_t st) {
+                        float kt, float invT, float move, float* logprob, float* row_lse,
+                        float* entropy, int32_t* top_ids, float* top_lp, int C, cudaStream_t st) {
   auto f = ent ? (with_top ? launch_lp<T, true, true> : launch_lp<T, true, false>)
                : (with_top ? launch_lp<T, false, true> : launch_lp<T, false, false>);
-  return f(logits, ld, R, V, rows, M, tokens, n, top, kt, logprob, row_lse, entropy, top_ids,
-           top_lp, C, st);
+  return f(logits, ld, R, V, rows, M, tokens, n, top, kt, invT, move, logprob, row_lse, entropy,
+           top_ids, top_lp, C, st);
 }
 
 // CTAs per row.  Rows that fill the GPU take one each; fewer are split until about as
@@ -711,12 +719,12 @@ extern "C" int spec_token_logprobs(const void* logits, int dtype, int64_t ld, in
   if ((uintptr_t)logits % el != 0 || !f32_ok(rows) || !f32_ok(tokens) || !f32_ok(logprob) ||
       !f32_ok(row_lse) || !f32_ok(entropy) || !f32_ok(top_ids) || !f32_ok(top_logprob))
     return SPEC_ERR_ARG;
-  const float kt = fminf(kLog2e / temperature, FLT_MAX);
+  const float kt = fminf(kLog2e / temperature, FLT_MAX), invT = fminf(1.f / temperature, FLT_MAX);
   const int C = row_ctas(M, V, el);
   auto f = dtype == SPEC_F32 ? launch_lp_t<float> : launch_lp_t<uint16_t>;
   const cudaError_t e = f(entropy != nullptr, top > 0, logits, ld, R, V, rows, M, tokens, n, top,
-                          kt, logprob, row_lse, entropy, top_ids, top_logprob, C,
-                          (cudaStream_t)stream);
+                          kt, invT, kMove / kt, logprob, row_lse, entropy, top_ids, top_logprob,
+                          C, (cudaStream_t)stream);
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
