@@ -727,7 +727,10 @@ int spec_token_logprobs(const void* logits, int dtype, int64_t ld, int R, int V,
  * given tokens: their choice has no gradient), repeated ones adding up and
  * tokens outside [0, V) left out.
  * row_lse [M] and entropy [M]: what spec_token_logprobs returned for these rows
- *     at this temperature (without `rows`).  entropy and g_entropy [M] may both
+ *     at this temperature (without `rows`).  A normaliser of 2^12 or more in size
+ *     (a row of nothing but finite masks, a very low temperature) is too coarse
+ *     for p and only marks its row, whose own is formed again from the logits
+ *     (one CTA a row: three times as long, a lone row ten times).  entropy and g_entropy [M] may both
  *     be NULL; tokens, g_logprob [M, n] or top_ids, g_top [M, top] may be NULL
  *     if n or top is 0.
  * grad [M, V] (out, dtype of the logits, row r at grad + r*ld_grad): computed in

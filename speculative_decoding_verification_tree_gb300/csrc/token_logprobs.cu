@@ -547,8 +547,87 @@ __global__ void __launch_bounds__(kThreads, 4)
 // ------------------------------------------------------------------ gradient
 constexpr int kGradGroups = 4;  // 16-byte groups per thread
 constexpr int kMaxGiven = SPEC_MAX_CHILDREN + SPEC_MAX_TOP_K;
+// From here on half a unit in the last place of a normaliser is 2^-12 or more (a row
+// of nothing but finite masks, a very low temperature): the row's own terms are formed
+// again instead.
+constexpr float kFarLse = 4096.f;
 
-// CTA: one chunk of one row.  kEnt: the entropy's gradient too.
+struct GradSmem {
+  int id[kMaxGiven];     // the given tokens of the row, -1: none
+  float gv[kMaxGiven];   // and their gradients
+  float gsum, red[2][kWarps];
+};
+struct GradRow {         // of a row's dense term
+  float kt, invT, G, gh, H;
+};
+// dense term of a logit with log2 p = d: -(p / T) (G + g_H (ln p + H))
+template <bool kEnt>
+__device__ __forceinline__ float dense_term(const GradRow& t, float d) {
+  if (!kEnt) return ex2(d) * (-t.G * t.invT);
+  d = max_nan(d, kFloor);  // p = 0: 0 times a finite logarithm
+  return -t.invT * ex2(d) * fmaf(t.gh, fmaf(kLn2, d, t.H), t.G);
+}
+// The sum of the gradients of given token tid if it is the first of its kind (true).
+__device__ __forceinline__ bool given_sum(const GradSmem& sm, int m, float& s) {
+  const int tid = threadIdx.x, x = sm.id[tid];
+  bool first = true;
+  s = 0.f;
+  for (int j = 0; j < m && first; ++j)
+    if (sm.id[j] == x) {
+      first = j >= tid;
+      s += sm.gv[j];
+    }
+  return first;
+}
+
+// A whole row by one CTA, from its own largest logit and sum: nothing of it is
+// overwritten before they are formed.  (4096 rows of 128256 bf16 logits, all of them
+// far: 960 us, 301 where none is; one row 46 us instead of 4.)
+template <typename T, bool kEnt>
+__device__ __noinline__ void far_row(const T* row, T* dst, int V, int m, const GradRow t,
+                                     GradSmem& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float top = neg_inf(), s = 0.f;
+#pragma unroll 8
+  for (int i = tid; i < V; i += kThreads) top = fmaxf(top, ElemIO<T>::get(row, i));
+  top = warp_max(top);
+  if (lane == 0) sm.red[0][warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.red[0][w]);
+#pragma unroll 8
+  for (int i = tid; i < V; i += kThreads) s += ex2((ElemIO<T>::get(row, i) - top) * t.kt);
+  s = warp_sum(s);
+  if (lane == 0) sm.red[1][warp] = s;
+  __syncthreads();
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) s += sm.red[1][w];
+  const float ls = log2f(s);
+  auto dense = [&](float z) { return dense_term<kEnt>(t, fmaf(z - top, t.kt, -ls)); };
+  int put = -1;
+  float val = 0.f, g;
+  if (tid < m && sm.id[tid] >= 0 && given_sum(sm, m, g)) {
+    put = sm.id[tid];
+    val = fmaf(g, t.invT, dense(ElemIO<T>::get(row, put)));
+  }
+  __syncthreads();
+  constexpr int kAhead = 8;  // (the stores may be to the logits themselves)
+  for (int i0 = tid; i0 < V; i0 += kAhead * kThreads) {
+    float z[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (i0 + j * kThreads < V) z[j] = ElemIO<T>::get(row, i0 + j * kThreads);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (i0 + j * kThreads < V) Vec<T>::store(dst + i0 + j * kThreads, dense(z[j]));
+  }
+  __syncthreads();
+  if (put >= 0) Vec<T>::store(dst + put, val);
+}
+
+// CTA: one chunk of one row (the first one of a row with a far normaliser takes all of
+// it).  kEnt: the entropy's gradient too.
 template <typename T, bool kEnt>
 __global__ void __launch_bounds__(kThreads)
     token_logprobs_grad(const T* logits, int64_t ld, int V, int chunks,
@@ -559,9 +638,7 @@ __global__ void __launch_bounds__(kThreads)
                         const float* __restrict__ g_ent, T* grad, int64_t ldg) {
   constexpr int kN = Vec<T>::kN;
   constexpr int kChunk = kThreads * kGradGroups;  // groups per CTA
-  __shared__ int id[kMaxGiven];
-  __shared__ float gv[kMaxGiven];
-  __shared__ float gsum;
+  __shared__ GradSmem sm;
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t r = blockIdx.x / chunks;
   const int c = blockIdx.x % chunks;
@@ -593,41 +670,33 @@ __global__ void __launch_bounds__(kThreads)
   for (int j = tid; j < m; j += kThreads) {
     const int x = j < n ? tokens[r * n + j] : top_ids[r * top + j - n];
     const bool ok = x >= 0 && x < V;
-    id[j] = ok ? x : -1;
-    gv[j] = ok ? (j < n ? g_lp[r * n + j] : g_top[r * top + j - n]) : 0.f;
+    sm.id[j] = ok ? x : -1;
+    sm.gv[j] = ok ? (j < n ? g_lp[r * n + j] : g_top[r * top + j - n]) : 0.f;
   }
   __syncthreads();
   if (tid < 32) {
     float s = 0.f;
-    for (int j = lane; j < m; j += 32) s += gv[j];
+    for (int j = lane; j < m; j += 32) s += sm.gv[j];
     s = warp_sum(s);
-    if (lane == 0) gsum = s;
+    if (lane == 0) sm.gsum = s;
   }
   __syncthreads();
-  const float G = gsum;
-  // dense term of one logit: -(p / T) (G + g_H (ln p + H))
-  auto dense = [&](float z) {
-    float d = fmaf(z, kt, -lse);
-    if (!kEnt) return ex2(d) * (-G * invT);
-    d = max_nan(d, kFloor);  // p = 0: 0 times a finite logarithm
-    return -invT * ex2(d) * fmaf(gh, fmaf(kLn2, d, H), G);
-  };
+  const GradRow t{kt, invT, sm.gsum, gh, H};
+  if (fabsf(lse) >= kFarLse) {
+    if (c == 0) far_row<T, kEnt>(row, dst, V, m, t, sm);
+    return;
+  }
+  auto dense = [&](float z) { return dense_term<kEnt>(t, fmaf(z, kt, -lse)); };
   // the given tokens inside this chunk: their logits before anything is written
   // (chunk 0 also owns the row's loose logits)
   const int lo = span.head + g0 * kN, hi = span.head + min(span.groups, g0 + kChunk) * kN;
   float val = 0.f;
   int put = -1;
-  if (tid < m && id[tid] >= 0) {
-    const int x = id[tid];
+  if (tid < m && sm.id[tid] >= 0) {
+    const int x = sm.id[tid];
     const bool here = (x >= lo && x < hi) || (c == 0 && (x < span.head || x >= span.tail));
-    bool first = here;
-    float s = 0.f;
-    for (int j = 0; j < m && first; ++j)
-      if (id[j] == x) {
-        first = j >= tid;
-        s += gv[j];
-      }
-    if (first) {
+    float s;
+    if (here && given_sum(sm, m, s)) {
       put = x;
       val = fmaf(s, invT, dense(ElemIO<T>::get(row, x)));
     }
@@ -756,7 +825,7 @@ extern "C" int spec_token_logprobs_grad(const void* logits, int dtype, int64_t l
   const char *a = (const char*)logits, *b = (const char*)grad;
   const int64_t na = ((int64_t)(M - 1) * ld + V) * el, nb = ((int64_t)(M - 1) * ld_grad + V) * el;
   if (a < b + nb && b < a + na && !(a == b && (ld == ld_grad || M == 1))) return SPEC_ERR_ARG;
-  const float kt = fminf(kLog2e / temperature, FLT_MAX), invT = 1.f / temperature;
+  const float kt = fminf(kLog2e / temperature, FLT_MAX), invT = fminf(1.f / temperature, FLT_MAX);
   const unsigned grid = (unsigned)((int64_t)M * chunks);
   cudaStream_t st = (cudaStream_t)stream;
 #define SV_GRAD(T, E)                                                                           \
