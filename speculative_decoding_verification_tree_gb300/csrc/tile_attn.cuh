@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     if (warp == 0) {
       // ---------------------------------------------------------- producer
       uint32_t n = 0, upar = 0;  // steps; parity of each Q tile's next wait
-      uint32_t nk = 0, nv = 0;   // copies begun
+      uint32_t nk = 0, nv = 0, nq[2] = {0, 0};  // copies begun
       // whether stage s may be filled (once a wait has given up, nothing is copied any
       // more: copies without waits would pile up on a barrier)
       auto slot = [&](int s, uint32_t fill) {
@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 for (int h = 0; h < Geo::kHalves; ++h)
                   w.load_q(t, base + (uint32_t)(t * Geo::kTile + h * Geo::kHalf), 64 * h,
                            &sm.qfull[t]);
+                ++nq[t];
               }
             }
             upar ^= w.have;
@@ -299,12 +300,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           __syncwarp();
         }
       }
-      // this CTA's last copy into each stage has landed before it exits
+      // this CTA's last copy into each stage and each Q tile has landed before it exits
+      // (also where an issuer no longer waits for it)
       if (lane == 0) {
         for (uint32_t s = 0; s < (uint32_t)kKs && s < nk; ++s)
           mbar_wait_bounded(&sm.full[s], ((nk - s - 1) / kKs) & 1u);
         for (uint32_t s = 0; s < (uint32_t)kVs && s < nv; ++s)
           mbar_wait_bounded(&sm.full[kKs + s], ((nv - s - 1) / kVs) & 1u);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (nq[t] > 0) mbar_wait_bounded(&sm.qfull[t], (nq[t] - 1) & 1u);
       }
     } else if (warp <= 2) {
       // ------------------------------------------------- tile t's issuer
