@@ -611,9 +611,11 @@ int spec_philox_uniforms(uint64_t seed, uint32_t offset, const int32_t* b,
  * lse [B, N, Hq] float32 (out, may be NULL): the rows' base-2 log normalisers.
  * out, lse and the workspace must not overlap the inputs or one another.
  * Sequences outside every group are not written.  A row that sees nothing gives
- * zeros and lse = -inf (a key whose score is -inf counts as not seen).  What cache
+ * zeros and lse = -inf, as does one whose scores are all -inf.  What cache
  * positions behind shared_len or prefix_len + N hold does not matter, and NaN or
- * infinite keys and values reach only the rows that see them.
+ * infinite keys and values reach only the rows that see them: an infinite value
+ * whose key weighs 0 in a row (a score of -inf, or too far below the largest) as
+ * 0 times infinity, NaN.
  * Softmax, sums and the join of split work in float32, weights rounded to bf16
  * for the second product, the output to bf16.  Deterministic.
  * Workspace: spec_tree_attention_shared_workspace_bytes(...) bytes, 256-byte
@@ -662,7 +664,8 @@ int spec_tree_attention_shared(const void* q, const void* k_prefix,
  *   lse must not overlap the inputs or one another.
  * Softmax and accumulation in float32, weights rounded to bf16 for the second
  * product, the output to bf16.  A token's NaN or infinite key or value reaches
- * its own and later tokens of its prompt only.  Deterministic.
+ * its own and later tokens of its prompt only (an infinite value whose key weighs
+ * 0 there as 0 times infinity, NaN).  Deterministic.
  * Errors: SPEC_ERR_SHAPE for sizes < 0, Hq % Hkv != 0, G > 128, T >
  * SPEC_MAX_POSITIONS or strides too small; SPEC_ERR_UNSUPPORTED unless D is 64
  * or 128 and the strides are multiples of 8; SPEC_ERR_ARG for scale <= 0 or not

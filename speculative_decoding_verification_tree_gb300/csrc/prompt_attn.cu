@@ -32,10 +32,10 @@ struct PromptWalk {
   struct Params {
     CUtensorMap q, k, v;
     const int32_t* seq_start;
-    const uint16_t* vptr;
+    const uint16_t *qptr, *kptr, *vptr;
     uint16_t* out;
     float* lse;
-    int64_t v_token;  // elements between tokens of v
+    int64_t q_token, k_token, v_token;  // elements between tokens
     int B, T, Hq, Hkv, G, tpt;  // tpt: tokens per tile
     float scale_log2;
   };
@@ -219,6 +219,12 @@ struct PromptWalkD : PromptWalk {
   __device__ __forceinline__ const uint16_t* value(int i) const {
     return p.vptr + (int64_t)(a + key0 + i) * p.v_token + (int64_t)h * D;
   }
+  __device__ __forceinline__ const uint16_t* key(int i) const {
+    return p.kptr + (int64_t)(a + key0 + i) * p.k_token + (int64_t)h * D;
+  }
+  __device__ __forceinline__ const uint16_t* query(const Row& row) const {
+    return p.qptr + (int64_t)(a + row.pos) * p.q_token + (int64_t)(h * p.G + row.head) * D;
+  }
   __device__ __forceinline__ void begin_finish(Row& row, int, float mref, float l) const {
     row.mul = l == 0.f ? 0.f : 1.f / l;
     const int64_t at_ = (int64_t)(a + row.pos) * p.Hq + h * p.G + row.head;
@@ -283,9 +289,13 @@ extern "C" int spec_prompt_attention(const void* q, int64_t q_token, const void*
       !ta_map(&prm.v, v, D, Hkv, T, (int64_t)D * 2, v_token * 2, 1, kKeys))
     return SPEC_ERR_CUDA;
   prm.seq_start = seq_start;
+  prm.qptr = (const uint16_t*)q;
+  prm.kptr = (const uint16_t*)k;
   prm.vptr = (const uint16_t*)v;
   prm.out = (uint16_t*)out;
   prm.lse = lse;
+  prm.q_token = q_token;
+  prm.k_token = k_token;
   prm.v_token = v_token;
   prm.B = B;
   prm.T = T;

@@ -56,7 +56,7 @@ struct SharedWalk {
     CUtensorMap q, ks, vs, ko, vo;
     const int32_t *shared_len, *group_start, *prefix_len;
     const uint64_t* mask_bits;
-    const uint16_t *vs_ptr, *vo_ptr;
+    const uint16_t *q_ptr, *ks_ptr, *ko_ptr, *vs_ptr, *vo_ptr;
     uint16_t* out;
     float* lse;
     SharedPart part;
@@ -387,9 +387,18 @@ struct SharedWalk {
 template <int D>
 struct SharedWalkD : SharedWalk {
   using SharedWalk::SharedWalk;
+  __device__ __forceinline__ int64_t place(int i) const {  // key i of the step
+    return own ? (((int64_t)b * p.Hkv + h) * p.S + key0 + i) * D
+               : (((int64_t)g * p.Hkv + h) * p.Sp + key0 + i) * D;
+  }
   __device__ __forceinline__ const uint16_t* value(int i) const {
-    return own ? p.vo_ptr + (((int64_t)b * p.Hkv + h) * p.S + key0 + i) * D
-               : p.vs_ptr + (((int64_t)g * p.Hkv + h) * p.Sp + key0 + i) * D;
+    return (own ? p.vo_ptr : p.vs_ptr) + place(i);
+  }
+  __device__ __forceinline__ const uint16_t* key(int i) const {
+    return (own ? p.ko_ptr : p.ks_ptr) + place(i);
+  }
+  __device__ __forceinline__ const uint16_t* query(const Row& row) const {
+    return p.q_ptr + ((int64_t)row.token * p.Hq + h * p.G + row.head) * D;
   }
   __device__ __forceinline__ void begin_finish(Row& row, int t, float mref, float l) const {
     if (!whole) {
@@ -488,9 +497,9 @@ __global__ void __launch_bounds__(kShares * 2 * kRows)
     if (c != c0 + share) load(c);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      // (a piece that saw something keeps a positive weight: infinite values stay)
-      const float w = ml[i].x == neg_inf() ? (ml[i].y == 0.f ? 0.f : 1.f)
-                                           : fmaxf(ex2(ml[i].x - ref), FLT_MIN);
+      // (0 for a piece that saw nothing, and for one far below the others: what is
+      // infinite there becomes NaN, as it does inside a piece)
+      const float w = ex2(ml[i].x - ref);
       l = fmaf(ml[i].y, w, l);
       o[0] = fmaf(x[i].x, w, o[0]); o[1] = fmaf(x[i].y, w, o[1]);
       o[2] = fmaf(x[i].z, w, o[2]); o[3] = fmaf(x[i].w, w, o[3]);
@@ -634,6 +643,9 @@ extern "C" int spec_tree_attention_shared(
   prm.group_start = group_start;
   prm.prefix_len = prefix_len;
   prm.mask_bits = mask_bits;
+  prm.q_ptr = (const uint16_t*)q;
+  prm.ks_ptr = (const uint16_t*)ks;
+  prm.ko_ptr = (const uint16_t*)k_cache;
   prm.vs_ptr = (const uint16_t*)vs;
   prm.vo_ptr = (const uint16_t*)v_cache;
   prm.out = (uint16_t*)out;

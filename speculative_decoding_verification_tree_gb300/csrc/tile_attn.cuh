@@ -18,7 +18,8 @@
 //   warp 3      every V tile on its way to the products: rows behind the last key
 //               become zeros, and in steps that some row does not see in full so do
 //               NaN and infinite elements (0 times them would reach rows that do not
-//               see them; rows that do see them get them back at the end);
+//               see them; rows that do see them get them back at the end, times their
+//               weight in as far as that is 0 or not);
 //   warps 4-11  softmax, a thread per row: S from TMEM, online base-2 softmax against
 //               a reference maximum that moves only when a row's maximum grows by
 //               more than 2^8 (O is then rescaled in TMEM), P as bf16 pairs into the
@@ -178,6 +179,26 @@ __device__ __forceinline__ uint32_t times_zero(uint32_t w, uint32_t acc) {
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(acc));
   return d;
 }
+// bit 15 / 31 set where a bf16 half is infinite
+__device__ __forceinline__ uint32_t infinite2(uint32_t w) {
+  const uint32_t x = (w & 0x7fff7fffu) ^ 0x7f807f80u;  // 0: infinite
+  return ~((x + 0x7fff7fffu) | x) & 0x80008000u;
+}
+// Whether a key's weight in a row is 0 (D dims of both, bf16; statistics of the row).
+// (One word at a time: this is rare, and the softmax needs the registers.)
+template <int D>
+__device__ __forceinline__ bool weightless(const uint16_t* q, const uint16_t* k, float scale_log2,
+                                           float mref) {
+  float s = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < D; i += 2) {
+    const uint32_t x = *reinterpret_cast<const uint32_t*>(q + i);
+    const uint32_t y = *reinterpret_cast<const uint32_t*>(k + i);
+    s = fmaf(bf16_lo(x), bf16_lo(y), s);
+    s = fmaf(bf16_hi(x), bf16_hi(y), s);
+  }
+  return ex2(fmaf(s, scale_log2, mref == neg_inf() ? 0.f : -mref)) == 0.f;
+}
 // NaN and infinite halves as 0
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   return w & ~((not_finite2(w) >> 15) * 0xffffu);
@@ -193,7 +214,8 @@ __device__ __forceinline__ uint32_t finite2(uint32_t w) {
 // and, per softmax thread, a Row (set_row at a unit's start):
 //   bool warp_blind(row)          no row of this warp sees anything of the step
 //   void hide(row, half, s)       scores of keys 64 half + i that it does not see: -inf
-//   bool sees(row, i), const uint16_t* value(i)   key i of the step; its V row
+//   bool sees(row, i), const uint16_t *value(i), *key(i)   key i of the step
+//   const uint16_t* query(row)    the row's query
 //   void finish(...)              what becomes of the row
 template <int D, int kKs, int kVs, class W>
 __global__ void __launch_bounds__(kTaThreads, 1)
@@ -595,7 +617,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
         if (bad) {
-          // NaN and infinite values of keys this row sees (their weight is positive)
+          // NaN and infinite values of keys this row sees (0 times infinity is NaN, as in
+          // the steps whose values were left as they are)
           W again(w);
           again.restart();
           while (again.next_step()) {
@@ -603,11 +626,16 @@ __global__ void __launch_bounds__(kTaThreads, 1)
             for (int k = 0; k < again.keys; ++k)
               if (again.sees(row, k)) {
                 const uint32_t* v = reinterpret_cast<const uint32_t*>(again.value(k) + 32 * c);
+                uint32_t inf = 0u;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) inf |= infinite2(v[i]);
+                const float mul =
+                    inf && weightless<D>(again.query(row), again.key(k), sc, mref) ? 0.f : 1.f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                   const uint32_t x = v[i], f = not_finite2(x);
-                  if (f & 0x8000u) o[2 * i] += bf16_lo(x);
-                  if (f >> 31) o[2 * i + 1] += bf16_hi(x);
+                  if (f & 0x8000u) o[2 * i] += bf16_lo(x) * mul;
+                  if (f >> 31) o[2 * i + 1] += bf16_hi(x) * mul;
                 }
               }
           }
