@@ -617,7 +617,8 @@ int spec_philox_uniforms(uint64_t seed, uint32_t offset, const int32_t* b,
  * whose key weighs 0 in a row (a score of -inf, or too far below the largest) as
  * 0 times infinity, NaN.
  * Softmax, sums and the join of split work in float32, weights rounded to bf16
- * for the second product, the output to bf16.  Deterministic.
+ * for the second product, the output to bf16.  Scaled scores lie below 2^28 in
+ * size.  Deterministic.
  * Workspace: spec_tree_attention_shared_workspace_bytes(...) bytes, 256-byte
  * aligned, uninitialised (0: invalid sizes, or B = 0, which needs none).
  * Errors: SPEC_ERR_SHAPE unless 0 <= B <= 65535, 1 <= N <= 64, Hq % Hkv == 0 with
@@ -663,9 +664,10 @@ int spec_tree_attention_shared(const void* q, const void* k_prefix,
  * Tokens outside every prompt are not written.  Empty prompts are fine.  out and
  *   lse must not overlap the inputs or one another.
  * Softmax and accumulation in float32, weights rounded to bf16 for the second
- * product, the output to bf16.  A token's NaN or infinite key or value reaches
- * its own and later tokens of its prompt only (an infinite value whose key weighs
- * 0 there as 0 times infinity, NaN).  Deterministic.
+ * product, the output to bf16.  Scaled scores lie below 2^28 in size.  A token's
+ * NaN or infinite key or value reaches its own and later tokens of its prompt
+ * only (an infinite value whose key weighs 0 there as 0 times infinity, NaN).
+ * Deterministic.
  * Errors: SPEC_ERR_SHAPE for sizes < 0, Hq % Hkv != 0, G > 128, T >
  * SPEC_MAX_POSITIONS or strides too small; SPEC_ERR_UNSUPPORTED unless D is 64
  * or 128 and the strides are multiples of 8; SPEC_ERR_ARG for scale <= 0 or not
@@ -707,9 +709,8 @@ int spec_prompt_attention(const void* q, int64_t q_token, const void* k,
  * scaled, so rows may hold logits of any size (a row of one value throughout is
  * uniform); what passes float32's range, row_lse among them, is infinite.  A row
  * with NaN or +inf, or with nothing but -inf, has NaN log probabilities and
- * entropy (alternatives are
- * still ordered by logit; NaN is never one, and where numbers run out ids are
- * -1 with NaN).
+ * entropy (alternatives are still ordered by logit; NaN is never one, and where
+ * numbers run out ids are -1 with NaN).
  * Errors: SPEC_ERR_DTYPE; SPEC_ERR_SHAPE for sizes < 0, V outside [1,
  * SPEC_MAX_VOCAB], ld < V, n > SPEC_MAX_CHILDREN, top > min(V,
  * SPEC_MAX_TOP_K), M > R without rows, or M >= 2^28; SPEC_ERR_ARG for a
@@ -733,9 +734,9 @@ int spec_token_logprobs(const void* logits, int dtype, int64_t ld, int R, int V,
  *     at this temperature (without `rows`).  A normaliser of 2^12 or more in size
  *     (a row of nothing but finite masks, a very low temperature) is too coarse
  *     for p and only marks its row, whose own is formed again from the logits
- *     (one CTA a row: three times as long, a lone row ten times).  entropy and g_entropy [M] may both
- *     be NULL; tokens, g_logprob [M, n] or top_ids, g_top [M, top] may be NULL
- *     if n or top is 0.
+ *     (one CTA a row: three times as long, a lone row ten times).
+ * entropy and g_entropy [M] may both be NULL; tokens, g_logprob [M, n] or
+ *     top_ids, g_top [M, top] may be NULL if n or top is 0.
  * grad [M, V] (out, dtype of the logits, row r at grad + r*ld_grad): computed in
  *     float32, rounded once.  What lies between the rows is not written.  grad
  *     may be the logits themselves (same pointer and stride); no other overlap.

@@ -29,8 +29,8 @@
 // nothing is checked, one softmax warp of a tile works), and the join.  Trees of 60 nodes
 // of 16 samples behind 8 K keys: 125 us = 1.11 PFLOP/s, the products at 53% of the tensor
 // pipe, the softmax warps' latency and the join (40 MB of partial results, which cutting
-// 128 units into 152 equal pieces leaves; not cutting them would take 69 steps instead of
-// 58).
+// 128 units into 152 equal pieces of 58 steps leaves; not cut, the longest unit would take
+// 73, the mean one 69).
 #include "tile_attn.cuh"
 
 namespace sv {

@@ -39,8 +39,13 @@
 // S of a half is issued after P V of the same half of the step before, which reads P from
 // the same columns, and its commit covers that P V.  A softmax warp that rescales O_t waits
 // for the P V of the half before as well.
-// Sums, statistics and outputs are float32; P is rounded to bf16 for the product and
-// the output to bf16 at the end.
+// Sums, statistics and O are float32.  P is rounded to bf16 for the product, whose
+// operands have one type, V's: each weight is off by at most 2^-8 of itself, the row's
+// sum is of the unrounded ones.  Outputs are rounded to bf16 once, at the end.  (Against
+// 64 bits they differ by 2.2e-3 of their norm, 1.6e-3 of it that last rounding alone.)
+// Scores times the scale in base 2 are taken to lie below 2^29 in size: there an FMA
+// against the rounded reference is off by up to 2^5 at the row's maximum, which the sums
+// bear; float32 tells such scores apart by 32.
 //
 // Every mbarrier wait is bounded; a CTA that gives up stops waiting, still frees its
 // TMEM after waiting, bounded, for its own products and copies, and returns NaN rows
@@ -404,7 +409,8 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           if (pend) put_pv(0);
           if (act) {
             await(sm, &sm.full[n % kKs], (n / kKs) & 1u);
-            // (not before the unit before is settled: its rows wait for that)
+            // (On a unit's first step this holds up the second half of the product before,
+            // and with it the rows of a unit that ended there, until K and Q have landed.)
             if (!started) await(sm, &sm.qfull[t], qpar);
             put_s(0);
           }

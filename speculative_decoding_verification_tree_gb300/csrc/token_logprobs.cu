@@ -26,7 +26,8 @@
 // alternatives: 26.8 us; with the smallest of the warps' third largest 28.9, for more is
 // read again; now 21.9, of which 14.3 without alternatives).  Parts where the bound leaves
 // too few or too many candidates (ties, NaN, masked vocabularies) take an exact radix
-// selection instead.
+// selection instead: 224 such rows of 128256 with 20 alternatives 325 us (13 logits that
+// are not -inf, or 2000 side by side), one such row 59; with 128 logits spread out, 16 us.
 //
 // Few rows are split over the CTAs of a cluster, joined through distributed
 // shared memory (one row of 32000 float32 logits, 5 alternatives: 7.8 us; 128: 21).
