@@ -77,12 +77,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// two floats -> bf16x2 (nearest even), lo in the low half
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // scale log2(e) unit 2^e for a row scaled by 2^-e, |e| <= 126; exact but for the
 // rounding in m (a step leaves the range only if the whole does), and kept normal:
 // a factor of 0 or infinity would make NaN of a masked score (-inf) or of a score

@@ -33,14 +33,11 @@
 // up sets SPEC_STATUS_TIMEOUT and a CTA-wide flag after which no wait blocks,
 // and before TMEM is freed the CTA waits (again bounded) for its own MMAs and
 // copies in flight.
-#include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
-
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tensor_map.h"
 
 namespace sv {
 namespace {
@@ -401,24 +398,10 @@ __global__ void lse_merge(const float2* __restrict__ stats, int M, int nn, float
   if (lane == 0) lse[row] = a.m + log2f(a.z);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 // Row-major [rows, K] bf16 matrix as K-major 64 x box_rows tiles, 128-byte
 // swizzle, zero fill outside.
 bool make_map(CUtensorMap* map, const void* base, int rows, int K, int box_rows) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)K * 2};

@@ -524,8 +524,8 @@ __global__ void __launch_bounds__(kShares * 2 * kRows)
   const int64_t row = (int64_t)(u.tok0 + i) * Hq + u.h * G + r % G;
   const float mul = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint4*>(out + row * D + 8 * blockIdx.y) =
-      make_uint4(pack_bf16(o[0] * mul, o[1] * mul), pack_bf16(o[2] * mul, o[3] * mul),
-                 pack_bf16(o[4] * mul, o[5] * mul), pack_bf16(o[6] * mul, o[7] * mul));
+      make_uint4(pack_bf16x2(o[0] * mul, o[1] * mul), pack_bf16x2(o[2] * mul, o[3] * mul),
+                 pack_bf16x2(o[4] * mul, o[5] * mul), pack_bf16x2(o[6] * mul, o[7] * mul));
   if (lse && blockIdx.y == 0) lse[row] = M + log2f(l);
 }
 

@@ -53,14 +53,11 @@
 #pragma once
 
 #include <cfloat>
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tensor_map.h"
 
 namespace sv {
 namespace {
@@ -116,11 +113,6 @@ __device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* map, int 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // Rows of 64 bytes, a lane each, written so that four lanes write one row at a time:
 // place[i] is the row of lane 4 (lane / 4) + i (its 64 bytes; null: not written).  A
 // store then covers 8 rows instead of 16 bytes of each of 32.
@@ -161,10 +153,10 @@ __device__ __forceinline__ void share_rows(uint4* mine, uint4* (&place)[4]) {
 __device__ __forceinline__ void pack_row(const float (&o)[32], float mul, uint4 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    v[i] = make_uint4(pack_bf16(o[8 * i] * mul, o[8 * i + 1] * mul),
-                      pack_bf16(o[8 * i + 2] * mul, o[8 * i + 3] * mul),
-                      pack_bf16(o[8 * i + 4] * mul, o[8 * i + 5] * mul),
-                      pack_bf16(o[8 * i + 6] * mul, o[8 * i + 7] * mul));
+    v[i] = make_uint4(pack_bf16x2(o[8 * i] * mul, o[8 * i + 1] * mul),
+                      pack_bf16x2(o[8 * i + 2] * mul, o[8 * i + 3] * mul),
+                      pack_bf16x2(o[8 * i + 4] * mul, o[8 * i + 5] * mul),
+                      pack_bf16x2(o[8 * i + 6] * mul, o[8 * i + 7] * mul));
 }
 // True in one lane of a warp that is whole here.
 __device__ __forceinline__ bool elect_one() {
@@ -583,7 +575,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
                 const float2 e = ffma2(make_float2(s[j], s[j + 1]), sc2, nm2);
                 const float p0 = ex2(e.x), p1 = ex2(e.y);
                 ls4[i & 3] = fadd2(ls4[i & 3], make_float2(p0, p1));
-                pk[i] = pack_bf16(p0, p1);
+                pk[i] = pack_bf16x2(p0, p1);
               }
               tst16(tS + (uint32_t)(64 * h + 16 * c), pk);
             }
@@ -660,25 +652,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 ta_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &qr) == cudaSuccess &&
-        qr == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 // bf16 array [n2, n1, D], strides in bytes (multiples of 16), copied in boxes of 64
 // dims x b1 x b2 with the 128-byte swizzle; what lies outside reads as zeros.
 bool ta_map(CUtensorMap* map, const void* base, int D, int64_t n1, int64_t n2, int64_t s1,
             int64_t s2, int b1, int b2) {
-  auto fn = ta_encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)n1, (cuuint64_t)n2};
   cuuint64_t strides[2] = {(cuuint64_t)s1, (cuuint64_t)s2};

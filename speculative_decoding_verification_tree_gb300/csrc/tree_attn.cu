@@ -44,14 +44,11 @@
 // its TMEM after waiting, bounded, for its own MMAs and copies, and returns
 // NaN rows and normalisers (there is no status word).
 #include <cfloat>
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
+#include "tensor_map.h"
 
 namespace sv {
 namespace {
@@ -110,12 +107,6 @@ __device__ __forceinline__ void tma2d_prefetch(const CUtensorMap* map, int x, in
                    reinterpret_cast<uint64_t>(map)),
                "r"(x), "r"(y)
                : "memory");
-}
-// two floats -> bf16x2 (round to nearest even), lo in the low half
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 __global__ void __launch_bounds__(kAThreads, 1)
@@ -403,7 +394,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
           const float2 e = ffma2(make_float2(s[2 * i], s[2 * i + 1]), sc2, nm2);
           const float p0 = ex2(e.x), p1 = ex2(e.y);
           ls4[i & 3] = fadd2(ls4[i & 3], make_float2(p0, p1));
-          pk[i] = pack_bf16(p0, p1);
+          pk[i] = pack_bf16x2(p0, p1);
         }
         const float2 lsa = fadd2(fadd2(ls4[0], ls4[1]), fadd2(ls4[2], ls4[3]));
         const float ls = lsa.x + lsa.y;
@@ -463,10 +454,10 @@ __global__ void __launch_bounds__(kAThreads, 1)
           for (int v = 0; v < 4; ++v) {
             const int i = 8 * v;
             dst[4 * c + v] = make_uint4(
-                pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv),
-                pack_bf16(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv),
-                pack_bf16(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv),
-                pack_bf16(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv));
+                pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv),
+                pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv),
+                pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv),
+                pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv));
           }
         }
       }
@@ -482,23 +473,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult qr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &qr) == cudaSuccess &&
-        qr == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 // A cache [rows, 128] bf16 as 64-dim x 64-key boxes, 128-byte swizzle.
 bool cache_map(CUtensorMap* map, const void* base, int64_t rows) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)kAD, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)kAD * 2};
