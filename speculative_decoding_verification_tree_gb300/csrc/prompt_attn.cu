@@ -17,10 +17,10 @@
 // behind 63: 209 / 192, behind 255 of 100: 254 / 270.
 //
 // Bound: the tensor pipe and the shared memory that feeds it.  16384 tokens, 32 / 8 heads,
-// D 128: 1.45 ms = 1.52 PFLOP/s of visible pairs (88% of cuBLAS's sustained bf16 rate); a
+// D 128: 1.44 ms = 1.52 PFLOP/s of visible pairs (88% of cuBLAS's sustained bf16 rate); a
 // step of 128 keys and two tiles takes about 3070 cycles, of which the products need 2048
 // at the pipe's rate and 2560 at shared memory's (Q and K of S in 64-key halves, V, and the
-// copies into the ring).  Prompts of 37 to 4095 tokens: 623 us, 1.22 PFLOP/s: every unit
+// copies into the ring).  Prompts of 37 to 4095 tokens: 616 us, 1.24 PFLOP/s: every unit
 // adds about 7000 cycles (the first scores, the mask, the last P V and the rows' way out),
 // and half of its first step is masked.  1000 tokens: 20 us, 128 units of one CTA each,
 // the longest a chain of eight steps.  D 64: the softmax warps, 55 us for prompts of up to

@@ -22,12 +22,12 @@
 // most one tile of rows puts them in both tiles, which take its steps in turn: one
 // tile's softmax then runs beside the other's products.
 //
-// Bounds (32 / 8 heads, D 128).  Single tokens of 32 samples behind 32 K keys: 56.7 us, 30
+// Bounds (32 / 8 heads, D 128).  Single tokens of 32 samples behind 32 K keys: 59 us, 30
 // of them the bytes at the copy rate.  CTAs whose piece is all shared keys take 2800 cycles
 // a step, what 64 KB take at that rate; the rest is the start (3 us: lengths, scans, the
 // first loads), own steps, which cost about a sixth more (a V tile of which most rows see
 // nothing is checked, one softmax warp of a tile works), and the join.  Trees of 60 nodes
-// of 16 samples behind 8 K keys: 125 us = 1.11 PFLOP/s, the products at 53% of the tensor
+// of 16 samples behind 8 K keys: 124 us = 1.12 PFLOP/s, the products at 53% of the tensor
 // pipe, the softmax warps' latency and the join (40 MB of partial results, which cutting
 // 128 units into 152 equal pieces of 58 steps leaves; not cut, the longest unit would take
 // 73, the mean one 69).

@@ -24,20 +24,20 @@
 // read again, from L2, and the few candidates ranked by (value, lower index).  The exact
 // top-th of the 256 maxima, by counting, cost more than it saved (224 rows of 128256, 20
 // alternatives: 26.8 us; with the smallest of the warps' third largest 28.9, for more is
-// read again; now 21.9, of which 14.3 without alternatives).  Parts where the bound leaves
+// read again; now 22.2, of which 16.1 without alternatives).  Parts where the bound leaves
 // too few or too many candidates (ties, NaN, masked vocabularies) take an exact radix
 // selection instead: 224 such rows of 128256 with 20 alternatives 325 us (13 logits that
 // are not -inf, or 2000 side by side), one such row 59; with 128 logits spread out, 16 us.
 //
 // Few rows are split over the CTAs of a cluster, joined through distributed
-// shared memory (one row of 32000 float32 logits, 5 alternatives: 7.8 us; 128: 21).
+// shared memory (one row of 32000 float32 logits, 5 alternatives: 7.9 us; 128: 22).
 //
 // Gradient: dz_x = (1/T) (sum_j g_j 1[t_j = x] - p_x (sum_j g_j + g_H (ln p_x + H))).
 // One read and one write of the row; the given tokens' own terms are put in
 // after the dense part, by the CTA that owns their place (their logits are
 // read before, so that the gradient may overwrite the logits).  4096 rows of 128256 bf16
-// logits 332 us, 95% of the copy rate; 777 odd float32 rows of 50257 inside padded ones
-// 50.4 us (their gradient lies at another alignment: logits one by one, gradient in
+// logits 329 us, 95% of the copy rate; 777 odd float32 rows of 50257 inside padded ones
+// 50.0 us (their gradient lies at another alignment: logits one by one, gradient in
 // 16-byte words).
 #include <cfloat>
 #include <cmath>
