@@ -427,7 +427,10 @@ __global__ void __launch_bounds__(kTaThreads, 1)
           __syncwarp();
           qpar ^= 1u;
         }
-        ends = have;
+        // (A tile without a step in the unit has no end to signal.  Its softmax warps give
+        // this warp nothing to wait for there: it could signal the next end as well before
+        // they have seen the first, and a wait for a phase that is two behind never ends.)
+        ends = started;
       }
       if (n > 0) await(sm, &sm.clean[(n - 1) % kVs], ((n - 1) / kVs) & 1u);
       if (pend) {
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(kTaThreads, 1)
     const uint32_t tS = tmem + lanes + 128u * t;
     const uint32_t tO = tmem + lanes + 256u + 128u * t;
     const float sc = prm.scale_log2;
-    uint32_t steps = 0, upar = 0;  // steps of this tile; parity of its next unit's end
+    uint32_t steps = 0, upar = 0;  // steps of this tile; parity of its next end
     typename W::Row row(prm, r);
     while (w.next_unit()) {
       if (!((w.have >> t) & 1u)) continue;
@@ -589,9 +592,11 @@ __global__ void __launch_bounds__(kTaThreads, 1)
         any = true;
         ++steps;
       }
-      await(sm, &sm.ofull[t], upar);
-      upar ^= 1u;
-      fence_after();
+      if (any) {
+        await(sm, &sm.ofull[t], upar);
+        upar ^= 1u;
+        fence_after();
+      }
       // whoever gave up wrote `dead` before the arrival that led here
       bool gave_up = *(volatile uint32_t*)&sm.dead != 0;
 #ifdef SV_TEST_GAVE_UP  // a test's build: CTA 0 as if one of its waits had
